@@ -65,7 +65,8 @@ typedef enum rvq_status {
 
 typedef enum rvq_dtype {
     RVQ_F32 = 0,
-    RVQ_BF16 = 1
+    RVQ_BF16 = 1,
+    RVQ_F8E4M3 = 2   /* 8 bits (4 exponent, 3 mantissa, largest 448): only where named */
 } rvq_dtype;
 
 /* Static text for a status code. */
@@ -285,6 +286,157 @@ rvq_status rvq_embed_tokens(const int32_t *ids, const uint8_t *is_visual, int64_
                             const void *text_table, int64_t V, const void *level_tables,
                             int32_t K, int32_t D, rvq_dtype table_dtype, void *out,
                             rvq_dtype out_dtype, uint32_t *bad_ids, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Learning the token embedding.
+ *
+ * "Visual codebook embeddings are learned jointly with the backbone"
+ * ("LongCat-2.5 发布：面向智能体任务的原生多模态大模型", paragraph "Native Visual
+ * Representation").  The calls below are the parts of one training step
+ * around the embedded rows: the norm that a model's first layer applies to
+ * them and its gradient, the gradient of the embedding tables, and the
+ * optimizer's step.  Pointers need only the alignment of their elements;
+ * 16-byte alignment is fastest.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * RMS norm of rows, with the residual's addition and an 8-bit output:
+ *   h = x + residual (or x),  r = 1 / sqrt(mean(h^2) + eps),  y = h r weight,
+ * in fp32; each output is rounded once (y uses the unrounded h).
+ *
+ * x, residual  : device, [n][d] rows in x_dtype (RVQ_F32 or RVQ_BF16);
+ *                residual may be NULL.
+ * weight       : device, [d] in weight_dtype (RVQ_F32 or RVQ_BF16), or NULL
+ *                for ones.
+ * eps          : > 0.
+ * sum_out      : device, [n][d] in x_dtype: h, the residual stream that goes
+ *                on; or NULL.  May be x or residual itself (in place), not
+ *                another overlap.
+ * y            : device, [n][d] in y_dtype.  RVQ_F8E4M3: row i holds
+ *                e4m3(y / y_scale[i]), nearest even, with
+ *                y_scale[i] = max(max|y| / 448, 2^-100) (NaN where the row
+ *                holds NaN or infinity).  May be x itself if the types agree.
+ * y_scale      : device, [n] fp32, required for RVQ_F8E4M3, else ignored.
+ * rstd         : device, [n] fp32: r of every row, for the gradient; or NULL.
+ * Limits: n <= 2^25, d <= 2^20.
+ */
+rvq_status rvq_rms_norm(const void *x, const void *residual, rvq_dtype x_dtype, int64_t n,
+                        int32_t d, const void *weight, rvq_dtype weight_dtype, float eps,
+                        void *sum_out, void *y, rvq_dtype y_dtype, float *y_scale, float *rstd,
+                        hipStream_t stream);
+
+/* Workspace bytes of rvq_rms_norm_backward with dweight. */
+rvq_status rvq_rms_norm_backward_workspace_size(int64_t n, int32_t d, size_t *bytes);
+
+/*
+ * Gradient of rvq_rms_norm.  With g = dy weight and u = h rstd:
+ *   dx = rstd (g - u mean(g u)) + dsum,   dweight = sum over rows of dy u.
+ * dx is the gradient of x and of residual alike.
+ *
+ * dy, h        : device, [n][d] in dtype; h is the norm's sum_out (x where
+ *                there was no residual).
+ * rstd         : device, [n] fp32, from rvq_rms_norm.
+ * weight       : as for rvq_rms_norm.
+ * dsum         : device, [n][d] in dtype: the gradient that arrives at
+ *                sum_out; or NULL.
+ * dx           : device, [n][d] in dtype.  May be dy or dsum itself.
+ * dweight      : device, [d] fp32, overwritten; NULL when not wanted (the
+ *                workspace is then not used).  Summed in an order that
+ *                depends on n and d only (bitwise reproducible).
+ */
+rvq_status rvq_rms_norm_backward(const void *dy, const void *h, rvq_dtype dtype, int64_t n,
+                                 int32_t d, const float *rstd, const void *weight,
+                                 rvq_dtype weight_dtype, const void *dsum, void *dx,
+                                 float *dweight, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
+/* Workspace bytes of rvq_embed_tokens_backward. */
+rvq_status rvq_embed_tokens_backward_workspace_size(int64_t T, int32_t L, int32_t K, int64_t V,
+                                                    int32_t D, size_t *bytes);
+
+/*
+ * Gradient of rvq_embed_tokens with respect to its tables:
+ *   dlevel[l][k] = sum of dout[t] over visual tokens t with ids[t][l] == k,
+ *   dtext[v]     = sum of dout[t] over text tokens t with ids[t][0] == v,
+ * in fp32, without float atomics: the order of a row's sum depends on the
+ * IDs only (bitwise reproducible).  Every row of the tables is written.
+ *
+ * dout         : device, [T][D] in dout_dtype.
+ * ids, is_visual : as for rvq_embed_tokens.
+ * dlevel       : device, [L][K][D] in grad_dtype, or NULL (frozen tables).
+ * dtext        : device, [V][D] in grad_dtype, or NULL.  Not both NULL.
+ * accumulate   : nonzero adds to what dlevel and dtext hold (rows without a
+ *                token are left as they are); zero overwrites.
+ * bad_ids      : device uint32 counter (added to): out-of-range IDs, each
+ *                once, of the tables whose gradient is asked for; or NULL.
+ *                Such an ID adds to no row.
+ * Limits: L <= 64, T <= 2^25, T (L + 1) < 2^31, L K + V <= 2^28.
+ */
+rvq_status rvq_embed_tokens_backward(const void *dout, rvq_dtype dout_dtype, const int32_t *ids,
+                                     const uint8_t *is_visual, int64_t T, int32_t L, int32_t K,
+                                     int64_t V, int32_t D, void *dlevel, void *dtext,
+                                     rvq_dtype grad_dtype, int32_t accumulate, uint32_t *bad_ids,
+                                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One AdamW step over many tensors:
+ *   g' = f grad,  f = grad_scale min(1, max_norm / (norm + 1e-6))
+ *   m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2
+ *   param = param (1 - lr weight_decay)
+ *           - lr m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, the update using m and v before they are rounded.  norm is the
+ * 2-norm of grad_scale times all gradients of the call; without max_norm the
+ * factor f is grad_scale.
+ *
+ * States.  state_bits 32: m and v are fp32.  state_bits 8: m and sqrt(v) are
+ * held as e4m3 values with an fp32 scale for every 256 consecutive elements
+ * of the tensor: m = m[i] m_scale[i / 256], sqrt(v) = v[i] v_scale[i / 256],
+ * where a scale is max(largest magnitude of the 256 / 448, 2^-100).  All
+ * zeros is a valid start of both.
+ *
+ * Rounding.  8-bit states and bf16 parameters are rounded to nearest even, or
+ * where `stochastic` is nonzero at random (up with the probability of the
+ * remainder), from bits that depend on (seed, step, tensor's place in the
+ * call, element) only.  With beta2 = 0.999, 8-bit states need it: one step
+ * moves sqrt(v) by far less than half a step of its grid.
+ */
+typedef struct rvq_adamw_tensor {
+    void *param;          /* device, [numel] in param_dtype, updated */
+    const void *grad;     /* device, [numel] in grad_dtype */
+    void *m, *v;          /* device, [numel], updated: fp32 or e4m3 */
+    float *m_scale, *v_scale; /* device, [ceil(numel / 256)], updated; 8-bit states only */
+    void *copy;           /* device, [numel] bf16: the new parameters, nearest even; or NULL */
+    int64_t numel;        /* 0 .. 2^34 */
+    float weight_decay;
+    int32_t reserved;     /* 0 */
+} rvq_adamw_tensor;
+
+typedef struct rvq_adamw_options {
+    double lr, beta1, beta2, eps;  /* eps >= 1e-30 */
+    int64_t step;                  /* 1 for the first */
+    double grad_scale;             /* 1 for none */
+    double max_norm;               /* <= 0: no clipping */
+    int32_t stochastic;
+    uint32_t seed;
+} rvq_adamw_options;
+
+/* Workspace bytes of rvq_adamw_step with max_norm or grad_norm. */
+rvq_status rvq_adamw_workspace_size(int32_t count, size_t *bytes);
+
+/*
+ * tensors   : host, [count]; read before the call returns.  Tensors must not
+ *             overlap.
+ * options   : host.
+ * grad_norm : device, fp32: the norm before clipping; or NULL.  Where
+ *             max_norm > 0 or grad_norm is given and the norm is not finite,
+ *             no parameter and no state is written (the step is skipped).
+ * workspace : device, >= rvq_adamw_workspace_size bytes, 256-byte aligned;
+ *             used (and required) with max_norm > 0 or grad_norm only.
+ */
+rvq_status rvq_adamw_step(const rvq_adamw_tensor *tensors, int32_t count, rvq_dtype param_dtype,
+                          rvq_dtype grad_dtype, int32_t state_bits,
+                          const rvq_adamw_options *options, float *grad_norm, void *workspace,
+                          size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Resumable ID cache (host files).

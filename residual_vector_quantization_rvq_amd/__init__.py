@@ -11,13 +11,19 @@ Functions keep the C names:
   rvq_encode(x, codebooks, prepared)          -> ids [n, L] int32 (, residual)
   rvq_decode(ids, codebooks, out_dtype, ...)  -> reconstruction [n, d]
   rvq_level_stats(ids, K, x, codebooks)       -> (hist [L, K] int64, msr [L] fp64)
+
+Learning the token embedding:
+  rvq_rms_norm(x, weight, eps, residual)      -> (y, scale, sum, rstd)
+  rvq_rms_norm_backward(dy, h, rstd, weight)  -> (dx, dweight)
+  rvq_embed_tokens_backward(dout, ids, K)     -> (level_grad [L, K, D], text_grad [V, D])
+  rvq_adamw_init(params) -> state;  rvq_adamw_step(state, grads, step, lr)
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import re
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -29,6 +35,10 @@ __all__ = [
     "rvq_embed_tokens", "rvq_idcache_resume", "rvq_idcache_append", "rvq_idcache_read",
     "rvq_stream_workspace_size", "rvq_stream_encode", "rvq_stream_encode_to_cache",
     "rvq_pack_ranks", "rvq_mfma_rate", "rvq_status_string",
+    "RVQ_F8E4M3", "RMSNormResult", "rvq_rms_norm", "rvq_rms_norm_backward_workspace_size",
+    "rvq_rms_norm_backward", "rvq_embed_tokens_backward_workspace_size",
+    "rvq_embed_tokens_backward", "AdamWState", "rvq_adamw_init", "rvq_adamw_workspace_size",
+    "rvq_adamw_step",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,7 +46,7 @@ _LIB_PATH = os.path.join(_PKG, "librvq.so")
 _HEADER = os.path.join(os.path.dirname(_PKG), "include", "rvq.h")
 
 RVQ_OK, RVQ_ERR_INVALID_ARGUMENT, RVQ_ERR_UNSUPPORTED, RVQ_ERR_WORKSPACE_TOO_SMALL, RVQ_ERR_HIP = range(5)
-RVQ_F32, RVQ_BF16 = 0, 1
+RVQ_F32, RVQ_BF16, RVQ_F8E4M3 = 0, 1, 2
 
 
 class RVQError(RuntimeError):
@@ -93,6 +103,36 @@ _lib.rvq_mfma_rate_workspace_size.argtypes = [_i32]
 _lib.rvq_mfma_rate_workspace_size.restype = ctypes.c_size_t
 _lib.rvq_mfma_rate.argtypes = [_i32, _i32, _i32, _p, _sz, _p, ctypes.POINTER(ctypes.c_double),
                                ctypes.POINTER(ctypes.c_double)]
+_f32 = ctypes.c_float
+_lib.rvq_rms_norm.argtypes = [_p, _p, ctypes.c_int, _i64, _i32, _p, ctypes.c_int, _f32, _p, _p,
+                              ctypes.c_int, _p, _p, _p]
+_lib.rvq_rms_norm_backward_workspace_size.argtypes = [_i64, _i32, _psz]
+_lib.rvq_rms_norm_backward.argtypes = [_p, _p, ctypes.c_int, _i64, _i32, _p, _p, ctypes.c_int, _p,
+                                       _p, _p, _p, _sz, _p]
+_lib.rvq_embed_tokens_backward_workspace_size.argtypes = [_i64, _i32, _i32, _i64, _i32, _psz]
+_lib.rvq_embed_tokens_backward.argtypes = [_p, ctypes.c_int, _p, _p, _i64, _i32, _i32, _i64, _i32,
+                                           _p, _p, ctypes.c_int, _i32, _p, _p, _sz, _p]
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", _p), ("grad", _p), ("m", _p), ("v", _p), ("m_scale", _p),
+                ("v_scale", _p), ("copy", _p), ("numel", _i64), ("weight_decay", _f32),
+                ("reserved", _i32)]
+
+
+class _AdamWOptions(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", _i64), ("grad_scale", ctypes.c_double),
+                ("max_norm", ctypes.c_double), ("stochastic", _i32), ("seed", ctypes.c_uint32)]
+
+
+_lib.rvq_adamw_workspace_size.argtypes = [_i32, _psz]
+_lib.rvq_adamw_step.argtypes = [_p, _i32, ctypes.c_int, ctypes.c_int, _i32,
+                                ctypes.POINTER(_AdamWOptions), _p, _p, _sz, _p]
+for _f in ("rvq_rms_norm", "rvq_rms_norm_backward_workspace_size", "rvq_rms_norm_backward",
+           "rvq_embed_tokens_backward_workspace_size", "rvq_embed_tokens_backward",
+           "rvq_adamw_workspace_size", "rvq_adamw_step"):
+    getattr(_lib, _f).restype = ctypes.c_int
 for _f in ("rvq_mfma_rate", "rvq_prepared_size", "rvq_prepare_codebooks", "rvq_encode_workspace_size",
            "rvq_encode", "rvq_encode_noalloc", "rvq_encode_profiled", "rvq_decode",
            "rvq_level_stats_workspace_size", "rvq_level_stats", "rvq_decode_level_stats", "rvq_embed_tokens", "rvq_idcache_resume",
@@ -313,6 +353,309 @@ def rvq_embed_tokens(ids: torch.Tensor, level_tables: torch.Tensor,
                                  _ptr(level_tables), K, D, tdt, _ptr(out), _dtype_code(out.dtype),
                                  _ptr(bad_ids), _stream(ids.device)))
     return out
+
+
+def _on_device(dev: torch.device, call, *args) -> None:
+    """The library call with dev current (a launch goes to the current device)."""
+    if dev.index == torch.cuda.current_device():
+        _check(call(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(*args))
+
+
+def _address(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _need_workspace(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device) -> torch.Tensor:
+    """The caller's workspace if it is large enough, else a new one."""
+    if workspace is not None:
+        _need_cuda("workspace", workspace, dev)
+        if workspace.dtype != torch.uint8 or workspace.dim() != 1:
+            raise ValueError("workspace must be a uint8 [bytes] tensor")
+        if workspace.numel() >= nbytes:
+            return workspace
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def _need_weight(weight: Optional[torch.Tensor], d: int, dev: torch.device) -> int:
+    if weight is None:
+        return RVQ_F32
+    code = _dtype_code(weight.dtype)
+    _need_shape("weight", weight, (d,), weight.dtype, dev)
+    return code
+
+
+class RMSNormResult(NamedTuple):
+    y: torch.Tensor                  # [n, d]
+    scale: Optional[torch.Tensor]    # [n] fp32: 8-bit outputs only
+    sum: Optional[torch.Tensor]      # [n, d]: x + residual
+    rstd: Optional[torch.Tensor]     # [n] fp32
+
+
+def rvq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                 need_rstd: bool = False, out: Optional[torch.Tensor] = None,
+                 sum_out: Optional[torch.Tensor] = None) -> RMSNormResult:
+    """RMS norm of rows x [n, d] (fp32 or bf16) after adding the residual:
+    h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight.  out_dtype is
+    float32, bfloat16 (default: x's) or float8_e4m3fn, which comes with one
+    scale per row (y = out * scale).  ``sum`` is h in x's type where there is
+    a residual (sum_out may be x or residual: in place); ``rstd`` is what
+    rvq_rms_norm_backward needs."""
+    _need_cuda("x", x)
+    dev = x.device
+    if x.dim() != 2:
+        raise ValueError("x must be [n, d]")
+    n, d = x.shape
+    code = _dtype_code(x.dtype)
+    if residual is not None:
+        _need_shape("residual", residual, (n, d), x.dtype, dev)
+        if sum_out is None:
+            sum_out = torch.empty_like(x)
+    if sum_out is not None:
+        _need_shape("sum_out", sum_out, (n, d), x.dtype, dev)
+    wcode = _need_weight(weight, d, dev)
+    odt = x.dtype if out_dtype is None else out_dtype
+    f8 = odt == torch.float8_e4m3fn
+    ocode = RVQ_F8E4M3 if f8 else _dtype_code(odt)
+    if out is None:
+        out = torch.empty((n, d), dtype=odt, device=dev)
+    else:
+        _need_shape("out", out, (n, d), odt, dev)
+    scale = torch.empty(n, dtype=torch.float32, device=dev) if f8 else None
+    rstd = torch.empty(n, dtype=torch.float32, device=dev) if need_rstd else None
+    _on_device(dev, _lib.rvq_rms_norm, x.data_ptr(), _address(residual), code, n, d,
+               _address(weight), wcode, eps, _address(sum_out), out.data_ptr(), ocode,
+               _address(scale), _address(rstd), _stream(dev))
+    return RMSNormResult(out, scale, sum_out, rstd)
+
+
+def rvq_rms_norm_backward_workspace_size(n: int, d: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.rvq_rms_norm_backward_workspace_size(n, d, ctypes.byref(out)))
+    return out.value
+
+
+def rvq_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
+                          weight: Optional[torch.Tensor] = None,
+                          dsum: Optional[torch.Tensor] = None, need_dweight: bool = True,
+                          out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None
+                          ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gradient of rvq_rms_norm: (dx [n, d] in dy's type, dweight [d] fp32).
+    h is the forward call's ``sum`` (x without a residual), dsum the gradient
+    that arrives at it; dx is the gradient of x and of the residual.  out may
+    be dy or dsum (in place)."""
+    _need_cuda("dy", dy)
+    dev = dy.device
+    if dy.dim() != 2:
+        raise ValueError("dy must be [n, d]")
+    n, d = dy.shape
+    code = _dtype_code(dy.dtype)
+    _need_shape("h", h, (n, d), dy.dtype, dev)
+    _need_shape("rstd", rstd, (n,), torch.float32, dev)
+    if dsum is not None:
+        _need_shape("dsum", dsum, (n, d), dy.dtype, dev)
+    wcode = _need_weight(weight, d, dev)
+    if out is None:
+        out = torch.empty_like(dy)
+    else:
+        _need_shape("out", out, (n, d), dy.dtype, dev)
+    dweight, ws, nbytes = None, None, 0
+    if need_dweight:
+        dweight = torch.empty(d, dtype=torch.float32, device=dev)
+        ws = _need_workspace(workspace, rvq_rms_norm_backward_workspace_size(n, d), dev)
+        nbytes = ws.numel()
+    _on_device(dev, _lib.rvq_rms_norm_backward, dy.data_ptr(), h.data_ptr(), code, n, d,
+               rstd.data_ptr(), _address(weight), wcode, _address(dsum), out.data_ptr(),
+               _address(dweight), _address(ws), nbytes, _stream(dev))
+    return out, dweight
+
+
+def rvq_embed_tokens_backward_workspace_size(T: int, L: int, K: int, V: int, D: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.rvq_embed_tokens_backward_workspace_size(T, L, K, V, D, ctypes.byref(out)))
+    return out.value
+
+
+def rvq_embed_tokens_backward(dout: torch.Tensor, ids: torch.Tensor, K: int,
+                              is_visual: Optional[torch.Tensor] = None, V: int = 0,
+                              grad_dtype: torch.dtype = torch.float32,
+                              level_grad: Optional[torch.Tensor] = None,
+                              text_grad: Optional[torch.Tensor] = None, accumulate: bool = False,
+                              need_level: bool = True, need_text: bool = True,
+                              bad_ids: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None
+                              ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradient of rvq_embed_tokens with respect to its tables, for dout [T, D]
+    and ids [T, L]: (level_grad [L, K, D], text_grad [V, D] or None).
+    need_level / need_text false: that table is frozen.  accumulate adds to
+    the level_grad and text_grad given.  The same inputs give the same bits."""
+    _need_cuda("dout", dout)
+    dev = dout.device
+    _need_cuda("ids", ids, dev)
+    if dout.dim() != 2 or ids.dim() != 2 or ids.dtype != torch.int32 or ids.shape[0] != dout.shape[0]:
+        raise ValueError("dout must be [T, D] and ids int32 [T, L]")
+    T, D = dout.shape
+    L = ids.shape[1]
+    need_text = need_text and V > 0
+    if not need_level and not need_text:
+        raise ValueError("no table's gradient is asked for")
+    code, gcode = _dtype_code(dout.dtype), _dtype_code(grad_dtype)
+    if is_visual is not None:
+        _need_cuda("is_visual", is_visual, dev)
+        if is_visual.dtype == torch.bool:
+            is_visual = is_visual.view(torch.uint8)
+        if is_visual.dtype != torch.uint8 or is_visual.shape != (T,):
+            raise ValueError("is_visual must be uint8 or bool [T]")
+    if bad_ids is not None:
+        _need_shape("bad_ids", bad_ids, (1,), torch.int32, dev)
+    nbytes = rvq_embed_tokens_backward_workspace_size(T, L, K, V, D)
+    for name, wanted, given, shape in (("level_grad", need_level, level_grad, (L, K, D)),
+                                       ("text_grad", need_text, text_grad, (V, D))):
+        if given is not None:
+            _need_shape(name, given, shape, grad_dtype, dev)
+        elif wanted and accumulate:
+            raise ValueError(f"accumulate needs {name}")
+    if need_level and level_grad is None:
+        level_grad = torch.empty((L, K, D), dtype=grad_dtype, device=dev)
+    if need_text and text_grad is None:
+        text_grad = torch.empty((V, D), dtype=grad_dtype, device=dev)
+    ws = _need_workspace(workspace, nbytes, dev)
+    level_out, text_out = level_grad if need_level else None, text_grad if need_text else None
+    _on_device(dev, _lib.rvq_embed_tokens_backward, dout.data_ptr(), code, ids.data_ptr(),
+               _address(is_visual), T, L, K, V, D, _address(level_out), _address(text_out), gcode,
+               1 if accumulate else 0, _address(bad_ids), ws.data_ptr(), ws.numel(), _stream(dev))
+    return level_out, text_out
+
+
+class AdamWState:
+    """Parameters of one type and their AdamW state (see rvq_adamw_init):
+    lists params, m, v and, with 8-bit states, m_scale, v_scale; copies or
+    None.  Holds references to the tensors, not copies of them."""
+
+    def __init__(self, params, state_bits, weight_decay, copies, m, v, m_scale, v_scale):
+        self.params, self.state_bits, self.copies = params, state_bits, copies
+        self.m, self.v, self.m_scale, self.v_scale = m, v, m_scale, v_scale
+        self.device = params[0].device
+        self.param_dtype = params[0].dtype
+        self._numels = [p.numel() for p in params]
+        self._table = (_AdamWTensor * len(params))()
+        none = [None] * len(params)
+        for t, p, a, b, sa, sb, c, w in zip(self._table, params, m, v, m_scale or none,
+                                            v_scale or none, copies or none, weight_decay):
+            t.param, t.m, t.v = p.data_ptr(), a.data_ptr(), b.data_ptr()
+            t.m_scale, t.v_scale, t.copy = _address(sa), _address(sb), _address(c)
+            t.numel, t.weight_decay = p.numel(), w
+        self._workspace = torch.empty(rvq_adamw_workspace_size(len(params)), dtype=torch.uint8,
+                                      device=self.device)
+
+
+def rvq_adamw_init(params: Sequence[torch.Tensor], state_bits: int = 32, weight_decay=0.01,
+                   copies: Optional[Sequence[torch.Tensor]] = None,
+                   m: Optional[Sequence[torch.Tensor]] = None,
+                   v: Optional[Sequence[torch.Tensor]] = None,
+                   m_scale: Optional[Sequence[torch.Tensor]] = None,
+                   v_scale: Optional[Sequence[torch.Tensor]] = None) -> AdamWState:
+    """AdamW state of params (contiguous device tensors, all fp32 or all bf16).
+    state_bits 32: fp32 moments; 8: float8_e4m3fn values of m and sqrt(v) with
+    one fp32 scale for every 256 elements.  weight_decay: a number, or one
+    per parameter.  copies: bf16 tensors that receive the updated parameters
+    (fp32 masters).  m, v (and scales): states to go on with, e.g. from a
+    checkpoint; zeros otherwise.  An 8-bit state holds m = m * m_scale and
+    sqrt(v) = v * v_scale, block by block."""
+    params = list(params)
+    if not params:
+        raise ValueError("no parameters")
+    if state_bits not in (8, 32):
+        raise ValueError("state_bits must be 8 or 32")
+    dev, dt = params[0].device, params[0].dtype
+    _dtype_code(dt)
+    for i, p in enumerate(params):
+        _need_cuda(f"params[{i}]", p, dev)
+        if p.dtype != dt:
+            raise ValueError(f"params[{i}] is {p.dtype}, expected {dt}")
+    sdt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+
+    def states(name, given, dtype, shape):
+        if given is None:
+            return [torch.zeros(shape(p), dtype=dtype, device=dev) for p in params]
+        given = list(given)
+        if len(given) != len(params):
+            raise ValueError(f"{name} must have one tensor per parameter")
+        for i, (t, p) in enumerate(zip(given, params)):
+            _need_shape(f"{name}[{i}]", t, shape(p), dtype, dev)
+        return given
+
+    def same(p):
+        return tuple(p.shape)
+
+    def blocks(p):
+        return (-(-p.numel() // 256),)
+    if (m is None) != (v is None):
+        raise ValueError("m and v are given together")
+    if state_bits == 8 and m is not None and (m_scale is None or v_scale is None):
+        raise ValueError("8-bit m and v come with m_scale and v_scale")
+    m, v = states("m", m, sdt, same), states("v", v, sdt, same)
+    if state_bits == 8:
+        m_scale = states("m_scale", m_scale, torch.float32, blocks)
+        v_scale = states("v_scale", v_scale, torch.float32, blocks)
+    elif m_scale is not None or v_scale is not None:
+        raise ValueError("32-bit states have no scales")
+    if copies is not None:
+        copies = states("copies", copies, torch.bfloat16, same)
+    try:
+        decay = [float(w) for w in weight_decay]
+    except TypeError:
+        decay = [float(weight_decay)] * len(params)
+    if len(decay) != len(params):
+        raise ValueError("weight_decay must be a number or have one number per parameter")
+    return AdamWState(params, state_bits, decay, copies, m, v, m_scale, v_scale)
+
+
+def rvq_adamw_workspace_size(count: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.rvq_adamw_workspace_size(count, ctypes.byref(out)))
+    return out.value
+
+
+def rvq_adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: int, lr: float,
+                   betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+                   max_norm: Optional[float] = None, grad_scale: float = 1.0,
+                   seed: Optional[int] = None, need_norm: bool = False) -> Optional[torch.Tensor]:
+    """One AdamW step (step 1 is the first) of the state's parameters with
+    grads, one fp32 or one bf16 tensor per parameter.  max_norm clips by the
+    global norm of grad_scale * grads, which is returned (fp32 [1] on the
+    device; need_norm returns it without clipping); a norm that is not finite
+    leaves parameters and states as they are.  seed: round 8-bit states and
+    bf16 parameters at random (needed for 8-bit states in training), from
+    bits of (seed, step, tensor, element); None rounds to nearest."""
+    dev, table = state.device, state._table
+    if len(grads) != len(table):
+        raise ValueError(f"{len(table)} gradients are wanted, one per parameter (got {len(grads)})")
+    gdt = grads[0].dtype
+    gcode = _dtype_code(gdt)
+    index = dev.index
+    for t, g, n in zip(table, grads, state._numels):
+        if g.dtype is not gdt or g.numel() != n or not g.is_contiguous() or g.get_device() != index:
+            raise ValueError(f"gradients must be contiguous {gdt} tensors on {dev} with their "
+                             f"parameters' sizes (got {g.dtype} {list(g.shape)} on {g.device})")
+        t.grad = g.data_ptr()
+    norm, ws, nbytes = None, None, 0
+    if max_norm is not None and not max_norm > 0:
+        raise ValueError("max_norm must be positive")
+    if need_norm or max_norm is not None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        ws, nbytes = state._workspace.data_ptr(), state._workspace.numel()
+    opt = _AdamWOptions(lr, betas[0], betas[1], eps, step, grad_scale,
+                        0.0 if max_norm is None else max_norm, 0 if seed is None else 1,
+                        0 if seed is None else seed & 0xFFFFFFFF)
+    _on_device(dev, _lib.rvq_adamw_step, ctypes.addressof(table), len(table),
+               _dtype_code(state.param_dtype), gcode, state.state_bits, ctypes.byref(opt),
+               _address(norm), ws, nbytes, _stream(dev))
+    return norm
 
 
 def rvq_idcache_resume(path: str, n: int, L: int, K: int, chunk_rows: int) -> int:

@@ -1,0 +1,235 @@
+"""rvq_rms_norm and its gradient against their definitions in 64 bits."""
+import pytest
+import torch
+
+import learn_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def rvq():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import residual_vector_quantization_rvq_amd as m
+    return m
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return torch.device("cuda:0")
+
+
+def _chain(d):
+    # a row's terms that one lane adds one after the other (at most d / 64,
+    # or 64 where fewer lanes share a narrow row), the tree over 256 lanes,
+    # and the roundings of the mean, the root and the products
+    return max(d / 64, 64) + 24
+
+
+def _rows(n, d, dtype, seed, dev, spread=True):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    x = torch.randn((n, d), generator=g, device=dev)
+    if spread:
+        x[:, ::max(1, d // 3)] *= 30.0
+    return x.to(dtype)
+
+
+def _check_norm(rvq, x, res, w, odt, eps=1e-5, **kw):
+    n, d = x.shape
+    x0, r0 = x.clone(), None if res is None else res.clone()
+    out = rvq.rvq_rms_norm(x, w, eps, residual=res, out_dtype=odt, need_rstd=True, **kw)
+    torch.cuda.synchronize()
+    h, rstd, y = ref.rms_norm(x0, r0, w, eps)
+    b = _chain(d) * ref.U
+    ref.close(out.rstd, rstd, b * rstd, "rstd")
+    if res is not None:
+        ref.close(out.sum, h, h.abs() * (ref.U if x.dtype == F32 else ref.BF16_HALF * (1 + 2 ** -8)), "sum")
+    assert out.y.dtype == odt and out.y.shape == (n, d)
+    if odt == F8:
+        top = y.abs().amax(1) / ref.F8_MAX
+        ref.close(out.scale, top.clamp(min=ref.SCALE_MIN), b * top, "scale")
+        v = y / out.scale.double()[:, None]
+        near = torch.clamp(v, -ref.F8_MAX, ref.F8_MAX)
+        ref.close(out.y.float(), near, ref.f8_step(v) * 0.5 * (1 + 2 ** -8) + b * v.abs(), "y (e4m3)")
+    else:
+        assert out.scale is None
+        ref.close(out.y, y, y.abs() * (b if odt == F32 else ref.BF16_HALF * (1 + 2 ** -8) + b), "y")
+    return out
+
+
+# every width class (a few lanes, a wave, a workgroup per row; rows that stay
+# in registers or are read again), whole and broken 16-byte pieces
+WIDTHS = [1, 2, 7, 8, 24, 63, 64, 65, 128, 200, 256, 257, 500, 512, 1000, 1024, 1152, 1155, 2048,
+          2050, 4096, 4100, 5001, 8192, 8193, 12288, 20001]
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_norm(rvq, dev, d, dtype):
+    for n, odt, with_res, wdt in ((1, dtype, True, F32), (37, F8, True, BF16), (300, dtype, False, None),
+                                  (5, BF16 if dtype == F32 else F32, True, F32), (64, F8, False, F32)):
+        x = _rows(n, d, dtype, d + n, dev)
+        res = _rows(n, d, dtype, d + n + 1, dev) if with_res else None
+        w = None if wdt is None else (1 + 0.2 * _rows(1, d, F32, 5, dev, False)[0]).to(wdt)
+        _check_norm(rvq, x, res, w, odt)
+
+
+def test_norm_many_rows(rvq, dev):
+    for n, d in ((100003, 8), (70001, 64), (20011, 512)):
+        _check_norm(rvq, _rows(n, d, BF16, n, dev), _rows(n, d, BF16, n + 1, dev), None, BF16)
+
+
+def test_norm_in_place_and_unaligned(rvq, dev):
+    for dtype in (F32, BF16):
+        for d in (100, 1155, 4096):
+            w = 1 + 0.1 * _rows(1, d, F32, 3, dev, False)[0]
+            for which in ("x", "residual"):
+                x, res = _rows(9, d, dtype, d, dev), _rows(9, d, dtype, d + 1, dev)
+                _check_norm(rvq, x, res, w, dtype, sum_out=x if which == "x" else res)
+            # rows that begin one element into a buffer
+            buf = _rows(1, 20 * d + 2, dtype, d + 2, dev)[0]
+            x, res = buf[1:1 + 9 * d].view(9, d), buf[10 * d + 1:19 * d + 1].view(9, d)
+            o = torch.empty(9 * d + 1, dtype=dtype, device=dev)[1:].view(9, d)
+            _check_norm(rvq, x.clone(), None, w, dtype, out=o)
+            _check_norm(rvq, x, res, w[:d], dtype, out=o)
+            q = torch.empty(9 * d + 1, dtype=F8, device=dev)[1:].view(9, d)
+            _check_norm(rvq, x, res, w, F8, out=q)
+
+
+def test_norm_zero_rows_and_empty(rvq, dev):
+    for d in (48, 2048, 9000):
+        x = _rows(6, d, BF16, d, dev)
+        x[2] = 0
+        x[4] = 1e-30
+        for odt in (BF16, F8, F32):
+            out = _check_norm(rvq, x, None, None, odt)
+            assert torch.all(out.y[2].float() == 0)
+        assert out.rstd[2].item() == pytest.approx(1e-5 ** -0.5, rel=1e-6)
+        e = rvq.rvq_rms_norm(x[:0], None, need_rstd=True, out_dtype=F8)
+        assert e.y.shape == (0, d) and e.rstd.shape == (0,) and e.scale.shape == (0,)
+
+
+def test_norm_rows_with_nan_or_infinity_stay_alone(rvq, dev):
+    for d in (40, 3000, 9000):
+        x = _rows(8, d, F32, d, dev)
+        clean = rvq.rvq_rms_norm(x, out_dtype=F8)
+        x[1, d // 2] = float("nan")
+        x[5, 0] = float("inf")
+        out = rvq.rvq_rms_norm(x, out_dtype=F8)
+        plain = rvq.rvq_rms_norm(x)
+        keep = torch.tensor([0, 2, 3, 4, 6, 7], device=dev)
+        assert torch.equal(out.y[keep].view(torch.uint8), clean.y[keep].view(torch.uint8))
+        assert torch.equal(out.scale[keep], clean.scale[keep])
+        assert torch.isnan(out.scale[1]) and torch.isnan(out.scale[5])
+        assert torch.isnan(plain.y[1]).all() and torch.isnan(plain.y[5, 0])
+
+
+def _check_grad(rvq, n, d, dtype, wdt, with_sum, dev, in_place=None):
+    h, dy = _rows(n, d, dtype, n + d, dev), _rows(n, d, dtype, n + d + 1, dev, False)
+    ds = _rows(n, d, dtype, n + d + 2, dev, False) if with_sum else None
+    w = None if wdt is None else (1 + 0.2 * _rows(1, d, F32, 5, dev, False)[0]).to(wdt)
+    rstd = (h.double().square().mean(1) + 1e-5).rsqrt().float()
+    dx, size, dw, dwsize = ref.rms_norm_grad(dy, h, rstd, w, ds)
+    out = {None: None, "dy": dy, "dsum": ds}[in_place]
+    got, gotw = rvq.rvq_rms_norm_backward(dy, h, rstd, w, dsum=ds, out=out)
+    torch.cuda.synchronize()
+    b = _chain(d) * ref.U
+    extra = 0.0 if dtype == F32 else ref.BF16_HALF * (1 + 2 ** -8) * dx.abs()
+    ref.close(got, dx, b * size + extra, "dx")
+    # at most n / 256 + 512 additions in a row, and three roundings of each term
+    ref.close(gotw, dw, (min(n, n / 256 + 512) + 16) * ref.U * dwsize, "dweight")
+    return got, gotw
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_norm_grad(rvq, dev, d, dtype):
+    for n, wdt, with_sum in ((1, F32, False), (41, BF16, True), (300, None, True), (1030, F32, False)):
+        _check_grad(rvq, n, d, dtype, wdt, with_sum, dev)
+
+
+def test_norm_grad_many_rows_and_in_place(rvq, dev):
+    for n, d in ((100003, 8), (30011, 200), (20011, 1024)):
+        _check_grad(rvq, n, d, BF16, F32, True, dev)
+    for d in (100, 4096, 9000):
+        for which in ("dy", "dsum"):
+            _check_grad(rvq, 700, d, BF16, F32, True, dev, which)
+
+
+def test_norm_grad_repeats_and_options(rvq, dev):
+    h, dy = _rows(5000, 1152, BF16, 1, dev), _rows(5000, 1152, BF16, 2, dev)
+    rstd = (h.double().square().mean(1) + 1e-5).rsqrt().float()
+    a, aw = rvq.rvq_rms_norm_backward(dy, h, rstd)
+    b, bw = rvq.rvq_rms_norm_backward(dy, h, rstd)
+    c, none = rvq.rvq_rms_norm_backward(dy, h, rstd, need_dweight=False)
+    assert none is None
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(a, c)
+    assert torch.equal(aw.view(torch.int32), bw.view(torch.int32))
+    dx, dw = rvq.rvq_rms_norm_backward(dy[:0], h[:0], rstd[:0])
+    assert dx.shape == (0, 1152) and torch.all(dw == 0)
+
+
+def test_norm_grad_against_differences(rvq, dev):
+    # the loss sum(dy y + dsum h) of the forward definition in 64 bits, moved
+    # by 1e-5 either way: the difference is off by about 1e-10 (third order)
+    # and 1e-11 (cancellation), the kernel by its fp32 bound
+    n, d, eps, s = 3, 37, 1e-5, 1e-5
+    h, dy, ds = (_rows(n, d, F32, k, dev, False) for k in (1, 2, 3))
+    w = 1 + 0.2 * _rows(1, d, F32, 4, dev, False)[0]
+    rstd = rvq.rvq_rms_norm(h, w, eps, need_rstd=True).rstd
+    dx, dw = rvq.rvq_rms_norm_backward(dy, h, rstd, w, dsum=ds)
+
+    def loss(h, w):
+        return float((dy.double() * ref.rms_norm(h, None, w, eps)[2]).sum() + (ds.double() * h).sum())
+    for i in range(n):
+        for j in range(0, d, 5):
+            e = torch.zeros((n, d), dtype=torch.float64, device=dev)
+            e[i, j] = s
+            num = (loss(h.double() + e, w.double()) - loss(h.double() - e, w.double())) / (2 * s)
+            assert abs(num - dx[i, j].item()) <= 1e-4, (i, j)
+    for j in range(0, d, 4):
+        e = torch.zeros(d, dtype=torch.float64, device=dev)
+        e[j] = s
+        num = (loss(h.double(), w.double() + e) - loss(h.double(), w.double() - e)) / (2 * s)
+        assert abs(num - dw[j].item()) <= 1e-4, j
+
+
+def test_norm_offsets_past_32_bits(rvq, dev):
+    # 2^32 + elements: the last rows lie beyond a 32-bit element offset
+    n, d = 66000, 65536
+    x = torch.zeros((n, d), dtype=BF16, device=dev)
+    x[-3:] = _rows(3, d, BF16, 7, dev)
+    x[0] = _rows(1, d, BF16, 8, dev)[0]
+    pick = torch.tensor([0, n - 3, n - 2, n - 1], device=dev)
+    dy = torch.zeros_like(x)
+    dy[pick] = _rows(4, d, BF16, 9, dev, False)
+    out = rvq.rvq_rms_norm(x, need_rstd=True)
+    b = _chain(d) * ref.U
+    y = ref.rms_norm(x[pick], None, None, 1e-6)[2]
+    ref.close(out.y[pick], y, y.abs() * (ref.BF16_HALF * (1 + 2 ** -8) + b), "y")
+    dx, _ = rvq.rvq_rms_norm_backward(dy, x, out.rstd, need_dweight=False, out=out.y)
+    want, size, _, _ = ref.rms_norm_grad(dy[pick], x[pick], out.rstd[pick], None, None)
+    ref.close(dx[pick], want, b * size + ref.BF16_HALF * (1 + 2 ** -8) * want.abs(), "dx")
+    assert float(dx[1:n - 3:997].float().abs().sum()) == 0.0
+
+
+def test_norm_refusals(rvq, dev):
+    x = _rows(4, 32, F32, 1, dev)
+    rstd = torch.ones(4, device=dev)
+    for bad in (dict(residual=x[:3]), dict(residual=x.bfloat16()), dict(weight=torch.ones(31, device=dev)),
+                dict(weight=torch.ones(32, device=dev, dtype=torch.float64)), dict(out=x.bfloat16()),
+                dict(sum_out=x[:, :16]), dict(weight=torch.ones(32)), dict(residual=x.t().contiguous().t())):
+        with pytest.raises((ValueError, TypeError)):
+            rvq.rvq_rms_norm(x, **bad)
+    for bad in (x.cpu(), x[0], x.double(), x[:, ::2]):
+        with pytest.raises((ValueError, TypeError)):
+            rvq.rvq_rms_norm(bad)
+    for eps in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(rvq.RVQError):
+            rvq.rvq_rms_norm(x, eps=eps)
+    for bad in (dict(h=x[:3]), dict(h=x.bfloat16()), dict(rstd=rstd[:3]), dict(rstd=rstd.double()),
+                dict(dsum=x.bfloat16()), dict(out=x[:2]), dict(weight=rstd)):
+        with pytest.raises((ValueError, TypeError)):
+            rvq.rvq_rms_norm_backward(**{**dict(dy=x, h=x, rstd=rstd), **bad})
