@@ -50,6 +50,119 @@ __device__ __forceinline__ float load_either(const void *p, bool bf16, int64_t i
   return bf16 ? load_f32((const uint16_t *)p, i) : load_f32((const float *)p, i);
 }
 
+// ---- 16-byte pieces of a row: 4 fp32 or 8 bf16 elements ----
+// Rows need not begin at a multiple of 16 bytes (odd widths, slices): the
+// hardware takes wide loads and stores at any element's address, so one path
+// serves every alignment.  The piece a row ends in is taken by elements.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_at1 __attribute__((aligned(1)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
+typedef uint32_t u32_at1 __attribute__((aligned(1)));
+
+template <typename T>
+constexpr int kPiece = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ void unpack(u32x4 q, float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(q[e]);
+}
+__device__ __forceinline__ void unpack(u32x4 q, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(q[e] << 16);
+    v[2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
+}
+__device__ __forceinline__ u32x4 load16(const float *p) { return *(const u32x4_at4 *)p; }
+__device__ __forceinline__ u32x4 load16(const uint16_t *p) { return *(const u32x4_at2 *)p; }
+
+// N elements at p; `left` of them exist (the others read as zero)
+template <int N>
+__device__ __forceinline__ void load_n(const float *p, int left, float (&v)[N]) {
+  if (left >= N) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const u32x4 q = load16(p + j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[j + e] = __uint_as_float(q[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = e < left ? p[e] : 0.f;
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_n(const uint16_t *p, int left, float (&v)[N]) {
+  if (left >= N) {
+    if constexpr (N == 8) {
+      unpack(load16(p), v);
+    } else {
+      const u32x2 q = *(const u32x2_at2 *)p;
+      v[0] = __uint_as_float(q[0] << 16);
+      v[1] = __uint_as_float(q[0] & 0xffff0000u);
+      v[2] = __uint_as_float(q[1] << 16);
+      v[3] = __uint_as_float(q[1] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = e < left ? bf16_bits_to_f32(p[e]) : 0.f;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_n(float *p, int left, const float (&v)[N]) {
+  if (left >= N) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const u32x4 q = {__float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
+                       __float_as_uint(v[j + 3])};
+      *(u32x4_at4 *)(p + j) = q;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < left) p[e] = v[e];
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_n(uint16_t *p, int left, const float (&v)[N]) {
+  if (left >= N) {
+    if constexpr (N == 8) {
+      const u32x4 q = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7])};
+      *(u32x4_at2 *)p = q;
+    } else {
+      const u32x2 q = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      *(u32x2_at2 *)p = q;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < left) p[e] = f32_to_bf16_bits(v[e]);
+  }
+}
+// e4m3 bytes of values within +-448
+template <int N>
+__device__ __forceinline__ void store_f8_n(uint8_t *p, int left, const float (&v)[N]) {
+  if (left >= N) {
+    if constexpr (N == 8) {
+      const u32x2 q = {pack_f8x4(v[0], v[1], v[2], v[3]), pack_f8x4(v[4], v[5], v[6], v[7])};
+      *(u32x2_at1 *)p = q;
+    } else {
+      *(u32_at1 *)p = pack_f8x4(v[0], v[1], v[2], v[3]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < left) p[e] = f32_to_f8(v[e]);
+  }
+}
+
 __device__ __forceinline__ float wave_max_f32(float v) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
@@ -77,11 +190,11 @@ struct NormGradArgs {
   bool w_bf16;
   void *dx;
   float *dweight;             // null: not wanted
-  float *part;                // [norm_grad_parts(n)][d]
+  float *part;                // [norm_grad_parts(n, d, bf16)][d]
   int64_t n;
   int d;
 };
-int64_t norm_grad_parts(int64_t n);
+int64_t norm_grad_parts(int64_t n, int d, bool bf16);
 hipError_t launch_rms_norm_grad(const NormGradArgs &a, bool bf16, hipStream_t s);
 
 struct EmbedGradArgs {

@@ -103,7 +103,8 @@ rvq_status rvq_rms_norm(const void *x, const void *residual, rvq_dtype x_dtype, 
 rvq_status rvq_rms_norm_backward_workspace_size(int64_t n, int32_t d, size_t *bytes) {
   RVQ_TRY(check_rows(n, d));
   if (!bytes) return fail(RVQ_ERR_INVALID_ARGUMENT, "bytes must not be NULL");
-  *bytes = al256((size_t)norm_grad_parts(n) * (size_t)d * sizeof(float));
+  const int64_t p32 = norm_grad_parts(n, d, false), p16 = norm_grad_parts(n, d, true);
+  *bytes = al256((size_t)(p32 > p16 ? p32 : p16) * (size_t)d * sizeof(float));
   return RVQ_OK;
 }
 

@@ -5,6 +5,12 @@
 //
 // Everything between the loads and the stores is fp32; h is rounded to the
 // rows' type only where it is stored, and the norm uses the unrounded sum.
+//
+// Bound by memory: a row is read once, held in registers for the sum and for
+// the products, and written once.  A row is shared by W lanes of P 16-byte
+// pieces each: a part of a wave for narrow rows (several rows a wave), a wave
+// up to 128 pieces, else a workgroup.  Rows of more than 2048 pieces (8192
+// fp32 or 16384 bf16 elements) are read again for each pass over them.
 #include "learn.h"
 
 namespace rvq {
@@ -14,33 +20,149 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 1 << 20;  // workgroups of a launch; rows beyond are looped over
 
-__device__ __forceinline__ float block_sum(float v, float *red) {
-  v = wave_sum_f32(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.f;
+// Sum over the W lanes of a row; for W == kThreads through `red`, which is
+// free again after the next barrier.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float *red) {
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) s += red[w];
-  return s;
+  for (int off = (W < 64 ? W : 64) / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  if constexpr (W > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < W / 64; ++w) v += red[w];
+  }
+  return v;
+}
+template <int W>
+__device__ __forceinline__ float row_max(float v, float *red) {
+#pragma unroll
+  for (int off = (W < 64 ? W : 64) / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  if constexpr (W > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < W / 64; ++w) v = fmaxf(v, red[w]);
+  }
+  return v;
 }
 
-__device__ __forceinline__ float block_max(float v, float *red) {
-  v = wave_max_f32(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = red[0];
+template <int N>
+__device__ __forceinline__ void load_weight(const void *w, bool bf16, int c, int left, float (&v)[N]) {
+  if (!w) {
 #pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) s = fmaxf(s, red[w]);
-  return s;
+    for (int e = 0; e < N; ++e) v[e] = 1.f;
+  } else if (bf16) {
+    load_n<N>((const uint16_t *)w + c, left, v);
+  } else {
+    load_n<N>((const float *)w + c, left, v);
+  }
+}
+
+// how a row of `pieces` is shared: W lanes, P pieces each
+#define RVQ_NORM_SHAPES(X) \
+  X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(64, 2) X(256, 1) X(256, 2) X(256, 4) X(256, 8)
+struct Shape {
+  int w, p;
+};
+Shape shape_of(int64_t pieces) {
+#define RVQ_SHAPE(W, P) \
+  if (pieces <= W * P) return {W, P};
+  RVQ_NORM_SHAPES(RVQ_SHAPE)
+#undef RVQ_SHAPE
+  return {0, 0};
 }
 
 }  // namespace
 
-// One workgroup per row, which is read again for each pass over it.
-template <typename T>
+template <typename T, int W, int P>
 __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
+  constexpr int N = kPiece<T>, R = kThreads / W;
+  __shared__ float red[kThreads / 64];
+  const int lane = threadIdx.x % W;
+  // W == kThreads: the row is the same for the whole workgroup, as the barriers need
+  for (int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / W; row < a.n; row += (int64_t)gridDim.x * R) {
+    const int64_t at = row * a.d;
+    float h[P][N];
+    float ss = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * W + lane) * N;
+      if (c < a.d) {
+        load_n<N>((const T *)a.x + at + c, a.d - c, h[p]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[p][e] = 0.f;
+      }
+    }
+    if (a.residual) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int c = (p * W + lane) * N;
+        if (c >= a.d) continue;
+        float v[N];
+        load_n<N>((const T *)a.residual + at + c, a.d - c, v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[p][e] += v[e];
+      }
+    }
+    if (a.sum) {  // after this lane's own loads of the piece: sum may be x or residual itself
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int c = (p * W + lane) * N;
+        if (c < a.d) store_n<N>((T *)a.sum + at + c, a.d - c, h[p]);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int e = 0; e < N; ++e) ss += h[p][e] * h[p][e];
+    ss = row_sum<W>(ss, red);
+    const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+    if (a.rstd && lane == 0) a.rstd[row] = r;
+    float top = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * W + lane) * N;
+      if (c >= a.d) continue;
+      float w[N];
+      load_weight<N>(a.weight, a.w_bf16, c, a.d - c, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        h[p][e] = h[p][e] * r * w[e];
+        top = fmaxf(top, fabsf(h[p][e]));
+      }
+      if (a.y_type == RVQ_BF16)
+        store_n<N>((uint16_t *)a.y + at + c, a.d - c, h[p]);
+      else if (a.y_type == RVQ_F32)
+        store_n<N>((float *)a.y + at + c, a.d - c, h[p]);
+    }
+    if (a.y_type == RVQ_F8E4M3) {
+      top = row_max<W>(top, red);
+      // a row that holds NaN or infinity gets the scale NaN
+      const float scale = fmaxf(top / kF8Max, kScaleMin) + (ss - ss);
+      const float inv = 1.f / scale;
+      if (lane == 0) a.scale[row] = scale;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int c = (p * W + lane) * N;
+        if (c >= a.d) continue;
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[p][e] = clamp_f8(h[p][e] * inv);
+        store_f8_n<N>((uint8_t *)a.y + at + c, a.d - c, h[p]);
+      }
+    }
+  }
+}
+
+// Rows too wide for registers: one workgroup per row, which is read again for
+// each pass over it.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void rms_norm_wide_kernel(NormArgs a) {
   __shared__ float red[kThreads / 64];
   const T *x = (const T *)a.x, *res = (const T *)a.residual;
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
@@ -56,15 +178,14 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
       const float h = h_of(i);
       ss += h * h;
     }
-    ss = block_sum(ss, red);
+    ss = row_sum<kThreads>(ss, red);
     const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = r;
     float inv = 1.f;
     if (a.y_type == RVQ_F8E4M3) {
       float top = 0.f;
       for (int i = threadIdx.x; i < a.d; i += kThreads) top = fmaxf(top, fabsf(h_of(i) * r * w_of(i)));
-      top = block_max(top, red);
-      // a row that holds NaN or infinity gets the scale NaN
+      top = row_max<kThreads>(top, red);
       const float scale = fmaxf(top / kF8Max, kScaleMin) + (ss - ss);
       inv = 1.f / scale;
       if (threadIdx.x == 0) a.scale[row] = scale;
@@ -72,7 +193,6 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
     for (int i = threadIdx.x; i < a.d; i += kThreads) {
       const float h = h_of(i);
       const float y = h * r * w_of(i);
-      // stored after this thread's own loads of the element: sum may be x or residual itself
       if (a.sum) store_f32((T *)a.sum, at + i, h);
       if (a.y_type == RVQ_F8E4M3)
         ((uint8_t *)a.y)[at + i] = f32_to_f8(clamp_f8(y * inv));
@@ -84,23 +204,137 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
   }
 }
 
-hipError_t launch_rms_norm(const NormArgs &a, bool x_bf16, hipStream_t s) {
-  if (a.n == 0) return hipSuccess;
-  const dim3 grid((unsigned)(a.n < kMaxGroups ? a.n : kMaxGroups));
-  if (x_bf16)
-    rms_norm_kernel<uint16_t><<<grid, kThreads, 0, s>>>(a);
-  else
-    rms_norm_kernel<float><<<grid, kThreads, 0, s>>>(a);
+template <typename T>
+static hipError_t norm_rows(const NormArgs &a, hipStream_t s) {
+  const Shape sh = shape_of(ceil_div(a.d, kPiece<T>));
+  const int64_t groups = sh.w ? ceil_div(a.n, kThreads / sh.w) : a.n;
+  const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
+#define RVQ_NORM(W, P)                                           \
+  if (sh.w == W && sh.p == P) {                                  \
+    rms_norm_kernel<T, W, P><<<grid, kThreads, 0, s>>>(a);       \
+    return hipGetLastError();                                    \
+  }
+  RVQ_NORM_SHAPES(RVQ_NORM)
+#undef RVQ_NORM
+  rms_norm_wide_kernel<T><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
+hipError_t launch_rms_norm(const NormArgs &a, bool x_bf16, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  return x_bf16 ? norm_rows<uint16_t>(a, s) : norm_rows<float>(a, s);
+}
+
 // ---- gradient ----
-//   dx = r (g - h r mean(g h r)) + dsum with g = dy w;  dw = sum over rows of dy h r
-// The rows' sum is taken in fixed parts of consecutive rows, and the parts
-// in order, so it depends on n alone.
+//   dx = r (g - u mean(g u)) + dsum with g = dy w, u = h r;  dw = sum over rows of dy u
+// One pass: a workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its
+// part of dw in registers; the parts are added in order by a second launch.
+// The number of parts depends on n and d alone, so the result does too.
+
+namespace {
+
+constexpr int kMaxParts = 1024;
+constexpr int kWideParts = 256;
+
+int rows_per_group(int64_t pieces) {
+  const Shape sh = shape_of(pieces);
+  return sh.w ? kThreads / sh.w : 1;
+}
+
+}  // namespace
+
+int64_t norm_grad_parts(int64_t n, int d, bool bf16) {
+  const int64_t pieces = ceil_div(d, bf16 ? kPiece<uint16_t> : kPiece<float>);
+  if (n == 0) return 1;
+  if (!shape_of(pieces).w) return n < kWideParts ? n : kWideParts;
+  // four rows a workgroup's turn before there are as many as the device holds
+  const int64_t groups = ceil_div(n, 4 * rows_per_group(pieces));
+  return groups < kMaxParts ? groups : kMaxParts;
+}
+
+template <typename T, int W, int P, bool DW>
+__global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a) {
+  constexpr int N = kPiece<T>, R = kThreads / W;
+  __shared__ float red[kThreads / 64];
+  const int lane = threadIdx.x % W;
+  float acc[P][N];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[p][e] = 0.f;
+  for (int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / W; row < a.n; row += (int64_t)gridDim.x * R) {
+    const int64_t at = row * a.d;
+    const float r = a.rstd[row];
+    float g[P][N], u[P][N];
+    float dot = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * W + lane) * N;
+      if (c < a.d) {
+        load_n<N>((const T *)a.dy + at + c, a.d - c, g[p]);
+        load_n<N>((const T *)a.h + at + c, a.d - c, u[p]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) g[p][e] = u[p][e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * W + lane) * N;
+      if (c >= a.d) continue;
+      float w[N];
+      load_weight<N>(a.weight, a.w_bf16, c, a.d - c, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        u[p][e] *= r;
+        if (DW) acc[p][e] += g[p][e] * u[p][e];
+        g[p][e] *= w[e];
+        dot += g[p][e] * u[p][e];
+      }
+    }
+    const float mean = row_sum<W>(dot, red) / (float)a.d;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * W + lane) * N;
+      if (c >= a.d) continue;
+      float v[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = 0.f;
+      if (a.dsum) load_n<N>((const T *)a.dsum + at + c, a.d - c, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] += r * (g[p][e] - u[p][e] * mean);
+      // dx may be dy or dsum itself: both were loaded by this lane
+      store_n<N>((T *)a.dx + at + c, a.d - c, v);
+    }
+  }
+  if constexpr (DW) {
+    float *part = a.part + (int64_t)blockIdx.x * a.d;
+    if constexpr (R == 1) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int c = (p * W + lane) * N;
+        if (c < a.d) store_n<N>(part + c, a.d - c, acc[p]);
+      }
+    } else {  // the workgroup's rows, in order
+      constexpr int C = W * P * N;  // padded width
+      __shared__ float sums[R * C];
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int e = 0; e < N; ++e) sums[(threadIdx.x / W) * C + (p * W + lane) * N + e] = acc[p][e];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.d; c += kThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < R; ++q) s += sums[q * C + c];
+        part[c] = s;
+      }
+    }
+  }
+}
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a) {
+__global__ __launch_bounds__(kThreads) void rms_norm_grad_wide_kernel(NormGradArgs a) {
   __shared__ float red[kThreads / 64];
   const T *dy = (const T *)a.dy, *h = (const T *)a.h, *ds = (const T *)a.dsum;
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
@@ -110,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a)
     float dot = 0.f;
     for (int i = threadIdx.x; i < a.d; i += kThreads)
       dot += load_f32(dy, at + i) * w_of(i) * (load_f32(h, at + i) * r);
-    const float mean = block_sum(dot, red) / (float)a.d;
+    const float mean = row_sum<kThreads>(dot, red) / (float)a.d;
     for (int i = threadIdx.x; i < a.d; i += kThreads) {
       float v = r * (load_f32(dy, at + i) * w_of(i) - load_f32(h, at + i) * r * mean);
       if (ds) v += load_f32(ds, at + i);
@@ -120,7 +354,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a)
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void rms_norm_dweight_kernel(NormGradArgs a, int64_t parts) {
+__global__ __launch_bounds__(kThreads) void rms_norm_dweight_wide_kernel(NormGradArgs a, int64_t parts) {
   const int c = blockIdx.x * kThreads + threadIdx.x;
   const int64_t part = blockIdx.y;
   if (c >= a.d) return;
@@ -131,36 +365,56 @@ __global__ __launch_bounds__(kThreads) void rms_norm_dweight_kernel(NormGradArgs
   a.part[part * a.d + c] = s;
 }
 
-__global__ __launch_bounds__(kThreads) void rms_norm_dweight_join_kernel(const float *part,
-                                                                         int64_t parts, int d,
-                                                                         float *dweight) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= d) return;
+// Columns' sums over the parts: 64 columns a workgroup, a wave for every 1/16
+// of the parts.
+__global__ __launch_bounds__(1024) void rms_norm_dweight_join_kernel(const float *part, int64_t parts,
+                                                                     int d, float *dweight) {
+  __shared__ float sums[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
   float s = 0.f;
-  for (int64_t p = 0; p < parts; ++p) s += part[p * d + c];
-  dweight[c] = s;
+  if (c < d)
+    for (int64_t p = parts * wave / 16; p < parts * (wave + 1) / 16; ++p) s += part[p * d + c];
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < d) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += sums[w][lane];
+    dweight[c] = s;
+  }
 }
 
-int64_t norm_grad_parts(int64_t n) { return n < 256 ? (n > 0 ? n : 1) : 256; }
+template <typename T>
+static hipError_t norm_grad_rows(const NormGradArgs &a, hipStream_t s) {
+  const int64_t parts = norm_grad_parts(a.n, a.d, sizeof(T) == 2);
+  const Shape sh = shape_of(ceil_div(a.d, kPiece<T>));
+  if (!sh.w || a.n == 0) {
+    if (a.dweight)  // before dx, which may take the place of dy
+      rms_norm_dweight_wide_kernel<T>
+          <<<dim3((unsigned)ceil_div(a.d, kThreads), (unsigned)parts), kThreads, 0, s>>>(a, parts);
+    if (a.n > 0)
+      rms_norm_grad_wide_kernel<T>
+          <<<dim3((unsigned)(a.n < kMaxGroups ? a.n : kMaxGroups)), kThreads, 0, s>>>(a);
+  }
+  const dim3 grid((unsigned)parts);
+#define RVQ_NORM(W, P)                                                                    \
+  if (a.n > 0 && sh.w == W && sh.p == P) {                                                \
+    if (a.dweight)                                                                        \
+      rms_norm_grad_kernel<T, W, P, true><<<grid, kThreads, 0, s>>>(a);                   \
+    else                                                                                  \
+      rms_norm_grad_kernel<T, W, P, false><<<grid, kThreads, 0, s>>>(a);                  \
+  }
+  RVQ_NORM_SHAPES(RVQ_NORM)
+#undef RVQ_NORM
+  if (a.dweight)
+    rms_norm_dweight_join_kernel<<<dim3((unsigned)ceil_div(a.d, 64)), 1024, 0, s>>>(a.part, parts, a.d,
+                                                                                    a.dweight);
+  return hipGetLastError();
+}
 
 hipError_t launch_rms_norm_grad(const NormGradArgs &a, bool bf16, hipStream_t s) {
-  const unsigned cols = (unsigned)ceil_div(a.d, kThreads);
-  if (a.dweight) {  // before dx, which may take the place of dy
-    const int64_t parts = norm_grad_parts(a.n);
-    const dim3 grid(cols, (unsigned)parts);
-    if (bf16)
-      rms_norm_dweight_kernel<uint16_t><<<grid, kThreads, 0, s>>>(a, parts);
-    else
-      rms_norm_dweight_kernel<float><<<grid, kThreads, 0, s>>>(a, parts);
-    rms_norm_dweight_join_kernel<<<cols, kThreads, 0, s>>>(a.part, parts, a.d, a.dweight);
-  }
-  if (a.n == 0) return hipGetLastError();
-  const dim3 grid((unsigned)(a.n < kMaxGroups ? a.n : kMaxGroups));
-  if (bf16)
-    rms_norm_grad_kernel<uint16_t><<<grid, kThreads, 0, s>>>(a);
-  else
-    rms_norm_grad_kernel<float><<<grid, kThreads, 0, s>>>(a);
-  return hipGetLastError();
+  return bf16 ? norm_grad_rows<uint16_t>(a, s) : norm_grad_rows<float>(a, s);
 }
 
 }  // namespace rvq
