@@ -23,11 +23,14 @@ namespace rvq {
 
 namespace {
 
-constexpr int kRange = 128;        // destination rows of one index workgroup
-constexpr int kIndexThreads = 1024;
-constexpr int kIndexWaves = kIndexThreads / 64;
+constexpr int kRange = 512;        // destination rows of one index workgroup
+constexpr int kBatch = 8;          // loads in flight: ID batches of a wave, rows of a sum
+constexpr int kFlight = 4;         // rows of dout in flight while as many are added
+constexpr int kKeysFrom = 2048;   // tokens
+constexpr int kFewTokens = 8192;  // up to here four waves an index workgroup, else sixteen
+constexpr int kNone = INT32_MIN;   // not an ID of this table
 constexpr int kThreads = 256;
-constexpr int kMaxGroups = 1 << 20;
+constexpr int kMaxGroups = 1 << 22;
 
 // Length of a segment of the list.  A row of at most this many tokens is
 // summed in one go.
@@ -43,6 +46,7 @@ struct Tables {
   int64_t V;       // 0: no text gradient
   int64_t T;
   int64_t rows, positions, seg, segments;
+  bool keys;       // the IDs are laid out by table first
 };
 
 Tables tables_of(int64_t T, int L, int K, int64_t V) {
@@ -56,14 +60,32 @@ Tables tables_of(int64_t T, int L, int K, int64_t V) {
   t.seg = segment_length(t.positions);
   // a row has at most T tokens: none is long if T is not
   t.segments = T > t.seg ? ceil_div(t.positions, t.seg) : 0;
+  // the layout is a launch of its own, which short sequences do not win back
+  t.keys = T > kKeysFrom;
   return t;
 }
 
 }  // namespace
 
-__global__ __launch_bounds__(kIndexThreads) void embed_index_kernel(EmbedGradArgs a, Tables tb) {
+// The IDs by table: keys[l][t] is token t's ID in table l (L: the text table),
+// kNone where the token is of the other kind.  The index workgroups read a
+// table's IDs many times over; out of ids [T][L] each such load would touch L
+// times the lines.
+__global__ __launch_bounds__(kThreads) void embed_keys_kernel(EmbedGradArgs a, Tables tb) {
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= tb.T) return;
+  const bool visual = a.is_visual == nullptr || a.is_visual[t] != 0;
+  const int32_t *id = a.ids + t * a.L;
+  for (int l = 0; l < tb.L; ++l) a.keys[l * tb.T + t] = visual ? id[l] : kNone;
+  if (tb.V > 0) a.keys[tb.L * tb.T + t] = visual ? kNone : id[0];
+}
+
+template <int NW>  // waves of a workgroup
+__global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, Tables tb) {
+  constexpr int kIndexWaves = NW, kIndexThreads = NW * 64;
   __shared__ int cnt[kIndexWaves][kRange];
-  __shared__ int below_sum, total;
+  __shared__ int sums[kRange / 64];
+  __shared__ int below_sum;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // this workgroup's rows [r0, r1) of its table
@@ -71,9 +93,9 @@ __global__ __launch_bounds__(kIndexThreads) void embed_index_kernel(EmbedGradArg
   const bool text = (int64_t)blockIdx.x >= (int64_t)tb.L * per_level;
   const int l = text ? 0 : blockIdx.x / per_level;
   const int range = text ? (int)(blockIdx.x - (int64_t)tb.L * per_level) : blockIdx.x % per_level;
-  const int64_t limit = text ? tb.V : tb.K;
-  const int64_t r0 = (int64_t)range * kRange;
-  const int64_t r1 = r0 + kRange < limit ? r0 + kRange : limit;
+  const int limit = (int)(text ? tb.V : tb.K);
+  const int r0 = range * kRange;
+  const int r1 = r0 + kRange < limit ? r0 + kRange : limit;
   const int64_t region = text ? tb.L * tb.T : l * tb.T;
   const int64_t row0 = (text ? (int64_t)tb.L * tb.K : (int64_t)l * tb.K) + r0;
 
@@ -84,23 +106,36 @@ __global__ __launch_bounds__(kIndexThreads) void embed_index_kernel(EmbedGradArg
   const int64_t piece = round_up(ceil_div(tb.T, kIndexWaves), 64);
   const int64_t t0 = wave * piece < tb.T ? wave * piece : tb.T;
   const int64_t t1 = t0 + piece < tb.T ? t0 + piece : tb.T;
-  // the token's ID in this table, or -1 (a token of the other kind)
-  const auto id_of = [&](int64_t t, bool &mine) {
-    mine = (a.is_visual == nullptr || a.is_visual[t] != 0) != text;
-    return a.ids[t * a.L + l];
+  // IDs of kBatch x 64 tokens in this table; kNone for a token of the other kind
+  const auto load_ids = [&](int64_t tw, int (&id)[kBatch]) {
+    if (tb.keys) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t t = tw + u * 64 + lane;
+        id[u] = t < t1 ? a.keys[region + t] : kNone;
+      }
+      return;
+    }
+    bool mine[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t t = tw + u * 64 + lane;
+      id[u] = t < t1 ? a.ids[t * a.L + l] : 0;
+      mine[u] = t < t1 && (a.is_visual == nullptr || a.is_visual[t] != 0) != text;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) id[u] = mine[u] ? id[u] : kNone;
   };
 
   int below = 0, bad = 0;
-  for (int64_t t = t0 + lane; t < t1; t += 64) {
-    bool mine;
-    const int id = id_of(t, mine);
-    if (!mine) continue;
-    if (id < 0 || id >= limit) {
-      ++bad;
-    } else if (id < r0) {
-      ++below;
-    } else if (id < r1) {
-      atomicAdd(&cnt[wave][id - (int)r0], 1);
+  for (int64_t tw = t0; tw < t1; tw += kBatch * 64) {
+    int id[kBatch];
+    load_ids(tw, id);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      below += id[u] >= 0 && id[u] < r0;
+      bad += (id[u] < 0 && id[u] != kNone) || id[u] >= limit;
+      if (id[u] >= r0 && id[u] < r1) atomicAdd(&cnt[wave][id[u] - r0], 1);
     }
   }
 #pragma unroll
@@ -114,80 +149,134 @@ __global__ __launch_bounds__(kIndexThreads) void embed_index_kernel(EmbedGradArg
   }
   __syncthreads();
 
-  // a row's tokens: its waves' in turn; the rows one after the other
-  if (wave == 0) {
-    int mine[kRange / 64], sum = 0;
+  // RP rows a thread: a row's waves' tokens in turn, the rows one after the other
+  constexpr int RP = kRange / kIndexThreads > 1 ? kRange / kIndexThreads : 1;
+  const int r = threadIdx.x * RP;
+  int mine[RP], all = 0, incl = 0;
+  if (r < kRange) {
 #pragma unroll
-    for (int j = 0; j < kRange / 64; ++j) {
-      int c = 0;
-      for (int w = 0; w < kIndexWaves; ++w) {
-        const int v = cnt[w][lane * (kRange / 64) + j];
-        cnt[w][lane * (kRange / 64) + j] = c;
-        c += v;
-      }
-      mine[j] = c;
-      sum += c;
+    for (int j = 0; j < RP; ++j) {
+      mine[j] = 0;
+#pragma unroll
+      for (int w = 0; w < kIndexWaves; ++w) mine[j] += cnt[w][r + j];
+      all += mine[j];
     }
-    int incl = sum;
+    incl = all;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int v = __shfl_up(incl, off, 64);
       if (lane >= off) incl += v;
     }
-    int at = (int)region + below_sum + incl - sum;
+    if (lane == 63) sums[wave] = incl;
+  }
+  __syncthreads();
+  constexpr int kSums = kRange / RP / 64;
+  int total = (int)region + below_sum;
 #pragma unroll
-    for (int j = 0; j < kRange / 64; ++j) {
-      const int r = lane * (kRange / 64) + j;
-      for (int w = 0; w < kIndexWaves; ++w) cnt[w][r] += at;
-      if (r0 + r < r1) {
-        a.start[row0 + r] = at;
-        a.count[row0 + r] = mine[j];
+  for (int w = 0; w < kSums; ++w) total += sums[w];
+  if (r < kRange) {
+    int at = (int)region + below_sum + incl - all;
+    for (int w = 0; w < wave; ++w) at += sums[w];
+#pragma unroll
+    for (int j = 0; j < RP; ++j) {
+      if (r0 + r + j < r1) {
+        a.start[row0 + r + j] = at;
+        a.count[row0 + r + j] = mine[j];
       }
-      at += mine[j];
+#pragma unroll
+      for (int w = 0; w < kIndexWaves; ++w) {
+        const int c = cnt[w][r + j];
+        cnt[w][r + j] = at;
+        at += c;
+      }
     }
-    if (lane == 63) total = at;
   }
   __syncthreads();
   // the table's last workgroup marks the positions that no token has
   if (r1 == limit)
     for (int64_t i = total + (int64_t)threadIdx.x; i < region + tb.T; i += kIndexThreads) a.row[i] = -1;
 
-  for (int64_t tw = t0; tw < t1; tw += 64) {
-    const int64_t t = tw + lane;
-    bool mine = false;
-    int id = -1;
-    if (t < t1) id = id_of(t, mine);
-    const bool hit = mine && id >= r0 && id < r1;
-    if (__ballot(hit) == 0) continue;
-    const int r = hit ? id - (int)r0 : 0;
-    // lanes of the same row
-    unsigned long long same = __ballot(hit);
+  for (int64_t tw = t0; tw < t1; tw += kBatch * 64) {
+    int id[kBatch];
+    load_ids(tw, id);
 #pragma unroll
-    for (int b = 0; (1 << b) < kRange; ++b) {
-      const unsigned long long m = __ballot((r >> b) & 1);
-      same &= ((r >> b) & 1) ? m : ~m;
-    }
-    const int first = hit ? __ffsll((long long)same) - 1 : lane;
-    int at = 0;
-    if (hit && lane == first) at = atomicAdd(&cnt[wave][r], __popcll(same));
-    at = __shfl(at, first, 64);
-    if (hit) {
-      at += __popcll(same & ((1ull << lane) - 1));
-      a.token[at] = (int)t;
-      a.row[at] = (int)(row0 + r);
+    for (int u = 0; u < kBatch; ++u) {
+      const bool hit = id[u] >= r0 && id[u] < r1;
+      unsigned long long same = __ballot(hit);  // then: lanes of the same row
+      if (same == 0) continue;
+      const int k = hit ? id[u] - r0 : 0;
+#pragma unroll
+      for (int b = 0; (1 << b) < kRange; ++b) {
+        const unsigned long long m = __ballot((k >> b) & 1);
+        same &= ((k >> b) & 1) ? m : ~m;
+      }
+      const int first = hit ? __ffsll((long long)same) - 1 : lane;
+      int at = 0;
+      if (hit && lane == first) at = atomicAdd(&cnt[wave][k], __popcll(same));
+      at = __shfl(at, first, 64);
+      if (hit) {
+        at += __popcll(same & ((1ull << lane) - 1));
+        a.token[at] = (int)(tw + u * 64 + lane);
+        a.row[at] = (int)(row0 + k);
+      }
     }
   }
 }
 
 namespace {
 
-// sum of list entries [e0, e1) in column c
-template <typename T>
-__device__ __forceinline__ float sum_entries(const EmbedGradArgs &a, int64_t e0, int64_t e1, int c) {
-  float s = 0.f;
-  for (int64_t e = e0; e < e1; ++e) s += load_f32((const T *)a.dout, (int64_t)a.token[e] * a.D + c);
-  return s;
-}
+// A lane's 16-byte piece of the rows: where it is read, and which of its
+// elements are the lane's to write.  A row that ends inside the piece is read
+// from N elements before its end on, so that every load is whole; rows of
+// fewer than N elements (TINY) are read by elements.
+template <typename T, bool TINY>
+struct Piece {
+  static constexpr int N = kPiece<T>;
+  uint32_t at;      // byte offset of the first element read
+  int first, last;  // elements [first, last) are written; none where the lane is past the row
+
+  __device__ __forceinline__ Piece(int c, int D) {
+    const int left = D - c;
+    const int from = TINY || left >= N ? c : D - N;
+    at = left > 0 ? (uint32_t)from * (uint32_t)sizeof(T) : 0;
+    first = left > 0 ? c - from : 0;
+    last = left <= 0 ? 0 : TINY && left < N ? left : N;
+  }
+  __device__ __forceinline__ u32x4 load(const T *row) const {
+    const T *x = (const T *)((const char *)row + at);
+    if constexpr (!TINY) {
+      return load16(x);
+    } else {
+      u32x4 q = {0, 0, 0, 0};
+      for (int j = 0; j < last; ++j) {
+        if constexpr (sizeof(T) == 4)
+          q[j] = __float_as_uint(x[j]);
+        else
+          q[j / 2] |= (uint32_t)x[j] << (16 * (j & 1));
+      }
+      return q;
+    }
+  }
+  // o: where element 0 of the piece goes
+  template <typename G>
+  __device__ __forceinline__ void store(G *o, const float (&s)[N], bool accumulate) const {
+    if (first == 0 && last == N) {
+      if (!accumulate) {
+        store_n<N>(o, N, s);
+        return;
+      }
+      float v[N];
+      load_n<N>(o, N, v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] += s[j];
+      store_n<N>(o, N, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (j >= first && j < last) store_f32(o, j, accumulate ? s[j] + load_f32(o, j) : s[j]);
+    }
+  }
+};
 
 template <typename G>
 __device__ __forceinline__ G *row_of(const EmbedGradArgs &a, const Tables &tb, int64_t row) {
@@ -197,37 +286,137 @@ __device__ __forceinline__ G *row_of(const EmbedGradArgs &a, const Tables &tb, i
 
 }  // namespace
 
-// Workgroups [0, row_groups) take rows; the others a segment each, whose
-// first and last row may be long ones: their sums go to part[2 s] (the row
-// that holds the segment's first position) and part[2 s + 1] (the row that
-// begins inside it).
-template <typename T, typename G>
-__global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Tables tb,
-                                                             int row_groups) {
-  if ((int)blockIdx.x < row_groups) {
-    for (int64_t row = blockIdx.x; row < tb.rows; row += row_groups) {
-      const int64_t n = a.count[row], e0 = a.start[row];
-      if ((tb.segments && n > tb.seg) || (a.accumulate && n == 0)) continue;
-      G *o = row_of<G>(a, tb, row);
-      for (int c = threadIdx.x; c < a.D; c += kThreads) {
-        float s = sum_entries<T>(a, e0, e0 + n, c);
-        if (a.accumulate) s += load_f32(o, c);
-        store_f32(o, c, s);
+// W lanes sum W x N columns (a slab) of R consecutive rows of one table,
+// R <= W.  Their tokens follow one another in the list, so the wave runs
+// through the list: kFlight rows of dout are loaded while the kFlight before
+// them are added, and a row is stored when its last token has been.  Lane j
+// holds row j's place in the list and the tokens of W positions, so that the
+// only loads that are waited for are those of dout.
+// The first 2 x segments units are pieces of long rows: of a segment, the row
+// that holds its first position (part[2 s]), and the row that begins inside
+// it (part[2 s + 1]).
+template <typename T, typename G, int W, bool TINY>
+__global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Tables tb, int R,
+                                                             int slabs) {
+  constexpr int N = kPiece<T>;
+  const int lane = threadIdx.x % W;
+  // lane j's value, j the same for the W lanes
+  const auto from = [](int v, int j) {
+    if constexpr (W == 64)
+      return __builtin_amdgcn_readlane(v, j);
+    else
+      return __shfl(v, j, W);
+  };
+  const int level_groups = (int)ceil_div(tb.K, R);
+  const int64_t groups = (int64_t)tb.L * level_groups + ceil_div(tb.V, R);
+  const int64_t units = 2 * tb.segments + groups;
+  int64_t v = (int64_t)blockIdx.x * (kThreads / W) + threadIdx.x / W;
+  if constexpr (W == 64)  // the same for the wave
+    v = (int64_t)blockIdx.x * (kThreads / W) + __builtin_amdgcn_readfirstlane(threadIdx.x / W);
+  for (; v < units * slabs; v += (int64_t)gridDim.x * (kThreads / W)) {
+    const int64_t u = v / slabs;
+    const int c = ((int)(v - u * slabs) * W + lane) * N;
+    const Piece<T, TINY> piece(c, a.D);
+    const bool mine = c < a.D;
+    float s[N];
+    int counts = 0, starts = 0, rows = 1;
+    G *o = nullptr;         // the row that is being summed
+    float *part = nullptr;  // instead of it: a long row's piece
+    if (u < 2 * tb.segments) {
+      const int64_t p0 = (u >> 1) * tb.seg;
+      const int64_t p1 = p0 + tb.seg < tb.positions ? p0 + tb.seg : tb.positions;
+      const int ra = a.row[p0], row = u & 1 ? a.row[p1 - 1] : ra;
+      if (row < 0 || (u & 1 && row == ra) || a.count[row] <= tb.seg) continue;
+      const int64_t b = a.start[row], e = b + a.count[row];
+      starts = (int)(b > p0 ? b : p0);
+      counts = (int)(e < p1 ? e : p1) - starts;
+      part = a.part + u * a.D;
+    } else {
+      // rows row0 .. row0 + rows - 1, of one table
+      const int64_t g = u - 2 * tb.segments;
+      const bool text = g >= (int64_t)tb.L * level_groups;
+      const int l = text ? tb.L : (int)(g / level_groups);
+      const int64_t r0 = (text ? g - (int64_t)tb.L * level_groups : g - (int64_t)l * level_groups) * R;
+      const int64_t limit = text ? tb.V : tb.K;
+      rows = (int)(limit - r0 < R ? limit - r0 : R);
+      const int64_t row0 = (int64_t)l * tb.K + r0;
+      if (lane < rows) {
+        counts = a.count[row0 + lane];
+        starts = a.start[row0 + lane];
       }
+      o = row_of<G>(a, tb, row0);
     }
-    return;
-  }
-  const int64_t s = blockIdx.x - row_groups;
-  const int64_t p0 = s * tb.seg, p1 = p0 + tb.seg < tb.positions ? p0 + tb.seg : tb.positions;
-  const int ra = a.row[p0], rb = a.row[p1 - 1];
-  if (ra >= 0 && a.count[ra] > tb.seg) {
-    const int64_t end = (int64_t)a.start[ra] + a.count[ra];
-    for (int c = threadIdx.x; c < a.D; c += kThreads)
-      a.part[2 * s * a.D + c] = sum_entries<T>(a, p0, end < p1 ? end : p1, c);
-  }
-  if (rb >= 0 && rb != ra && a.count[rb] > tb.seg) {
-    for (int c = threadIdx.x; c < a.D; c += kThreads)
-      a.part[(2 * s + 1) * a.D + c] = sum_entries<T>(a, a.start[rb], p1, c);
+    const auto store = [&](int n) {
+      if (mine && part)
+        piece.store(part + piece.at / sizeof(T), s, false);
+      else if (mine && !(a.accumulate && n == 0))
+        piece.store(o + piece.at / sizeof(T), s, a.accumulate);
+      o += a.D;
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[j] = 0.f;
+    };
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] = 0.f;
+
+    for (int i = 0; i < rows;) {
+      // rows [i, k) are short; k is a long row, which is not this wave's, or the end
+      int k = i;
+      if (tb.segments)
+        while (k < rows && from(counts, k) <= tb.seg) ++k;
+      else
+        k = rows;
+      int e = 0, e1 = 0;
+      if (k > i) {
+        e = from(starts, i);
+        e1 = from(starts, k - 1) + from(counts, k - 1);
+      }
+      int n = k > i ? from(counts, i) : 0, end = e + n;   // row i's
+      int w0 = e, tokens = 0, next = 0;                   // positions [w0, w0 + W), and the W after them
+      if (e < e1) {
+        tokens = e + lane < e1 ? a.token[e + lane] : 0;
+        next = e + W + lane < e1 ? a.token[e + W + lane] : 0;
+      }
+      u32x4 raw[2][kFlight];
+      const auto load = [&](int p, u32x4(&q)[kFlight]) {  // positions p .. p + kFlight - 1 below e1
+        if (p - w0 >= W) {                                // kFlight divides W and p - w0
+          w0 += W;
+          tokens = next;
+          next = w0 + W + lane < e1 ? a.token[w0 + W + lane] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j)
+          if (p + j < e1)
+            q[j] = piece.load((const T *)a.dout + (int64_t)from(tokens, p + j - w0) * a.D);
+      };
+      const auto add = [&](int p, const u32x4(&q)[kFlight]) {
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j)
+          if (p + j < e1) {
+            while (p + j >= end) {  // the rows that end here
+              store(n);
+              n = from(counts, ++i);
+              end += n;
+            }
+            float f[N];
+            unpack(q[j], f);
+#pragma unroll
+            for (int m = 0; m < N; ++m) s[m] += f[m];
+          }
+      };
+      if (e < e1) load(e, raw[0]);
+      for (; e < e1; e += 2 * kFlight) {
+        load(e + kFlight, raw[1]);
+        add(e, raw[0]);
+        load(e + 2 * kFlight, raw[0]);
+        add(e + kFlight, raw[1]);
+      }
+      for (; i < k; ++i) {
+        store(n);
+        n = i + 1 < k ? from(counts, i + 1) : 0;
+      }
+      if (k < rows) o += a.D;
+      i = k + 1;
+    }
   }
 }
 
@@ -241,12 +430,12 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a, T
   const int64_t end = (int64_t)a.start[row] + a.count[row];
   const int64_t first = a.start[row] == p0 ? 2 * s : 2 * s + 1;
   G *o = row_of<G>(a, tb, row);
-  for (int c = threadIdx.x; c < a.D; c += kThreads) {
-    float v = a.part[first * a.D + c];
-    for (int64_t q = s + 1; q * tb.seg < end; ++q) v += a.part[2 * q * a.D + c];
-    if (a.accumulate) v += load_f32(o, c);
-    store_f32(o, c, v);
-  }
+  const int c = blockIdx.y * kThreads + threadIdx.x;
+  if (c >= a.D) return;
+  float v = a.part[first * a.D + c];
+  for (int64_t q = s + 1; q * tb.seg < end; ++q) v += a.part[2 * q * a.D + c];
+  if (a.accumulate) v += load_f32(o, c);
+  store_f32(o, c, v);
 }
 
 EmbedGradLayout embed_grad_layout(int64_t T, int L, int K, int64_t V, int D) {
@@ -257,16 +446,33 @@ EmbedGradLayout embed_grad_layout(int64_t T, int L, int K, int64_t V, int D) {
   w.token = w.count + al256((size_t)tb.rows * 4);
   w.row = w.token + al256((size_t)tb.positions * 4);
   w.part = w.row + al256((size_t)tb.positions * 4);
-  w.total = w.part + al256((size_t)tb.segments * 2 * D * sizeof(float));
+  w.keys = w.part + al256((size_t)tb.segments * 2 * D * sizeof(float));
+  w.total = w.keys + al256(tb.keys ? (size_t)tb.positions * 4 : 0);
   if (w.total == 0) w.total = 256;
   return w;
 }
 
 template <typename T, typename G>
 static hipError_t launch_sums(const EmbedGradArgs &a, const Tables &tb, hipStream_t s) {
-  const int row_groups = (int)(tb.rows < kMaxGroups ? tb.rows : kMaxGroups);
-  embed_sum_kernel<T, G><<<dim3((unsigned)(row_groups + tb.segments)), kThreads, 0, s>>>(a, tb, row_groups);
-  if (tb.segments) embed_join_kernel<G><<<dim3((unsigned)tb.segments), kThreads, 0, s>>>(a, tb);
+  const int64_t pieces = ceil_div(a.D, kPiece<T>);
+  // rows a wave takes in turn: enough to pay for looking its list up, few
+  // enough for several waves a SIMD
+#define RVQ_SUM(W, TINY)                                                                        \
+  do {                                                                                      \
+    const int64_t slabs = ceil_div(pieces, W);                                              \
+    int64_t R = tb.rows * slabs / (65536 * (64 / W));                                       \
+    R = R < 1 ? 1 : R > W ? W : R;                                                          \
+    const int64_t units = 2 * tb.segments + tb.L * ceil_div(tb.K, R) + ceil_div(tb.V, R);   \
+    const int64_t groups = ceil_div(units * slabs, kThreads / W);                           \
+    embed_sum_kernel<T, G, W, TINY><<<dim3((unsigned)(groups < kMaxGroups ? groups : kMaxGroups)), \
+                                kThreads, 0, s>>>(a, tb, (int)R, (int)slabs);               \
+  } while (0)
+  if (a.D < kPiece<T>) RVQ_SUM(8, true); else if (pieces <= 8) RVQ_SUM(8, false);
+  else if (pieces <= 16) RVQ_SUM(16, false); else if (pieces <= 32) RVQ_SUM(32, false);
+  else RVQ_SUM(64, false);
+#undef RVQ_SUM
+  if (tb.segments) 
+    embed_join_kernel<G><<<dim3((unsigned)tb.segments, (unsigned)ceil_div(a.D, kThreads)), kThreads, 0, s>>>(a, tb);
   return hipGetLastError();
 }
 
@@ -274,7 +480,11 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, bool x_bf16, bool g_bf16, h
   const Tables tb = tables_of(a.T, a.dlevel ? a.L : 0, a.K, a.dtext ? a.V : 0);
   if (tb.rows == 0) return hipSuccess;
   const int64_t units = (int64_t)tb.L * ceil_div(tb.K, kRange) + ceil_div(tb.V, kRange);
-  embed_index_kernel<<<dim3((unsigned)units), kIndexThreads, 0, s>>>(a, tb);
+  if (tb.keys) embed_keys_kernel<<<dim3((unsigned)ceil_div(a.T, kThreads)), kThreads, 0, s>>>(a, tb);
+  if (a.T <= kFewTokens)
+    embed_index_kernel<4><<<dim3((unsigned)units), 256, 0, s>>>(a, tb);
+  else
+    embed_index_kernel<16><<<dim3((unsigned)units), 1024, 0, s>>>(a, tb);
   if (x_bf16)
     return g_bf16 ? launch_sums<uint16_t, uint16_t>(a, tb, s) : launch_sums<uint16_t, float>(a, tb, s);
   return g_bf16 ? launch_sums<float, uint16_t>(a, tb, s) : launch_sums<float, float>(a, tb, s);

@@ -211,9 +211,10 @@ struct EmbedGradArgs {
   int32_t *start, *count;     // [rows]: each destination row's piece of the list
   int32_t *token, *row;       // the list: tokens by destination row, in token order; its row
   float *part;                // [2 segments][D]: sums of the pieces of long rows
+  int32_t *keys;              // [tables][T]: the IDs by table
 };
 struct EmbedGradLayout {
-  size_t start, count, token, row, part, total;
+  size_t start, count, token, row, part, keys, total;
 };
 EmbedGradLayout embed_grad_layout(int64_t T, int L, int K, int64_t V, int D);
 hipError_t launch_embed_grad(const EmbedGradArgs &a, bool x_bf16, bool g_bf16, hipStream_t s);

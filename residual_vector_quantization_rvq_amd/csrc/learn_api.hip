@@ -63,6 +63,7 @@ rvq_status check_tables(int64_t T, int32_t L, int32_t K, int64_t V, int32_t D) {
                 L, K, D, (long long)V);
   if (L > kMaxLevels)
     return fail(RVQ_ERR_UNSUPPORTED, "embedding supports L <= %d (got %d)", kMaxLevels, L);
+  if (D > kMaxWidth) return fail(RVQ_ERR_UNSUPPORTED, "D above %d (got %d)", kMaxWidth, D);
   if (T > kMaxRows || T * (L + 1) > INT32_MAX)
     return fail(RVQ_ERR_UNSUPPORTED, "T above %lld tokens, or T (L + 1) above 2^31 - 1 (got %lld, %d)",
                 (long long)kMaxRows, (long long)T, L);
@@ -183,7 +184,8 @@ rvq_status rvq_embed_tokens_backward(const void *dout, rvq_dtype dout_dtype, con
   char *ws = (char *)workspace;
   EmbedGradArgs a = {dout, ids, is_visual, T, L, K, D, V, dlevel, dtext, accumulate != 0, bad_ids,
                      (int32_t *)(ws + w.start), (int32_t *)(ws + w.count),
-                     (int32_t *)(ws + w.token), (int32_t *)(ws + w.row), (float *)(ws + w.part)};
+                     (int32_t *)(ws + w.token), (int32_t *)(ws + w.row), (float *)(ws + w.part),
+                     (int32_t *)(ws + w.keys)};
   return launched(launch_embed_grad(a, dout_dtype == RVQ_BF16, grad_dtype == RVQ_BF16, stream),
                   "embedding gradient launch");
 }
