@@ -412,7 +412,7 @@ typedef struct rvq_adamw_tensor {
 } rvq_adamw_tensor;
 
 typedef struct rvq_adamw_options {
-    double lr, beta1, beta2, eps;  /* eps >= 1e-30 */
+    double lr, beta1, beta2, eps;  /* eps >= 1e-12 */
     int64_t step;                  /* 1 for the first */
     double grad_scale;             /* 1 for none */
     double max_norm;               /* <= 0: no clipping */

@@ -29,7 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kTable = 40;          // tensors of one launch (kernel arguments: 4 KB)
 constexpr int kChunk = 2048;        // elements of one workgroup; a multiple of kBlock
 constexpr int kBlock = 256;         // elements that share a scale
-constexpr int kNormGroups = 1024;   // partial sums of squares of one launch
+constexpr int kNormGroups = 2048;   // partial sums of squares of one launch
 
 struct Entry {
   void *p;
@@ -66,18 +66,52 @@ __device__ __forceinline__ uint32_t round_bits(uint32_t base, int64_t i) {
   return mix(base + (uint32_t)i * 0x9E3779B1u + (uint32_t)(i >> 32) * 0x3504F333u);
 }
 
-// |v| <= 448 rounded to the e4m3 grid at random: 20 random bits are added
-// under the three bits of the mantissa that stay.  Below 2^-6 the grid is
-// that of 2^-6, reached by adding it for the rounding.
-__device__ __forceinline__ float round_f8(float v, uint32_t random20) {
-  const float a = fabsf(v);
-  const bool small = a < 0x1p-6f;
-  float r = __uint_as_float((__float_as_uint(small ? a + 0x1p-6f : a) + random20) & 0xfff00000u);
-  r = fminf(small ? r - 0x1p-6f : r, kF8Max);
-  return copysignf(r, v);
+// |v| <= 448 rounded to the e4m3 grid at random, into byte `Byte` of `w`.  The
+// instruction adds the upper 20 of the random bits under the three bits of
+// the mantissa that stay; below 2^-6 the grid is that of 2^-6, and the bits
+// stand for the same share of its step.
+template <int Byte>
+__device__ __forceinline__ int random_f8(float v, uint32_t random, int w) {
+  return __builtin_amdgcn_cvt_sr_fp8_f32(v, (int)random, w, Byte);
 }
 __device__ __forceinline__ float round_bf16(float v, uint32_t random16) {
   return __uint_as_float((__float_as_uint(v) + random16) & 0xffff0000u);
+}
+
+// the largest of the 32 lanes of a half wave
+__device__ __forceinline__ float half_wave_max(float v) {
+#define RVQ_ROR(N) \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + N, 0xf, 0xf, false)))
+  RVQ_ROR(8);
+  RVQ_ROR(4);
+  RVQ_ROR(2);
+  RVQ_ROR(1);
+#undef RVQ_ROR
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401f)));  // lane ^ 16
+}
+
+// 8 e4m3 bytes at p; `left` of them exist (the others read as zero)
+__device__ __forceinline__ void load_f8x8(const uint8_t *p, int left, float (&v)[8]) {
+  u32x2 q = {0, 0};
+  if (left >= 8) {
+    q = *(const u32x2_at1 *)p;
+  } else {
+    for (int e = 0; e < left; ++e) q[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    v[4 * j] = __builtin_amdgcn_cvt_f32_fp8((int)q[j], 0);
+    v[4 * j + 1] = __builtin_amdgcn_cvt_f32_fp8((int)q[j], 1);
+    v[4 * j + 2] = __builtin_amdgcn_cvt_f32_fp8((int)q[j], 2);
+    v[4 * j + 3] = __builtin_amdgcn_cvt_f32_fp8((int)q[j], 3);
+  }
+}
+__device__ __forceinline__ void store_8_bytes(uint8_t *p, int left, u32x2 q) {
+  if (left >= 8) {
+    *(u32x2_at1 *)p = q;
+  } else {
+    for (int e = 0; e < left; ++e) p[e] = (uint8_t)(q[e >> 2] >> (8 * (e & 3)));
+  }
 }
 
 // the entry of a workgroup's chunk
@@ -90,30 +124,39 @@ __device__ __forceinline__ int entry_of(const Table &t, int64_t chunk) {
   return lo;
 }
 
-__device__ __forceinline__ void update(float &p, float g, float &m, float &v, const Consts &k,
-                                       float decay) {
+// Root and quotient are the hardware's (one unit in the last place): they act
+// on lr times the update alone.  Returns sqrt(v).
+__device__ __forceinline__ float update(float &p, float g, float &m, float &v, const Consts &k,
+                                        float decay) {
   m = k.b1 * m + k.c1 * g;
   v = k.b2 * v + k.c2 * (g * g);
-  p = p * decay - k.lr1 * m / (sqrtf(v) * k.rk2 + k.eps);
+  const float root = __builtin_amdgcn_sqrtf(v);
+  p = p * decay - k.lr1 * m * __builtin_amdgcn_rcpf(root * k.rk2 + k.eps);
+  return root;
 }
 
 }  // namespace
 
-// Sums of squares of the gradients: a workgroup's chunks in order, in fp64.
+// Sums of squares of the gradients: eight of a lane in fp32, the rest in fp64.
+// A workgroup takes consecutive chunks.
 template <typename G>
 __global__ __launch_bounds__(kThreads) void adamw_norm_kernel(Table t, double *part) {
   __shared__ double red[kThreads / 64];
   double s = 0.0;
-  for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
-    const Entry &e = t.e[entry_of(t, chunk)];
-    const int64_t i0 = (chunk - e.chunk0) * kChunk;
-    const int64_t i1 = i0 + kChunk < e.n ? i0 + kChunk : e.n;
-    float c = 0.f;
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-      const float g = load_f32((const G *)e.g, i);
-      c += g * g;
+  const int64_t c0 = t.chunks * blockIdx.x / gridDim.x, c1 = t.chunks * (blockIdx.x + 1) / gridDim.x;
+  int at = entry_of(t, c0);
+  for (int64_t chunk = c0; chunk < c1; ++chunk) {
+    while (at + 1 < t.count && t.e[at + 1].chunk0 <= chunk) ++at;
+    const Entry &e = t.e[at];
+    const int64_t i = (chunk - e.chunk0) * kChunk + threadIdx.x * 8;
+    if (i < e.n) {
+      float g[8];
+      load_n<8>((const G *)e.g + i, (int)(e.n - i < 8 ? e.n - i : 8), g);
+      float c = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c += g[j] * g[j];
+      s += (double)c;
     }
-    s += (double)c;
   }
   s = wave_sum_f64(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
@@ -127,17 +170,17 @@ __global__ __launch_bounds__(kThreads) void adamw_norm_kernel(Table t, double *p
 
 // The norm, and the factor of every gradient: NaN where the norm is not
 // finite, which leaves the parameters and states as they are.
-__global__ __launch_bounds__(kThreads) void adamw_clip_kernel(const double *part, int64_t n, Consts k,
-                                                              float *clip, float *grad_norm) {
-  __shared__ double red[kThreads / 64];
+__global__ __launch_bounds__(1024) void adamw_clip_kernel(const double *part, int64_t n, Consts k,
+                                                          float *clip, float *grad_norm) {
+  __shared__ double red[16];
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kThreads) s += part[i];
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
   s = wave_sum_f64(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
     double v = 0.0;
-    for (int w = 0; w < kThreads / 64; ++w) v += red[w];
+    for (int w = 0; w < 16; ++w) v += red[w];
     const float norm = (float)(sqrt(v) * (double)fabsf(k.grad_scale));
     if (grad_norm) *grad_norm = norm;
     const float f = k.max_norm / (norm + 1e-6f);
@@ -145,73 +188,109 @@ __global__ __launch_bounds__(kThreads) void adamw_clip_kernel(const double *part
   }
 }
 
+// 32-bit states: two pieces of four elements a lane, all of whose loads are
+// issued before the first is used.
 template <typename P, typename G>
 __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, const float *clip) {
+  constexpr int N = 4, J = kChunk / (kThreads * N);
+  const Entry &e = t.e[entry_of(t, blockIdx.x)];
+  const int64_t i0 = (blockIdx.x - e.chunk0) * kChunk + threadIdx.x * N;
+  float p[J][N], g[J][N], m[J][N], v[J][N];
+  int left[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int64_t i = i0 + j * kThreads * N;
+    left[j] = (int)(e.n - i < 0 ? 0 : e.n - i < N ? e.n - i : N);
+    load_n<N>((const P *)e.p + i, left[j], p[j]);
+    load_n<N>((const G *)e.g + i, left[j], g[j]);
+    load_n<N>((const float *)e.m + i, left[j], m[j]);
+    load_n<N>((const float *)e.v + i, left[j], v[j]);
+  }
   const float c = clip ? *clip : k.grad_scale;
   if (!(c == c)) return;
-  const Entry &e = t.e[entry_of(t, blockIdx.x)];
-  const int64_t i0 = (blockIdx.x - e.chunk0) * kChunk;
-  const int64_t i1 = i0 + kChunk < e.n ? i0 + kChunk : e.n;
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-    float p = load_f32((const P *)e.p, i), m = ((float *)e.m)[i], v = ((float *)e.v)[i];
-    update(p, load_f32((const G *)e.g, i) * c, m, v, k, e.decay);
-    if (sizeof(P) == 2 && k.stochastic) p = round_bf16(p, ((round_bits(e.base, i) >> 21) << 5) + 16);
-    store_f32((P *)e.p, i, p);
-    ((float *)e.m)[i] = m;
-    ((float *)e.v)[i] = v;
-    if (e.copy) e.copy[i] = f32_to_bf16_bits(p);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int64_t i = i0 + j * kThreads * N;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      update(p[j][q], g[j][q] * c, m[j][q], v[j][q], k, e.decay);
+      if (sizeof(P) == 2 && k.stochastic)
+        p[j][q] = round_bf16(p[j][q], ((round_bits(e.base, i + q) >> 21) << 5) + 16);
+    }
+    store_n<N>((P *)e.p + i, left[j], p[j]);
+    store_n<N>((float *)e.m + i, left[j], m[j]);
+    store_n<N>((float *)e.v + i, left[j], v[j]);
+    if (e.copy) store_n<N>(e.copy + i, left[j], p[j]);
   }
 }
 
-// One wave per block of kBlock elements, four of them per lane.
+// 8-bit states: a half wave per block of kBlock elements, eight a lane.
 template <typename P, typename G>
 __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, const float *clip) {
+  constexpr int N = kChunk / kThreads;
+  static_assert(N == 8 && kBlock == 32 * N, "a half wave holds a block");
+  const Entry &e = t.e[entry_of(t, blockIdx.x)];
+  const int64_t i = (blockIdx.x - e.chunk0) * kChunk + threadIdx.x * N, block = i / kBlock;
+  if (block * kBlock >= e.n) return;  // the whole half wave
+  const int left = (int)(e.n - i < 0 ? 0 : e.n - i < N ? e.n - i : N);
+  float p[N], g[N], m[N], v[N];
+  load_n<N>((const P *)e.p + i, left, p);
+  load_n<N>((const G *)e.g + i, left, g);
+  load_f8x8((const uint8_t *)e.m + i, left, m);
+  load_f8x8((const uint8_t *)e.v + i, left, v);
+  const float sm = e.ms[block], sv = e.vs[block];
   const float c = clip ? *clip : k.grad_scale;
   if (!(c == c)) return;
-  const Entry &e = t.e[entry_of(t, blockIdx.x)];
-  const int lane = threadIdx.x & 63;
-  for (int b = threadIdx.x >> 6; b < kChunk / kBlock; b += kThreads / 64) {
-    const int64_t block = (blockIdx.x - e.chunk0) * (kChunk / kBlock) + b;
-    const int64_t i0 = block * kBlock;
-    if (i0 >= e.n) return;
-    const float sm = e.ms[block], sv = e.vs[block];
-    float m[4], r[4], mtop = 0.f, rtop = 0.f;
+  float mtop = 0.f, rtop = 0.f;
+  uint32_t bits[N];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t i = i0 + 64 * j + lane;
-      m[j] = r[j] = 0.f;
-      if (i >= e.n) continue;
-      float p = load_f32((const P *)e.p, i);
-      const float root = f8_to_f32(((uint8_t *)e.v)[i]) * sv;
-      float v = root * root;
-      m[j] = f8_to_f32(((uint8_t *)e.m)[i]) * sm;
-      update(p, load_f32((const G *)e.g, i) * c, m[j], v, k, e.decay);
-      r[j] = sqrtf(v);
-      mtop = fmaxf(mtop, fabsf(m[j]));
-      rtop = fmaxf(rtop, r[j]);
-      if (sizeof(P) == 2 && k.stochastic) p = round_bf16(p, ((round_bits(e.base, i) >> 21) << 5) + 16);
-      store_f32((P *)e.p, i, p);
-      if (e.copy) e.copy[i] = f32_to_bf16_bits(p);
+  for (int q = 0; q < N; ++q) {
+    m[q] *= sm;
+    v[q] *= sv;
+    v[q] *= v[q];
+    v[q] = update(p[q], g[q] * c, m[q], v[q], k, e.decay);  // the root from here on
+    mtop = fmaxf(mtop, fabsf(m[q]));
+    rtop = fmaxf(rtop, v[q]);
+    if (k.stochastic) {
+      bits[q] = round_bits(e.base, i + q);
+      if (sizeof(P) == 2) p[q] = round_bf16(p[q], ((bits[q] >> 21) << 5) + 16);
     }
-    const float nsm = fmaxf(wave_max_f32(mtop) / kF8Max, kScaleMin);
-    const float nsv = fmaxf(wave_max_f32(rtop) / kF8Max, kScaleMin);
-    if (lane == 0) {
-      e.ms[block] = nsm;
-      e.vs[block] = nsv;
-    }
+  }
+  store_n<N>((P *)e.p + i, left, p);
+  if (e.copy) store_n<N>(e.copy + i, left, p);
+  const float nsm = fmaxf(half_wave_max(mtop) / kF8Max, kScaleMin);
+  const float nsv = fmaxf(half_wave_max(rtop) / kF8Max, kScaleMin);
+  const float im = 1.f / nsm, iv = 1.f / nsv;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t i = i0 + 64 * j + lane;
-      if (i >= e.n) continue;
-      float qm = clamp_f8(m[j] / nsm), qr = clamp_f8(r[j] / nsv);
-      if (k.stochastic) {
-        const uint32_t bits = round_bits(e.base, i);
-        qm = round_f8(qm, ((bits & 0x3ff) << 10) + 512);
-        qr = round_f8(qr, (((bits >> 10) & 0x7ff) << 9) + 256);
-      }
-      ((uint8_t *)e.m)[i] = f32_to_f8(qm);
-      ((uint8_t *)e.v)[i] = f32_to_f8(qr);
+  for (int q = 0; q < N; ++q) {
+    m[q] = clamp_f8(m[q] * im);
+    v[q] = fminf(v[q] * iv, kF8Max);
+  }
+  u32x2 qm, qv;
+  if (k.stochastic) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      int wm = 0, wv = 0;
+#define RVQ_RANDOM(B)                                                                       \
+  wm = random_f8<B>(m[4 * h + B], (bits[4 * h + B] << 22) | 0x200000u, wm);                 \
+  wv = random_f8<B>(v[4 * h + B], ((bits[4 * h + B] << 11) & 0xffe00000u) | 0x100000u, wv);
+      RVQ_RANDOM(0) RVQ_RANDOM(1) RVQ_RANDOM(2) RVQ_RANDOM(3)
+#undef RVQ_RANDOM
+      qm[h] = (uint32_t)wm;
+      qv[h] = (uint32_t)wv;
     }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      qm[h] = pack_f8x4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]);
+      qv[h] = pack_f8x4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+    }
+  }
+  store_8_bytes((uint8_t *)e.m + i, left, qm);
+  store_8_bytes((uint8_t *)e.v + i, left, qv);
+  if ((threadIdx.x & 31) == 0) {
+    e.ms[block] = nsm;
+    e.vs[block] = nsv;
   }
 }
 
@@ -269,7 +348,7 @@ hipError_t launch_adamw(const rvq_adamw_tensor *t, const AdamArgs &a, hipStream_
       }
 #undef RVQ_ADAM
     }
-    if (pass == 0) adamw_clip_kernel<<<1, kThreads, 0, s>>>(a.part, parts, k, a.clip, a.grad_norm);
+    if (pass == 0) adamw_clip_kernel<<<1, 1024, 0, s>>>(a.part, parts, k, a.clip, a.grad_norm);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

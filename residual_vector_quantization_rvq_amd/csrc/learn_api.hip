@@ -214,8 +214,8 @@ rvq_status rvq_adamw_step(const rvq_adamw_tensor *tensors, int32_t count, rvq_dt
   if (!(o.lr >= 0.0) || !std::isfinite(o.lr) || !(o.beta1 >= 0.0 && o.beta1 < 1.0) ||
       !(o.beta2 >= 0.0 && o.beta2 < 1.0))
     return fail(RVQ_ERR_INVALID_ARGUMENT, "need a finite lr >= 0 and beta1, beta2 in [0, 1)");
-  if (!(o.eps >= 1e-30) || !std::isfinite(o.eps))
-    return fail(RVQ_ERR_INVALID_ARGUMENT, "eps must be finite and at least 1e-30 (got %g)", o.eps);
+  if (!(o.eps >= 1e-12) || !std::isfinite(o.eps))
+    return fail(RVQ_ERR_INVALID_ARGUMENT, "eps must be finite and at least 1e-12 (got %g)", o.eps);
   if (o.step < 1)
     return fail(RVQ_ERR_INVALID_ARGUMENT, "step must be >= 1 (got %lld)", (long long)o.step);
   if (!std::isfinite(o.grad_scale) || !std::isfinite(o.max_norm))
