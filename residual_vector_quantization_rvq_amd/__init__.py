@@ -21,6 +21,7 @@ Learning the token embedding:
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import re
 from typing import NamedTuple, Optional, Sequence, Tuple
@@ -112,6 +113,9 @@ _lib.rvq_rms_norm_backward.argtypes = [_p, _p, ctypes.c_int, _i64, _i32, _p, _p,
 _lib.rvq_embed_tokens_backward_workspace_size.argtypes = [_i64, _i32, _i32, _i64, _i32, _psz]
 _lib.rvq_embed_tokens_backward.argtypes = [_p, ctypes.c_int, _p, _p, _i64, _i32, _i32, _i64, _i32,
                                            _p, _p, ctypes.c_int, _i32, _p, _p, _sz, _p]
+
+
+_DTYPE = operator.attrgetter("dtype")
 
 
 class _AdamWTensor(ctypes.Structure):
@@ -364,8 +368,20 @@ def _on_device(dev: torch.device, call, *args) -> None:
             _check(call(*args))
 
 
+def _raw_stream(dev: torch.device) -> int:
+    """The current stream's handle (_stream without the stream object, 2 us of a short call)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _address(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+def _need_like(name: str, t: torch.Tensor, x: torch.Tensor) -> None:
+    """t has x's shape, type and device and is contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is x.dtype and t.shape == x.shape and
+            t.device == x.device and t.is_contiguous()):
+        _need_shape(name, t, tuple(x.shape), x.dtype, x.device)
 
 
 def _need_workspace(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device) -> torch.Tensor:
@@ -411,11 +427,11 @@ def rvq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
     n, d = x.shape
     code = _dtype_code(x.dtype)
     if residual is not None:
-        _need_shape("residual", residual, (n, d), x.dtype, dev)
-        if sum_out is None:
-            sum_out = torch.empty_like(x)
+        _need_like("residual", residual, x)
     if sum_out is not None:
-        _need_shape("sum_out", sum_out, (n, d), x.dtype, dev)
+        _need_like("sum_out", sum_out, x)
+    elif residual is not None:
+        sum_out = torch.empty_like(x)
     wcode = _need_weight(weight, d, dev)
     odt = x.dtype if out_dtype is None else out_dtype
     f8 = odt == torch.float8_e4m3fn
@@ -428,7 +444,7 @@ def rvq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
     rstd = torch.empty(n, dtype=torch.float32, device=dev) if need_rstd else None
     _on_device(dev, _lib.rvq_rms_norm, x.data_ptr(), _address(residual), code, n, d,
                _address(weight), wcode, eps, _address(sum_out), out.data_ptr(), ocode,
-               _address(scale), _address(rstd), _stream(dev))
+               _address(scale), _address(rstd), _raw_stream(dev))
     return RMSNormResult(out, scale, sum_out, rstd)
 
 
@@ -454,15 +470,15 @@ def rvq_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
         raise ValueError("dy must be [n, d]")
     n, d = dy.shape
     code = _dtype_code(dy.dtype)
-    _need_shape("h", h, (n, d), dy.dtype, dev)
+    _need_like("h", h, dy)
     _need_shape("rstd", rstd, (n,), torch.float32, dev)
     if dsum is not None:
-        _need_shape("dsum", dsum, (n, d), dy.dtype, dev)
+        _need_like("dsum", dsum, dy)
     wcode = _need_weight(weight, d, dev)
     if out is None:
         out = torch.empty_like(dy)
     else:
-        _need_shape("out", out, (n, d), dy.dtype, dev)
+        _need_like("out", out, dy)
     dweight, ws, nbytes = None, None, 0
     if need_dweight:
         dweight = torch.empty(d, dtype=torch.float32, device=dev)
@@ -470,7 +486,7 @@ def rvq_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
         nbytes = ws.numel()
     _on_device(dev, _lib.rvq_rms_norm_backward, dy.data_ptr(), h.data_ptr(), code, n, d,
                rstd.data_ptr(), _address(weight), wcode, _address(dsum), out.data_ptr(),
-               _address(dweight), _address(ws), nbytes, _stream(dev))
+               _address(dweight), _address(ws), nbytes, _raw_stream(dev))
     return out, dweight
 
 
@@ -527,7 +543,7 @@ def rvq_embed_tokens_backward(dout: torch.Tensor, ids: torch.Tensor, K: int,
     level_out, text_out = level_grad if need_level else None, text_grad if need_text else None
     _on_device(dev, _lib.rvq_embed_tokens_backward, dout.data_ptr(), code, ids.data_ptr(),
                _address(is_visual), T, L, K, V, D, _address(level_out), _address(text_out), gcode,
-               1 if accumulate else 0, _address(bad_ids), ws.data_ptr(), ws.numel(), _stream(dev))
+               1 if accumulate else 0, _address(bad_ids), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     return level_out, text_out
 
 
@@ -537,12 +553,14 @@ class AdamWState:
     None.  Holds references to the tensors, not copies of them."""
 
     def __init__(self, params, state_bits, weight_decay, copies, m, v, m_scale, v_scale):
+        import numpy as np
         self.params, self.state_bits, self.copies = params, state_bits, copies
         self.m, self.v, self.m_scale, self.v_scale = m, v, m_scale, v_scale
         self.device = params[0].device
         self.param_dtype = params[0].dtype
         self._numels = [p.numel() for p in params]
         self._table = (_AdamWTensor * len(params))()
+        self._grads = np.frombuffer(self._table, np.uint64).reshape(len(params), -1)[:, 1]
         none = [None] * len(params)
         for t, p, a, b, sa, sb, c, w in zip(self._table, params, m, v, m_scale or none,
                                             v_scale or none, copies or none, weight_decay):
@@ -633,16 +651,18 @@ def rvq_adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: int, 
     bf16 parameters at random (needed for 8-bit states in training), from
     bits of (seed, step, tensor, element); None rounds to nearest."""
     dev, table = state.device, state._table
+    grads = list(grads)
     if len(grads) != len(table):
         raise ValueError(f"{len(table)} gradients are wanted, one per parameter (got {len(grads)})")
     gdt = grads[0].dtype
     gcode = _dtype_code(gdt)
-    index = dev.index
-    for t, g, n in zip(table, grads, state._numels):
-        if g.dtype is not gdt or g.numel() != n or not g.is_contiguous() or g.get_device() != index:
-            raise ValueError(f"gradients must be contiguous {gdt} tensors on {dev} with their "
-                             f"parameters' sizes (got {g.dtype} {list(g.shape)} on {g.device})")
-        t.grad = g.data_ptr()
+    # whole-list checks: a step of many small tensors is bound by this function
+    if (set(map(_DTYPE, grads)) != {gdt} or list(map(torch.Tensor.numel, grads)) != state._numels or
+            not all(map(torch.Tensor.is_contiguous, grads)) or
+            set(map(torch.Tensor.get_device, grads)) != {dev.index}):
+        raise ValueError(f"gradients must be contiguous {gdt} tensors on {dev} with their parameters' sizes (got "
+                         + ", ".join(f"{g.dtype} {list(g.shape)} on {g.device}" for g in grads[:8]) + ")")
+    state._grads[:] = list(map(torch.Tensor.data_ptr, grads))
     norm, ws, nbytes = None, None, 0
     if max_norm is not None and not max_norm > 0:
         raise ValueError("max_norm must be positive")
@@ -654,7 +674,7 @@ def rvq_adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: int, 
                         0 if seed is None else seed & 0xFFFFFFFF)
     _on_device(dev, _lib.rvq_adamw_step, ctypes.addressof(table), len(table),
                _dtype_code(state.param_dtype), gcode, state.state_bits, ctypes.byref(opt),
-               _address(norm), ws, nbytes, _stream(dev))
+               _address(norm), ws, nbytes, _raw_stream(dev))
     return norm
 
 

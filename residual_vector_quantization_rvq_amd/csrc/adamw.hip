@@ -26,7 +26,8 @@ namespace rvq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTable = 40;          // tensors of one launch (kernel arguments: 4 KB)
+constexpr int kTable = 54;          // tensors of one launch, and of one launch of the norm:
+constexpr int kNormTable = 160;     // as many as 4 KB of kernel arguments hold
 constexpr int kChunk = 2048;        // elements of one workgroup; a multiple of kBlock
 constexpr int kBlock = 256;         // elements that share a scale
 constexpr int kNormGroups = 2048;   // partial sums of squares of one launch
@@ -38,20 +39,31 @@ struct Entry {
   float *ms, *vs;
   uint16_t *copy;
   int64_t n;
-  int64_t chunk0;   // first workgroup of this tensor
+  uint32_t chunk0;  // first workgroup of this tensor
   float decay;      // 1 - lr wd
-  uint32_t base;    // rounding bits: mixed from (seed, step, tensor)
 };
-struct Table {
-  Entry e[kTable];
+struct NormEntry {
+  const void *g;
+  int64_t n;
+  uint32_t chunk0;
+};
+template <typename E, int Size>
+struct TableOf {
+  E e[Size];
   int count;
-  int64_t chunks;
+  int first;        // place in the call of the first entry; an empty tensor has an entry too
+  uint32_t chunks;
 };
+using Table = TableOf<Entry, kTable>;
+using NormTable = TableOf<NormEntry, kNormTable>;
 struct Consts {
   float b1, c1, b2, c2;  // c = 1 - b, from the 64-bit b: 1.f - 0.999f is 1e-5 off
   float eps, lr1, rk2, grad_scale, max_norm;
+  uint32_t key;      // of the rounding bits: mixed from seed and step
   bool stochastic;
 };
+static_assert(sizeof(Table) + sizeof(Consts) + 16 <= 4096 && sizeof(NormTable) + 16 <= 4096,
+              "kernel arguments");
 
 // 32 bits mixed from 32: xor of the high half, odd multipliers from the
 // fractions of sqrt(2) and sqrt(3)
@@ -61,6 +73,9 @@ __host__ __device__ inline uint32_t mix(uint32_t x) {
   x ^= x >> 15;
   x *= 0x5DB3D743u;
   return x ^ (x >> 16);
+}
+__device__ __forceinline__ uint32_t tensor_bits(uint32_t key, int tensor) {
+  return mix(key + (uint32_t)tensor);
 }
 __device__ __forceinline__ uint32_t round_bits(uint32_t base, int64_t i) {
   return mix(base + (uint32_t)i * 0x9E3779B1u + (uint32_t)(i >> 32) * 0x3504F333u);
@@ -115,7 +130,8 @@ __device__ __forceinline__ void store_8_bytes(uint8_t *p, int left, u32x2 q) {
 }
 
 // the entry of a workgroup's chunk
-__device__ __forceinline__ int entry_of(const Table &t, int64_t chunk) {
+template <typename TableT>
+__device__ __forceinline__ int entry_of(const TableT &t, uint32_t chunk) {
   int lo = 0, hi = t.count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -140,14 +156,15 @@ __device__ __forceinline__ float update(float &p, float g, float &m, float &v, c
 // Sums of squares of the gradients: eight of a lane in fp32, the rest in fp64.
 // A workgroup takes consecutive chunks.
 template <typename G>
-__global__ __launch_bounds__(kThreads) void adamw_norm_kernel(Table t, double *part) {
+__global__ __launch_bounds__(kThreads) void adamw_norm_kernel(NormTable t, double *part) {
   __shared__ double red[kThreads / 64];
   double s = 0.0;
-  const int64_t c0 = t.chunks * blockIdx.x / gridDim.x, c1 = t.chunks * (blockIdx.x + 1) / gridDim.x;
-  int at = entry_of(t, c0);
+  const int64_t c0 = (int64_t)t.chunks * blockIdx.x / gridDim.x;
+  const int64_t c1 = (int64_t)t.chunks * (blockIdx.x + 1) / gridDim.x;
+  int at = entry_of(t, (uint32_t)c0);
   for (int64_t chunk = c0; chunk < c1; ++chunk) {
     while (at + 1 < t.count && t.e[at + 1].chunk0 <= chunk) ++at;
-    const Entry &e = t.e[at];
+    const NormEntry &e = t.e[at];
     const int64_t i = (chunk - e.chunk0) * kChunk + threadIdx.x * 8;
     if (i < e.n) {
       float g[8];
@@ -193,8 +210,9 @@ __global__ __launch_bounds__(1024) void adamw_clip_kernel(const double *part, in
 template <typename P, typename G>
 __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, const float *clip) {
   constexpr int N = 4, J = kChunk / (kThreads * N);
-  const Entry &e = t.e[entry_of(t, blockIdx.x)];
-  const int64_t i0 = (blockIdx.x - e.chunk0) * kChunk + threadIdx.x * N;
+  const int at = entry_of(t, blockIdx.x);
+  const Entry &e = t.e[at];
+  const int64_t i0 = (int64_t)(blockIdx.x - e.chunk0) * kChunk + threadIdx.x * N;
   float p[J][N], g[J][N], m[J][N], v[J][N];
   int left[J];
 #pragma unroll
@@ -208,6 +226,7 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, c
   }
   const float c = clip ? *clip : k.grad_scale;
   if (!(c == c)) return;
+  const uint32_t base = tensor_bits(k.key, t.first + at);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int64_t i = i0 + j * kThreads * N;
@@ -215,7 +234,7 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, c
     for (int q = 0; q < N; ++q) {
       update(p[j][q], g[j][q] * c, m[j][q], v[j][q], k, e.decay);
       if (sizeof(P) == 2 && k.stochastic)
-        p[j][q] = round_bf16(p[j][q], ((round_bits(e.base, i + q) >> 21) << 5) + 16);
+        p[j][q] = round_bf16(p[j][q], ((round_bits(base, i + q) >> 21) << 5) + 16);
     }
     store_n<N>((P *)e.p + i, left[j], p[j]);
     store_n<N>((float *)e.m + i, left[j], m[j]);
@@ -229,8 +248,9 @@ template <typename P, typename G>
 __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, const float *clip) {
   constexpr int N = kChunk / kThreads;
   static_assert(N == 8 && kBlock == 32 * N, "a half wave holds a block");
-  const Entry &e = t.e[entry_of(t, blockIdx.x)];
-  const int64_t i = (blockIdx.x - e.chunk0) * kChunk + threadIdx.x * N, block = i / kBlock;
+  const int at = entry_of(t, blockIdx.x);
+  const Entry &e = t.e[at];
+  const int64_t i = (int64_t)(blockIdx.x - e.chunk0) * kChunk + threadIdx.x * N, block = i / kBlock;
   if (block * kBlock >= e.n) return;  // the whole half wave
   const int left = (int)(e.n - i < 0 ? 0 : e.n - i < N ? e.n - i : N);
   float p[N], g[N], m[N], v[N];
@@ -241,6 +261,7 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, co
   const float sm = e.ms[block], sv = e.vs[block];
   const float c = clip ? *clip : k.grad_scale;
   if (!(c == c)) return;
+  const uint32_t base = tensor_bits(k.key, t.first + at);
   float mtop = 0.f, rtop = 0.f;
   uint32_t bits[N];
 #pragma unroll
@@ -252,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, co
     mtop = fmaxf(mtop, fabsf(m[q]));
     rtop = fmaxf(rtop, v[q]);
     if (k.stochastic) {
-      bits[q] = round_bits(e.base, i + q);
+      bits[q] = round_bits(base, i + q);
       if (sizeof(P) == 2) p[q] = round_bf16(p[q], ((bits[q] >> 21) << 5) + 16);
     }
   }
@@ -294,65 +315,87 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, co
   }
 }
 
-size_t adam_part_count(int count) { return (size_t)ceil_div(count > 0 ? count : 1, kTable) * kNormGroups; }
+// a launch of the norm takes kNormTable tensors, or fewer of over 2^34
+// elements together: no more launches than tensors
+size_t adam_part_count(int count) { return (size_t)(count > 0 ? count : 1) * kNormGroups; }
+
+namespace {
+
+// Consecutive tables of all tensors, one launch(table) each; of at most
+// kMaxChunks workgroups, the most that one tensor has (2^34 elements).
+constexpr int64_t kMaxChunks = (int64_t)1 << 23;
+template <typename TableT, typename Fill, typename Launch>
+void for_each_table(const rvq_adamw_tensor *t, int count, int size, Fill fill, Launch launch) {
+  for (int first = 0; first < count;) {
+    TableT tab;
+    tab.first = first;
+    int64_t chunks = 0;
+    int i = 0;
+    for (; i < size && first + i < count; ++i) {
+      const int64_t n = t[first + i].numel, more = ceil_div(n, kChunk);
+      if (i > 0 && chunks + more > kMaxChunks) break;
+      fill(tab.e[i], t[first + i]);
+      tab.e[i].n = n;
+      tab.e[i].chunk0 = (uint32_t)chunks;
+      chunks += more;
+    }
+    tab.count = i;
+    tab.chunks = (uint32_t)chunks;
+    first += i;
+    if (chunks > 0) launch(tab);
+  }
+}
+
+template <typename P, typename G>
+void launch_step(const rvq_adamw_tensor *t, const AdamArgs &a, const Consts &k, hipStream_t s) {
+  for_each_table<Table>(
+      t, a.count, kTable,
+      [&](Entry &e, const rvq_adamw_tensor &x) {
+        e.p = x.param;
+        e.g = x.grad;
+        e.m = x.m;
+        e.v = x.v;
+        e.ms = x.m_scale;
+        e.vs = x.v_scale;
+        e.copy = (uint16_t *)x.copy;
+        e.decay = (float)(1.0 - a.lr * (double)x.weight_decay);
+      },
+      [&](const Table &tab) {
+        if (a.eight)
+          adamw_8_kernel<P, G><<<dim3(tab.chunks), kThreads, 0, s>>>(tab, k, a.clip);
+        else
+          adamw_32_kernel<P, G><<<dim3(tab.chunks), kThreads, 0, s>>>(tab, k, a.clip);
+      });
+}
+
+template <typename G>
+int64_t launch_norm(const rvq_adamw_tensor *t, const AdamArgs &a, hipStream_t s) {
+  int64_t parts = 0;
+  for_each_table<NormTable>(
+      t, a.count, kNormTable, [&](NormEntry &e, const rvq_adamw_tensor &x) { e.g = x.grad; },
+      [&](const NormTable &tab) {
+        const unsigned groups = tab.chunks < (unsigned)kNormGroups ? tab.chunks : kNormGroups;
+        adamw_norm_kernel<G><<<dim3(groups), kThreads, 0, s>>>(tab, a.part + parts);
+        parts += groups;
+      });
+  return parts;
+}
+
+}  // namespace
 
 hipError_t launch_adamw(const rvq_adamw_tensor *t, const AdamArgs &a, hipStream_t s) {
-  const Consts k = {a.b1, a.c1, a.b2, a.c2, a.eps, a.lr1, a.rk2, a.grad_scale, a.max_norm, a.stochastic};
-  const bool norm = a.clip != nullptr;
-  int64_t parts = 0;
-  for (int pass = norm ? 0 : 1; pass < 2; ++pass) {
-    for (int first = 0; first < a.count;) {
-      Table tab;
-      tab.count = 0;
-      tab.chunks = 0;
-      int i = first;
-      for (; i < a.count && tab.count < kTable; ++i) {
-        if (t[i].numel == 0) continue;
-        Entry &e = tab.e[tab.count++];
-        e.p = t[i].param;
-        e.g = t[i].grad;
-        e.m = t[i].m;
-        e.v = t[i].v;
-        e.ms = t[i].m_scale;
-        e.vs = t[i].v_scale;
-        e.copy = (uint16_t *)t[i].copy;
-        e.n = t[i].numel;
-        e.chunk0 = tab.chunks;
-        e.decay = (float)(1.0 - a.lr * (double)t[i].weight_decay);
-        e.base = mix(a.key + (uint32_t)i);
-        tab.chunks += ceil_div(e.n, kChunk);
-      }
-      first = i;
-      if (tab.count == 0) continue;
-      if (pass == 0) {
-        const unsigned groups = (unsigned)(tab.chunks < kNormGroups ? tab.chunks : kNormGroups);
-        if (a.g_bf16)
-          adamw_norm_kernel<uint16_t><<<groups, kThreads, 0, s>>>(tab, a.part + parts);
-        else
-          adamw_norm_kernel<float><<<groups, kThreads, 0, s>>>(tab, a.part + parts);
-        parts += groups;
-        continue;
-      }
-      const dim3 grid((unsigned)tab.chunks);
-#define RVQ_ADAM(P, G)                                                      \
-  do {                                                                      \
-    if (a.eight)                                                            \
-      adamw_8_kernel<P, G><<<grid, kThreads, 0, s>>>(tab, k, a.clip);       \
-    else                                                                    \
-      adamw_32_kernel<P, G><<<grid, kThreads, 0, s>>>(tab, k, a.clip);      \
-  } while (0)
-      if (a.p_bf16) {
-        if (a.g_bf16) RVQ_ADAM(uint16_t, uint16_t); else RVQ_ADAM(uint16_t, float);
-      } else {
-        if (a.g_bf16) RVQ_ADAM(float, uint16_t); else RVQ_ADAM(float, float);
-      }
-#undef RVQ_ADAM
-    }
-    if (pass == 0) adamw_clip_kernel<<<1, 1024, 0, s>>>(a.part, parts, k, a.clip, a.grad_norm);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  const Consts k = {a.b1, a.c1, a.b2, a.c2, a.eps, a.lr1, a.rk2, a.grad_scale, a.max_norm, a.key,
+                    a.stochastic};
+  if (a.clip) {
+    const int64_t parts = a.g_bf16 ? launch_norm<uint16_t>(t, a, s) : launch_norm<float>(t, a, s);
+    adamw_clip_kernel<<<1, 1024, 0, s>>>(a.part, parts, k, a.clip, a.grad_norm);
   }
-  return hipSuccess;
+  if (a.p_bf16) {
+    if (a.g_bf16) launch_step<uint16_t, uint16_t>(t, a, k, s); else launch_step<uint16_t, float>(t, a, k, s);
+  } else {
+    if (a.g_bf16) launch_step<float, uint16_t>(t, a, k, s); else launch_step<float, float>(t, a, k, s);
+  }
+  return hipGetLastError();
 }
 
 uint32_t adam_key(uint32_t seed, uint32_t step) { return mix(seed ^ (step * 0x9E3779B1u)); }

@@ -82,6 +82,25 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 __device__ __forceinline__ u32x4 load16(const float *p) { return *(const u32x4_at4 *)p; }
 __device__ __forceinline__ u32x4 load16(const uint16_t *p) { return *(const u32x4_at2 *)p; }
 
+// A piece as it is stored; `left` (which may be negative) of its elements
+// exist, the others read as zero.
+__device__ __forceinline__ u32x4 load_piece(const float *p, int left) {
+  if (left >= 4) return load16(p);
+  u32x4 q = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 3; ++e)
+    if (e < left) q[e] = __float_as_uint(p[e]);
+  return q;
+}
+__device__ __forceinline__ u32x4 load_piece(const uint16_t *p, int left) {
+  if (left >= 8) return load16(p);
+  u32x4 q = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < left) q[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+  return q;
+}
+
 // N elements at p; `left` of them exist (the others read as zero)
 template <int N>
 __device__ __forceinline__ void load_n(const float *p, int left, float (&v)[N]) {

@@ -9,7 +9,7 @@
 // Bound by memory: a row is read once, held in registers for the sum and for
 // the products, and written once.  A row is shared by W lanes of P 16-byte
 // pieces each: a part of a wave for narrow rows (several rows a wave), a wave
-// up to 128 pieces, else a workgroup.  Rows of more than 2048 pieces (8192
+// up to 192 pieces, else a workgroup.  Rows of more than 2048 pieces (8192
 // fp32 or 16384 bf16 elements) are read again for each pass over them.
 #include "learn.h"
 
@@ -65,7 +65,7 @@ __device__ __forceinline__ void load_weight(const void *w, bool bf16, int c, int
 
 // how a row of `pieces` is shared: W lanes, P pieces each
 #define RVQ_NORM_SHAPES(X) \
-  X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(64, 2) X(256, 1) X(256, 2) X(256, 4) X(256, 8)
+  X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(64, 2) X(64, 3) X(256, 1) X(256, 2) X(256, 4) X(256, 8)
 struct Shape {
   int w, p;
 };
@@ -247,11 +247,15 @@ int64_t norm_grad_parts(int64_t n, int d, bool bf16) {
   const int64_t pieces = ceil_div(d, bf16 ? kPiece<uint16_t> : kPiece<float>);
   if (n == 0) return 1;
   if (!shape_of(pieces).w) return n < kWideParts ? n : kWideParts;
-  // four rows a workgroup's turn before there are as many as the device holds
-  const int64_t groups = ceil_div(n, 4 * rows_per_group(pieces));
+  // two rows in turn before there are as many workgroups as the device holds
+  const int64_t groups = ceil_div(n, 2 * rows_per_group(pieces));
   return groups < kMaxParts ? groups : kMaxParts;
 }
 
+// kMaxParts workgroups of four waves are as many as fit at once with 128
+// registers: a second round of fewer would cost as much as the first.  All of
+// a row's loads are issued before its sum; more waves hide the rest (holding
+// the next row too was 2% slower).
 template <typename T, int W, int P, bool DW>
 __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a) {
   constexpr int N = kPiece<T>, R = kThreads / W;
@@ -265,19 +269,21 @@ __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a)
   for (int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / W; row < a.n; row += (int64_t)gridDim.x * R) {
     const int64_t at = row * a.d;
     const float r = a.rstd[row];
-    float g[P][N], u[P][N];
-    float dot = 0.f;
+    u32x4 q[P][3];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = (p * W + lane) * N;
-      if (c < a.d) {
-        load_n<N>((const T *)a.dy + at + c, a.d - c, g[p]);
-        load_n<N>((const T *)a.h + at + c, a.d - c, u[p]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) g[p][e] = u[p][e] = 0.f;
-      }
+      q[p][0] = load_piece((const T *)a.dy + at + c, a.d - c);
+      q[p][1] = load_piece((const T *)a.h + at + c, a.d - c);
+      if (a.dsum) q[p][2] = load_piece((const T *)a.dsum + at + c, a.d - c);
     }
+    float g[P][N], u[P][N];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      unpack(q[p][0], g[p]);
+      unpack(q[p][1], u[p]);
+    }
+    float dot = 0.f;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = (p * W + lane) * N;
@@ -298,9 +304,12 @@ __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a)
       const int c = (p * W + lane) * N;
       if (c >= a.d) continue;
       float v[N];
+      if (a.dsum) {
+        unpack(q[p][2], v);
+      } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = 0.f;
-      if (a.dsum) load_n<N>((const T *)a.dsum + at + c, a.d - c, v);
+        for (int e = 0; e < N; ++e) v[e] = 0.f;
+      }
 #pragma unroll
       for (int e = 0; e < N; ++e) v[e] += r * (g[p][e] - u[p][e] * mean);
       // dx may be dy or dsum itself: both were loaded by this lane
@@ -373,8 +382,11 @@ __global__ __launch_bounds__(1024) void rms_norm_dweight_join_kernel(const float
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
   float s = 0.f;
-  if (c < d)
-    for (int64_t p = parts * wave / 16; p < parts * (wave + 1) / 16; ++p) s += part[p * d + c];
+  if (c < d) {
+    const int p1 = (int)(parts * (wave + 1) / 16);
+#pragma unroll 8
+    for (int p = (int)(parts * wave / 16); p < p1; ++p) s += part[(int64_t)p * d + c];
+  }
   sums[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < d) {
