@@ -26,8 +26,10 @@ namespace {
 constexpr int kRange = 512;        // destination rows of one index workgroup
 constexpr int kBatch = 8;          // loads in flight: ID batches of a wave, rows of a sum
 constexpr int kFlight = 4;         // rows of dout in flight while as many are added
+constexpr int64_t kPanelBytes = (int64_t)100 << 20;
 constexpr int kKeysFrom = 2048;   // tokens
 constexpr int kFewTokens = 8192;  // up to here four waves an index workgroup, else sixteen
+constexpr int kFewHits = 12;       // of a wave's 64 IDs: rows told apart one by one, else bit by bit
 constexpr int kNone = INT32_MIN;   // not an ID of this table
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 1 << 22;
@@ -127,9 +129,9 @@ __global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, T
     for (int u = 0; u < kBatch; ++u) id[u] = mine[u] ? id[u] : kNone;
   };
 
+  int id[kBatch];
   int below = 0, bad = 0;
   for (int64_t tw = t0; tw < t1; tw += kBatch * 64) {
-    int id[kBatch];
     load_ids(tw, id);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -180,8 +182,7 @@ __global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, T
 #pragma unroll
     for (int j = 0; j < RP; ++j) {
       if (r0 + r + j < r1) {
-        a.start[row0 + r + j] = at;
-        a.count[row0 + r + j] = mine[j];
+        a.place[row0 + r + j] = make_int2(at, mine[j]);
       }
 #pragma unroll
       for (int w = 0; w < kIndexWaves; ++w) {
@@ -197,18 +198,28 @@ __global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, T
     for (int64_t i = total + (int64_t)threadIdx.x; i < region + tb.T; i += kIndexThreads) a.row[i] = -1;
 
   for (int64_t tw = t0; tw < t1; tw += kBatch * 64) {
-    int id[kBatch];
     load_ids(tw, id);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const bool hit = id[u] >= r0 && id[u] < r1;
-      unsigned long long same = __ballot(hit);  // then: lanes of the same row
-      if (same == 0) continue;
+      const unsigned long long hits = __ballot(hit);
+      if (hits == 0) continue;
       const int k = hit ? id[u] - r0 : 0;
+      unsigned long long same = 0;  // lanes of the same row
+      if (__popcll(hits) <= kFewHits) {  // row by row
+        for (unsigned long long rest = hits; rest;) {
+          const int of = __builtin_amdgcn_readlane(k, __ffsll((long long)rest) - 1);
+          const unsigned long long m = __ballot(hit && k == of);
+          if (k == of) same = m;
+          rest &= ~m;
+        }
+      } else {  // bit by bit
+        same = hits;
 #pragma unroll
-      for (int b = 0; (1 << b) < kRange; ++b) {
-        const unsigned long long m = __ballot((k >> b) & 1);
-        same &= ((k >> b) & 1) ? m : ~m;
+        for (int b = 0; (1 << b) < kRange; ++b) {
+          const unsigned long long m = __ballot((k >> b) & 1);
+          same &= ((k >> b) & 1) ? m : ~m;
+        }
       }
       const int first = hit ? __ffsll((long long)same) - 1 : lane;
       int at = 0;
@@ -225,55 +236,73 @@ __global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, T
 
 namespace {
 
-// A lane's 16-byte piece of the rows: where it is read, and which of its
-// elements are the lane's to write.  A row that ends inside the piece is read
-// from N elements before its end on, so that every load is whole; rows of
-// fewer than N elements (TINY) are read by elements.
-template <typename T, bool TINY>
+// A lane's 16 bytes of a slab of W lanes: where they are read, and which of
+// their elements are the lane's to write.  Where the gradients are wider than
+// dout, the lane has 8 bytes in either half of the slab, so that its stores of
+// 16 bytes still join into whole lines (fp32 rows out of bf16 stored 32 bytes
+// a lane went out at half the rate).  A row that ends inside a part is read
+// from the part's length before its end on, so that every load is whole; rows
+// narrower than a part (TINY) are read by elements.
+template <typename T, typename G, int W, bool TINY>
 struct Piece {
-  static constexpr int N = kPiece<T>;
-  uint32_t at;      // byte offset of the first element read
-  int first, last;  // elements [first, last) are written; none where the lane is past the row
+  static constexpr int N = kPiece<T>, H = sizeof(G) > sizeof(T) ? 2 : 1, M = N / H;
+  int at[H];                  // first element read
+  int8_t first[H], last[H];   // elements [first, last) of the part are written
 
-  __device__ __forceinline__ Piece(int c, int D) {
-    const int left = D - c;
-    const int from = TINY || left >= N ? c : D - N;
-    at = left > 0 ? (uint32_t)from * (uint32_t)sizeof(T) : 0;
-    first = left > 0 ? c - from : 0;
-    last = left <= 0 ? 0 : TINY && left < N ? left : N;
-  }
-  __device__ __forceinline__ u32x4 load(const T *row) const {
-    const T *x = (const T *)((const char *)row + at);
-    if constexpr (!TINY) {
-      return load16(x);
-    } else {
-      u32x4 q = {0, 0, 0, 0};
-      for (int j = 0; j < last; ++j) {
-        if constexpr (sizeof(T) == 4)
-          q[j] = __float_as_uint(x[j]);
-        else
-          q[j / 2] |= (uint32_t)x[j] << (16 * (j & 1));
-      }
-      return q;
+  __device__ __forceinline__ Piece(int slab, int lane, int D) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int c = slab * W * N + (h * W + lane) * M, left = D - c;
+      const int from = TINY || left >= M ? c : D - M;
+      at[h] = left > 0 ? from : 0;
+      first[h] = (int8_t)(left > 0 ? c - from : 0);
+      last[h] = (int8_t)(left <= 0 ? 0 : TINY && left < M ? left : M);
     }
   }
-  // o: where element 0 of the piece goes
-  template <typename G>
-  __device__ __forceinline__ void store(G *o, const float (&s)[N], bool accumulate) const {
-    if (first == 0 && last == N) {
-      if (!accumulate) {
-        store_n<N>(o, N, s);
-        return;
-      }
-      float v[N];
-      load_n<N>(o, N, v);
+  __device__ __forceinline__ u32x4 load(const T *row) const {
+    u32x4 q = {0, 0, 0, 0};
+    if constexpr (TINY) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] += s[j];
-      store_n<N>(o, N, v);
+      for (int h = 0; h < H; ++h)
+        for (int j = 0; j < last[h]; ++j) {
+          if constexpr (sizeof(T) == 4)
+            q[j] = __float_as_uint(row[at[h] + j]);
+          else
+            q[(h * M + j) / 2] |= (uint32_t)row[at[h] + j] << (16 * (j & 1));
+        }
+    } else if constexpr (H == 1) {
+      q = load16((const T *)((const char *)row + (uint32_t)at[0] * (uint32_t)sizeof(T)));
     } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (j >= first && j < last) store_f32(o, j, accumulate ? s[j] + load_f32(o, j) : s[j]);
+      for (int h = 0; h < 2; ++h) {
+        const u32x2 w = *(const u32x2_at2 *)((const char *)row + (uint32_t)at[h] * (uint32_t)sizeof(T));
+        q[2 * h] = w[0];
+        q[2 * h + 1] = w[1];
+      }
+    }
+    return q;
+  }
+  template <typename O>
+  __device__ __forceinline__ void store(O *row, const float (&s)[N], bool accumulate) const {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      O *o = row + at[h];
+      float v[M];
+#pragma unroll
+      for (int j = 0; j < M; ++j) v[j] = s[h * M + j];
+      if (first[h] == 0 && last[h] == M) {
+        if (accumulate) {
+          float w[M];
+          load_n<M>(o, M, w);
+#pragma unroll
+          for (int j = 0; j < M; ++j) v[j] += w[j];
+        }
+        stream_n<M>(o, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+          if (j >= first[h] && j < last[h]) store_f32(o, j, accumulate ? v[j] + load_f32(o, j) : v[j]);
+      }
     }
   }
 };
@@ -297,7 +326,7 @@ __device__ __forceinline__ G *row_of(const EmbedGradArgs &a, const Tables &tb, i
 // it (part[2 s + 1]).
 template <typename T, typename G, int W, bool TINY>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Tables tb, int R,
-                                                             int slabs) {
+                                                             int slabs, int panel) {
   constexpr int N = kPiece<T>;
   const int lane = threadIdx.x % W;
   // lane j's value, j the same for the W lanes
@@ -314,10 +343,12 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Ta
   if constexpr (W == 64)  // the same for the wave
     v = (int64_t)blockIdx.x * (kThreads / W) + __builtin_amdgcn_readfirstlane(threadIdx.x / W);
   for (; v < units * slabs; v += (int64_t)gridDim.x * (kThreads / W)) {
-    const int64_t u = v / slabs;
-    const int c = ((int)(v - u * slabs) * W + lane) * N;
-    const Piece<T, TINY> piece(c, a.D);
-    const bool mine = c < a.D;
+    // panel by panel of the slabs; in a panel a row group's slabs in turn
+    const int64_t at = v / (units * panel) * panel;
+    const int wide = slabs - at < panel ? (int)(slabs - at) : panel;
+    const int64_t u = (v - at * units) / wide;
+    const int slab = (int)(at + (v - at * units) - u * wide);
+    const Piece<T, G, W, TINY> piece(slab, lane, a.D);
     float s[N];
     int counts = 0, starts = 0, rows = 1;
     G *o = nullptr;         // the row that is being summed
@@ -326,8 +357,8 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Ta
       const int64_t p0 = (u >> 1) * tb.seg;
       const int64_t p1 = p0 + tb.seg < tb.positions ? p0 + tb.seg : tb.positions;
       const int ra = a.row[p0], row = u & 1 ? a.row[p1 - 1] : ra;
-      if (row < 0 || (u & 1 && row == ra) || a.count[row] <= tb.seg) continue;
-      const int64_t b = a.start[row], e = b + a.count[row];
+      if (row < 0 || (u & 1 && row == ra) || a.place[row].y <= tb.seg) continue;
+      const int64_t b = a.place[row].x, e = b + a.place[row].y;
       starts = (int)(b > p0 ? b : p0);
       counts = (int)(e < p1 ? e : p1) - starts;
       part = a.part + u * a.D;
@@ -341,16 +372,17 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Ta
       rows = (int)(limit - r0 < R ? limit - r0 : R);
       const int64_t row0 = (int64_t)l * tb.K + r0;
       if (lane < rows) {
-        counts = a.count[row0 + lane];
-        starts = a.start[row0 + lane];
+        const int2 at = a.place[row0 + lane];
+        starts = at.x;
+        counts = at.y;
       }
       o = row_of<G>(a, tb, row0);
     }
     const auto store = [&](int n) {
-      if (mine && part)
-        piece.store(part + piece.at / sizeof(T), s, false);
-      else if (mine && !(a.accumulate && n == 0))
-        piece.store(o + piece.at / sizeof(T), s, a.accumulate);
+      if (part)
+        piece.store(part, s, false);
+      else if (!(a.accumulate && n == 0))
+        piece.store(o, s, a.accumulate);
       o += a.D;
 #pragma unroll
       for (int j = 0; j < N; ++j) s[j] = 0.f;
@@ -426,9 +458,9 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a, T
   const int64_t s = blockIdx.x;
   const int64_t p0 = s * tb.seg, p1 = p0 + tb.seg < tb.positions ? p0 + tb.seg : tb.positions;
   const int row = a.row[p1 - 1];
-  if (row < 0 || a.count[row] <= tb.seg || a.start[row] < p0) return;
-  const int64_t end = (int64_t)a.start[row] + a.count[row];
-  const int64_t first = a.start[row] == p0 ? 2 * s : 2 * s + 1;
+  if (row < 0 || a.place[row].y <= tb.seg || a.place[row].x < p0) return;
+  const int64_t end = (int64_t)a.place[row].x + a.place[row].y;
+  const int64_t first = a.place[row].x == p0 ? 2 * s : 2 * s + 1;
   G *o = row_of<G>(a, tb, row);
   const int c = blockIdx.y * kThreads + threadIdx.x;
   if (c >= a.D) return;
@@ -441,9 +473,8 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a, T
 EmbedGradLayout embed_grad_layout(int64_t T, int L, int K, int64_t V, int D) {
   const Tables tb = tables_of(T, L, K, V);
   EmbedGradLayout w;
-  w.start = 0;
-  w.count = w.start + al256((size_t)tb.rows * 4);
-  w.token = w.count + al256((size_t)tb.rows * 4);
+  w.place = 0;
+  w.token = w.place + al256((size_t)tb.rows * sizeof(int2));
   w.row = w.token + al256((size_t)tb.positions * 4);
   w.part = w.row + al256((size_t)tb.positions * 4);
   w.keys = w.part + al256((size_t)tb.segments * 2 * D * sizeof(float));
@@ -460,12 +491,14 @@ static hipError_t launch_sums(const EmbedGradArgs &a, const Tables &tb, hipStrea
 #define RVQ_SUM(W, TINY)                                                                        \
   do {                                                                                      \
     const int64_t slabs = ceil_div(pieces, W);                                              \
+    const int64_t panels = ceil_div(a.T * a.D * (int64_t)sizeof(T), kPanelBytes);           \
+    const int64_t panel = panels > 1 ? ceil_div(slabs, panels) : slabs;                     \
     int64_t R = tb.rows * slabs / (65536 * (64 / W));                                       \
     R = R < 1 ? 1 : R > W ? W : R;                                                          \
     const int64_t units = 2 * tb.segments + tb.L * ceil_div(tb.K, R) + ceil_div(tb.V, R);   \
     const int64_t groups = ceil_div(units * slabs, kThreads / W);                           \
     embed_sum_kernel<T, G, W, TINY><<<dim3((unsigned)(groups < kMaxGroups ? groups : kMaxGroups)), \
-                                kThreads, 0, s>>>(a, tb, (int)R, (int)slabs);               \
+                                kThreads, 0, s>>>(a, tb, (int)R, (int)slabs, (int)panel);   \
   } while (0)
   if (a.D < kPiece<T>) RVQ_SUM(8, true); else if (pieces <= 8) RVQ_SUM(8, false);
   else if (pieces <= 16) RVQ_SUM(16, false); else if (pieces <= 32) RVQ_SUM(32, false);

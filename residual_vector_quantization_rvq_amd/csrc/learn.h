@@ -165,6 +165,27 @@ __device__ __forceinline__ void store_n(uint16_t *p, int left, const float (&v)[
       if (e < left) p[e] = f32_to_bf16_bits(v[e]);
   }
 }
+// the same, for what is not read again soon: kept out of the caches' way
+template <int N>
+__device__ __forceinline__ void stream_n(float *p, const float (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    const u32x4 q = {__float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
+                     __float_as_uint(v[j + 3])};
+    __builtin_nontemporal_store(q, (u32x4_at4 *)(p + j));
+  }
+}
+template <int N>
+__device__ __forceinline__ void stream_n(uint16_t *p, const float (&v)[N]) {
+  if constexpr (N == 8) {
+    const u32x4 q = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                     pack_bf16x2(v[6], v[7])};
+    __builtin_nontemporal_store(q, (u32x4_at2 *)p);
+  } else {
+    const u32x2 q = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    __builtin_nontemporal_store(q, (u32x2_at2 *)p);
+  }
+}
 // e4m3 bytes of values within +-448
 template <int N>
 __device__ __forceinline__ void store_f8_n(uint8_t *p, int left, const float (&v)[N]) {
@@ -227,13 +248,13 @@ struct EmbedGradArgs {
   bool accumulate;
   uint32_t *bad;
   // workspace
-  int32_t *start, *count;     // [rows]: each destination row's piece of the list
+  int2 *place;                // [rows]: where a destination row's tokens begin in the list, and how many
   int32_t *token, *row;       // the list: tokens by destination row, in token order; its row
   float *part;                // [2 segments][D]: sums of the pieces of long rows
   int32_t *keys;              // [tables][T]: the IDs by table
 };
 struct EmbedGradLayout {
-  size_t start, count, token, row, part, keys, total;
+  size_t place, token, row, part, keys, total;
 };
 EmbedGradLayout embed_grad_layout(int64_t T, int L, int K, int64_t V, int D);
 hipError_t launch_embed_grad(const EmbedGradArgs &a, bool x_bf16, bool g_bf16, hipStream_t s);

@@ -183,7 +183,7 @@ rvq_status rvq_embed_tokens_backward(const void *dout, rvq_dtype dout_dtype, con
   const EmbedGradLayout w = embed_grad_layout(T, dlevel ? L : 0, K, dtext ? V : 0, D);
   char *ws = (char *)workspace;
   EmbedGradArgs a = {dout, ids, is_visual, T, L, K, D, V, dlevel, dtext, accumulate != 0, bad_ids,
-                     (int32_t *)(ws + w.start), (int32_t *)(ws + w.count),
+                     (int2 *)(ws + w.place),
                      (int32_t *)(ws + w.token), (int32_t *)(ws + w.row), (float *)(ws + w.part),
                      (int32_t *)(ws + w.keys)};
   return launched(launch_embed_grad(a, dout_dtype == RVQ_BF16, grad_dtype == RVQ_BF16, stream),
