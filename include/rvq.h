@@ -370,7 +370,7 @@ rvq_status rvq_embed_tokens_backward_workspace_size(int64_t T, int32_t L, int32_
  * bad_ids      : device uint32 counter (added to): out-of-range IDs, each
  *                once, of the tables whose gradient is asked for; or NULL.
  *                Such an ID adds to no row.
- * Limits: L <= 64, D <= 2^20, T <= 2^25, T (L + 1) < 2^31, L K + V <= 2^28.
+ * Limits: L <= 64, D <= 2^20, T <= 2^25, T (L + 1) <= 2^30, L K + V <= 2^28.
  */
 rvq_status rvq_embed_tokens_backward(const void *dout, rvq_dtype dout_dtype, const int32_t *ids,
                                      const uint8_t *is_visual, int64_t T, int32_t L, int32_t K,

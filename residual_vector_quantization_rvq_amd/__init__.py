@@ -549,13 +549,20 @@ def rvq_embed_tokens_backward(dout: torch.Tensor, ids: torch.Tensor, K: int,
 
 class AdamWState:
     """Parameters of one type and their AdamW state (see rvq_adamw_init):
-    lists params, m, v and, with 8-bit states, m_scale, v_scale; copies or
-    None.  Holds references to the tensors, not copies of them."""
+    tuples params, m, v and, with 8-bit states, m_scale, v_scale; copies or
+    None.  Bound to these tensors' memory (which it keeps alive) and no copy of
+    it: to load a state, copy into them or make a new AdamWState."""
 
     def __init__(self, params, state_bits, weight_decay, copies, m, v, m_scale, v_scale):
         import numpy as np
-        self.params, self.state_bits, self.copies = params, state_bits, copies
-        self.m, self.v, self.m_scale, self.v_scale = m, v, m_scale, v_scale
+        def fixed(ts):
+            return None if ts is None else tuple(ts)
+        params = fixed(params)
+        self.params, self.state_bits, self.copies = params, state_bits, fixed(copies)
+        self.m, self.v, self.m_scale, self.v_scale = fixed(m), fixed(v), fixed(m_scale), fixed(v_scale)
+        self._memory = [t.untyped_storage() for ts in (params, self.m, self.v, self.m_scale, self.v_scale,
+                                                       self.copies) if ts for t in ts]
+        self._addresses = [p.data_ptr() for p in params]
         self.device = params[0].device
         self.param_dtype = params[0].dtype
         self._numels = [p.numel() for p in params]
@@ -662,6 +669,8 @@ def rvq_adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: int, 
             set(map(torch.Tensor.get_device, grads)) != {dev.index}):
         raise ValueError(f"gradients must be contiguous {gdt} tensors on {dev} with their parameters' sizes (got "
                          + ", ".join(f"{g.dtype} {list(g.shape)} on {g.device}" for g in grads[:8]) + ")")
+    if list(map(torch.Tensor.data_ptr, state.params)) != state._addresses:
+        raise ValueError("a parameter's memory is no longer the one that rvq_adamw_init was given")
     state._grads[:] = list(map(torch.Tensor.data_ptr, grads))
     norm, ws, nbytes = None, None, 0
     if max_norm is not None and not max_norm > 0:

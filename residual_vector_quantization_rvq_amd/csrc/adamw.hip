@@ -89,6 +89,11 @@ template <int Byte>
 __device__ __forceinline__ int random_f8(float v, uint32_t random, int w) {
   return __builtin_amdgcn_cvt_sr_fp8_f32(v, (int)random, w, Byte);
 }
+// the largest magnitude divided by its 448th may come out a unit above 448; a
+// NaN stays one
+__device__ __forceinline__ float at_most_448(float v) {
+  return fabsf(v) > kF8Max ? copysignf(kF8Max, v) : v;
+}
 __device__ __forceinline__ float round_bf16(float v, uint32_t random16) {
   return __uint_as_float((__float_as_uint(v) + random16) & 0xffff0000u);
 }
@@ -115,10 +120,12 @@ __device__ __forceinline__ void load_f8x8(const uint8_t *p, int left, float (&v)
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    v[4 * j] = __builtin_amdgcn_cvt_f32_fp8((int)q[j], 0);
-    v[4 * j + 1] = __builtin_amdgcn_cvt_f32_fp8((int)q[j], 1);
-    v[4 * j + 2] = __builtin_amdgcn_cvt_f32_fp8((int)q[j], 2);
-    v[4 * j + 3] = __builtin_amdgcn_cvt_f32_fp8((int)q[j], 3);
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[j], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[j], true);
+    v[4 * j] = lo[0];
+    v[4 * j + 1] = lo[1];
+    v[4 * j + 2] = hi[0];
+    v[4 * j + 3] = hi[1];
   }
 }
 __device__ __forceinline__ void store_8_bytes(uint8_t *p, int left, u32x2 q) {
@@ -140,15 +147,31 @@ __device__ __forceinline__ int entry_of(const TableT &t, uint32_t chunk) {
   return lo;
 }
 
-// Root and quotient are the hardware's (one unit in the last place): they act
-// on lr times the update alone.  Returns sqrt(v).
-__device__ __forceinline__ float update(float &p, float g, float &m, float &v, const Consts &k,
-                                        float decay) {
+// m and v with every operation rounded by itself, in the order of the formula
+// above: a stored 8-bit moment turns on the last place of what is rounded.
+__device__ __forceinline__ void moments(float g, float &m, float &v, const Consts &k) {
+#pragma clang fp contract(off)
   m = k.b1 * m + k.c1 * g;
   v = k.b2 * v + k.c2 * (g * g);
-  const float root = __builtin_amdgcn_sqrtf(v);
-  p = p * decay - k.lr1 * m * __builtin_amdgcn_rcpf(root * k.rk2 + k.eps);
-  return root;
+}
+
+// Root and quotient are the hardware's (one unit in the last place): they act
+// on lr times the update alone.
+__device__ __forceinline__ float updated(float p, float m, float root, const Consts &k, float decay) {
+  return p * decay - k.lr1 * m * __builtin_amdgcn_rcpf(root * k.rk2 + k.eps);
+}
+
+// The nearest fp32 to sqrt(v), by one Newton step from the hardware's 1 /
+// sqrt(v); roots under 2^-60 are taken for zero (eps is at least 1e-12).
+__device__ __forceinline__ float nearest_sqrt(float v) {
+  const float y = __builtin_amdgcn_rsqf(v), s = v * y;
+  const float r = __builtin_fmaf(-s, s, v);
+  return v > 0x1p-120f ? __builtin_fmaf(r, 0.5f * y, s) : 0.f;
+}
+// the nearest fp32 to x / d, inv the nearest to 1 / d
+__device__ __forceinline__ float nearest_quotient(float x, float d, float inv) {
+  const float q = x * inv;
+  return __builtin_fmaf(__builtin_fmaf(-q, d, x), inv, q);
 }
 
 }  // namespace
@@ -232,7 +255,8 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, c
     const int64_t i = i0 + j * kThreads * N;
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      update(p[j][q], g[j][q] * c, m[j][q], v[j][q], k, e.decay);
+      moments(g[j][q] * c, m[j][q], v[j][q], k);
+      p[j][q] = updated(p[j][q], m[j][q], __builtin_amdgcn_sqrtf(v[j][q]), k, e.decay);
       if (sizeof(P) == 2 && k.stochastic)
         p[j][q] = round_bf16(p[j][q], ((round_bits(base, i + q) >> 21) << 5) + 16);
     }
@@ -244,10 +268,17 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, c
 }
 
 // 8-bit states: a half wave per block of kBlock elements, eight a lane.
+// With fp32 parameters (16 bytes an element and more) the root and the
+// quotients that are stored are the nearest fp32 values, so that the state is
+// the definition's to the bit.  With bf16 parameters (10 bytes) they are within
+// two units of that, and about one stored value in 10^6 is the neighbour on the
+// grid: there the arithmetic is as long as the traffic, and the steps for the
+// last place cost 8%.
 template <typename P, typename G>
 __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, const float *clip) {
   constexpr int N = kChunk / kThreads;
   static_assert(N == 8 && kBlock == 32 * N, "a half wave holds a block");
+  constexpr bool kNearest = sizeof(P) == 4;
   const int at = entry_of(t, blockIdx.x);
   const Entry &e = t.e[at];
   const int64_t i = (int64_t)(blockIdx.x - e.chunk0) * kChunk + threadIdx.x * N, block = i / kBlock;
@@ -269,7 +300,9 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, co
     m[q] *= sm;
     v[q] *= sv;
     v[q] *= v[q];
-    v[q] = update(p[q], g[q] * c, m[q], v[q], k, e.decay);  // the root from here on
+    moments(g[q] * c, m[q], v[q], k);
+    v[q] = kNearest ? nearest_sqrt(v[q]) : __builtin_amdgcn_sqrtf(v[q]);  // the root from here on
+    p[q] = updated(p[q], m[q], v[q], k, e.decay);
     mtop = fmaxf(mtop, fabsf(m[q]));
     rtop = fmaxf(rtop, v[q]);
     if (k.stochastic) {
@@ -279,13 +312,13 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, co
   }
   store_n<N>((P *)e.p + i, left, p);
   if (e.copy) store_n<N>(e.copy + i, left, p);
-  const float nsm = fmaxf(half_wave_max(mtop) / kF8Max, kScaleMin);
-  const float nsv = fmaxf(half_wave_max(rtop) / kF8Max, kScaleMin);
+  const float nsm = fmaxf(half_wave_max(mtop) * kF8Unit, kScaleMin);
+  const float nsv = fmaxf(half_wave_max(rtop) * kF8Unit, kScaleMin);
   const float im = 1.f / nsm, iv = 1.f / nsv;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
-    m[q] = clamp_f8(m[q] * im);
-    v[q] = fminf(v[q] * iv, kF8Max);
+    m[q] = at_most_448(kNearest ? nearest_quotient(m[q], nsm, im) : m[q] * im);
+    v[q] = at_most_448(kNearest ? nearest_quotient(v[q], nsv, iv) : v[q] * iv);
   }
   u32x2 qm, qv;
   if (k.stochastic) {

@@ -17,6 +17,7 @@ inline bool float_or_bf16(rvq_dtype t) { return t == RVQ_F32 || t == RVQ_BF16; }
 
 // ---- 8-bit values: e4m3, largest 448, with fp32 scales ----
 constexpr float kF8Max = 448.f;
+constexpr float kF8Unit = 1.f / 448.f;  // scales: the largest value times this
 // The smallest scale: a block of zeros (or of values below 2^-91) divides by
 // it and not by zero.
 constexpr float kScaleMin = 0x1p-100f;

@@ -16,7 +16,8 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t)1 << 25;
 constexpr int kMaxWidth = 1 << 20;
 constexpr int kMaxLevels = 64;
-constexpr int64_t kMaxTableRows = (int64_t)1 << 28;  // 128 rows a workgroup of 1024: under 2^32 work-items
+constexpr int64_t kMaxTableRows = (int64_t)1 << 28;  // 512 rows a workgroup of 1024: under 2^32 work-items
+constexpr int64_t kMaxList = (int64_t)1 << 30;       // list positions are 32-bit, also a batch beyond the end
 constexpr int64_t kMaxNumel = (int64_t)1 << 34;      // a tensor's workgroups stay under 2^24
 
 rvq_status need(const void *p, const char *name, size_t align) {
@@ -64,8 +65,8 @@ rvq_status check_tables(int64_t T, int32_t L, int32_t K, int64_t V, int32_t D) {
   if (L > kMaxLevels)
     return fail(RVQ_ERR_UNSUPPORTED, "embedding supports L <= %d (got %d)", kMaxLevels, L);
   if (D > kMaxWidth) return fail(RVQ_ERR_UNSUPPORTED, "D above %d (got %d)", kMaxWidth, D);
-  if (T > kMaxRows || T * (L + 1) > INT32_MAX)
-    return fail(RVQ_ERR_UNSUPPORTED, "T above %lld tokens, or T (L + 1) above 2^31 - 1 (got %lld, %d)",
+  if (T > kMaxRows || T * (L + 1) > kMaxList)
+    return fail(RVQ_ERR_UNSUPPORTED, "T above %lld tokens, or T (L + 1) above 2^30 (got %lld, %d)",
                 (long long)kMaxRows, (long long)T, L);
   if (V > kMaxTableRows || (int64_t)L * K + V > kMaxTableRows)
     return fail(RVQ_ERR_UNSUPPORTED, "L K + V above %lld rows", (long long)kMaxTableRows);

@@ -144,7 +144,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
     if (a.y_type == RVQ_F8E4M3) {
       top = row_max<W>(top, red);
       // a row that holds NaN or infinity gets the scale NaN
-      const float scale = fmaxf(top / kF8Max, kScaleMin) + (ss - ss);
+      const float scale = fmaxf(top * kF8Unit, kScaleMin) + (ss - ss);
       const float inv = 1.f / scale;
       if (lane == 0) a.scale[row] = scale;
 #pragma unroll
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_wide_kernel(NormArgs a) {
       float top = 0.f;
       for (int i = threadIdx.x; i < a.d; i += kThreads) top = fmaxf(top, fabsf(h_of(i) * r * w_of(i)));
       top = row_max<kThreads>(top, red);
-      const float scale = fmaxf(top / kF8Max, kScaleMin) + (ss - ss);
+      const float scale = fmaxf(top * kF8Unit, kScaleMin) + (ss - ss);
       inv = 1.f / scale;
       if (threadIdx.x == 0) a.scale[row] = scale;
     }

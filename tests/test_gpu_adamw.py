@@ -249,3 +249,25 @@ def test_adamw_refusals(rvq, dev):
         with pytest.raises((ValueError, TypeError)):
             rvq.rvq_adamw_init(*args, **kw)
     assert all(torch.all(x == 0) for x in p)
+    # memory that was replaced after init
+    p[0].data = torch.ones(100, device=dev)
+    with pytest.raises(ValueError):
+        rvq.rvq_adamw_step(st, g, 1, 0.1)
+    assert torch.all(p[0] == 1)
+
+
+def test_adamw_nan_and_infinity_stay_in_their_places(rvq, dev):
+    # without a norm nothing is skipped: the elements become NaN, and those of
+    # other blocks are untouched by it
+    for bits, seed in ((32, None), (8, None), (8, 3)):
+        p, g = torch.ones(1024, device=dev), torch.ones(1024, device=dev)
+        g[300], g[700] = float("nan"), float("inf")
+        st = rvq.rvq_adamw_init([p], bits, 0.0)
+        rvq.rvq_adamw_step(st, [g], 1, 0.1, seed=seed)
+        bad = torch.isnan(p)
+        assert bad[300] and bad[700] and int(bad.sum()) == 2
+        assert torch.allclose(p[~bad], torch.full_like(p[~bad], 0.9), rtol=1e-5)
+        if bits == 8:
+            m = st.m[0].float() * st.m_scale[0].repeat_interleave(256)
+            assert torch.isnan(m[300]) and torch.isnan(m[700])
+            assert torch.isfinite(m[:256]).all() and torch.isfinite(m[768:]).all()

@@ -50,7 +50,7 @@ class Step:
 
     def tensors(self):
         s = self.state
-        return s.params + s.m + s.v + (s.m_scale or []) + (s.v_scale or [])
+        return s.params + s.m + s.v + (s.m_scale or ()) + (s.v_scale or ())
 
 
 def _bytes(ts):
@@ -65,7 +65,7 @@ def test_step_replays_from_a_graph(rvq, dev, bits):
     for _ in range(4):                                      # four eager steps, one after the other
         out = s.run()
         torch.cuda.synchronize()
-        want.append(_bytes(out + s.tensors()))
+        want.append(_bytes(out + list(s.tensors())))
 
     def restore():
         for t, a in zip(s.tensors(), start):
@@ -90,13 +90,13 @@ def test_step_replays_from_a_graph(rvq, dev, bits):
         torch.cuda.synchronize()
         g.replay()
         torch.cuda.synchronize()
-        for i, (a, b) in enumerate(zip(_bytes(out + s.tensors()), want[rep])):
+        for i, (a, b) in enumerate(zip(_bytes(out + list(s.tensors())), want[rep])):
             assert torch.equal(a, b), f"replay {rep}: tensor {i}"
 
 
 def test_step_on_another_stream(rvq, dev):
     a, b = Step(rvq, dev), Step(rvq, dev)
-    want = _bytes(a.run() + a.tensors())
+    want = _bytes(a.run() + list(a.tensors()))
     torch.cuda.synchronize()
     side = torch.cuda.Stream(device=dev)
     big = torch.randn(4096, 4096, device=dev)
@@ -111,7 +111,7 @@ def test_step_on_another_stream(rvq, dev):
         b.dy.copy_(dy)
         out = b.run()
     side.synchronize()
-    for i, (x, y) in enumerate(zip(_bytes(out + b.tensors()), want)):
+    for i, (x, y) in enumerate(zip(_bytes(out + list(b.tensors())), want)):
         assert torch.equal(x, y), i
 
 

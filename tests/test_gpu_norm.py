@@ -83,11 +83,14 @@ def test_norm_many_rows(rvq, dev):
 
 def test_norm_in_place_and_unaligned(rvq, dev):
     for dtype in (F32, BF16):
-        for d in (100, 1155, 4096):
+        for d in (100, 1155, 4096, 20001):
             w = 1 + 0.1 * _rows(1, d, F32, 3, dev, False)[0]
             for which in ("x", "residual"):
                 x, res = _rows(9, d, dtype, d, dev), _rows(9, d, dtype, d + 1, dev)
                 _check_norm(rvq, x, res, w, dtype, sum_out=x if which == "x" else res)
+            # y in the place of x
+            x, res = _rows(9, d, dtype, d, dev), _rows(9, d, dtype, d + 1, dev)
+            _check_norm(rvq, x, res, w, dtype, out=x)
             # rows that begin one element into a buffer
             buf = _rows(1, 20 * d + 2, dtype, d + 2, dev)[0]
             x, res = buf[1:1 + 9 * d].view(9, d), buf[10 * d + 1:19 * d + 1].view(9, d)
