@@ -26,6 +26,7 @@ namespace {
 constexpr int kRange = 512;        // destination rows of one index workgroup
 constexpr int kBatch = 8;          // loads in flight: ID batches of a wave, rows of a sum
 constexpr int kFlight = 4;         // rows of dout in flight while as many are added
+constexpr int kShort = 256;
 constexpr int64_t kPanelBytes = (int64_t)100 << 20;
 constexpr int kKeysFrom = 2048;   // tokens
 constexpr int kFewTokens = 8192;  // up to here four waves an index workgroup, else sixteen
@@ -35,10 +36,12 @@ constexpr int kThreads = 256;
 constexpr int kMaxGroups = 1 << 22;
 
 // Length of a segment of the list.  A row of at most this many tokens is
-// summed in one go.
-int64_t segment_length(int64_t positions) {
-  const int64_t h = round_up(ceil_div(positions, 4096), 64);
-  return h < 256 ? 256 : h;
+// summed by one wave in one go, at about 0.2 us a token; sequences of up to
+// kShort tokens have no longer rows, and so no third launch.
+int64_t segment_length(int64_t T, int64_t positions) {
+  if (T <= kShort) return kShort;
+  const int64_t h = round_up(ceil_div(positions, 2048), 64);
+  return h < 64 ? 64 : h;
 }
 
 // Which tables' gradients are wanted, and where their lists lie: T positions
@@ -59,7 +62,7 @@ Tables tables_of(int64_t T, int L, int K, int64_t V) {
   t.T = T;
   t.rows = (int64_t)L * K + V;
   t.positions = (L + (V > 0 ? 1 : 0)) * T;
-  t.seg = segment_length(t.positions);
+  t.seg = segment_length(T, t.positions);
   // a row has at most T tokens: none is long if T is not
   t.segments = T > t.seg ? ceil_div(t.positions, t.seg) : 0;
   // the layout is a launch of its own, which short sequences do not win back
@@ -493,7 +496,9 @@ static hipError_t launch_sums(const EmbedGradArgs &a, const Tables &tb, hipStrea
     const int64_t slabs = ceil_div(pieces, W);                                              \
     const int64_t panels = ceil_div(a.T * a.D * (int64_t)sizeof(T), kPanelBytes);           \
     const int64_t panel = panels > 1 ? ceil_div(slabs, panels) : slabs;                     \
-    int64_t R = tb.rows * slabs / (65536 * (64 / W));                                       \
+    const int64_t waves = tb.rows * slabs / (64 / W), few = waves / 8192;                   \
+    int64_t R = waves / 65536;                                                              \
+    if (R < 4) R = few < 4 ? few : 4;                                                       \
     R = R < 1 ? 1 : R > W ? W : R;                                                          \
     const int64_t units = 2 * tb.segments + tb.L * ceil_div(tb.K, R) + ceil_div(tb.V, R);   \
     const int64_t groups = ceil_div(units * slabs, kThreads / W);                           \
