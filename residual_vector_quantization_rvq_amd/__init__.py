@@ -21,6 +21,7 @@ Learning the token embedding:
 from __future__ import annotations
 
 import ctypes
+import functools
 import operator
 import os
 import re
@@ -377,6 +378,9 @@ def _address(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+_CODES = {torch.float32: RVQ_F32, torch.bfloat16: RVQ_BF16}
+
+
 def _need_like(name: str, t: torch.Tensor, x: torch.Tensor) -> None:
     """t has x's shape, type and device and is contiguous."""
     if not (isinstance(t, torch.Tensor) and t.dtype is x.dtype and t.shape == x.shape and
@@ -398,8 +402,10 @@ def _need_workspace(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.d
 def _need_weight(weight: Optional[torch.Tensor], d: int, dev: torch.device) -> int:
     if weight is None:
         return RVQ_F32
-    code = _dtype_code(weight.dtype)
-    _need_shape("weight", weight, (d,), weight.dtype, dev)
+    code = _CODES.get(weight.dtype)
+    if code is None or weight.shape != (d,) or weight.device != dev or not weight.is_contiguous():
+        _need_shape("weight", weight, (d,), weight.dtype, dev)
+        _dtype_code(weight.dtype)
     return code
 
 
@@ -421,10 +427,9 @@ def rvq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
     a residual (sum_out may be x or residual: in place); ``rstd`` is what
     rvq_rms_norm_backward needs."""
     _need_cuda("x", x)
-    dev = x.device
     if x.dim() != 2:
         raise ValueError("x must be [n, d]")
-    n, d = x.shape
+    dev, (n, d) = x.device, x.shape
     code = _dtype_code(x.dtype)
     if residual is not None:
         _need_like("residual", residual, x)
@@ -434,10 +439,10 @@ def rvq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
         sum_out = torch.empty_like(x)
     wcode = _need_weight(weight, d, dev)
     odt = x.dtype if out_dtype is None else out_dtype
-    f8 = odt == torch.float8_e4m3fn
+    f8 = odt is torch.float8_e4m3fn
     ocode = RVQ_F8E4M3 if f8 else _dtype_code(odt)
     if out is None:
-        out = torch.empty((n, d), dtype=odt, device=dev)
+        out = torch.empty_like(x, dtype=odt)
     else:
         _need_shape("out", out, (n, d), odt, dev)
     scale = torch.empty(n, dtype=torch.float32, device=dev) if f8 else None
@@ -448,6 +453,7 @@ def rvq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
     return RMSNormResult(out, scale, sum_out, rstd)
 
 
+@functools.lru_cache(maxsize=256)
 def rvq_rms_norm_backward_workspace_size(n: int, d: int) -> int:
     out = ctypes.c_size_t()
     _check(_lib.rvq_rms_norm_backward_workspace_size(n, d, ctypes.byref(out)))
@@ -490,6 +496,7 @@ def rvq_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     return out, dweight
 
 
+@functools.lru_cache(maxsize=256)
 def rvq_embed_tokens_backward_workspace_size(T: int, L: int, K: int, V: int, D: int) -> int:
     out = ctypes.c_size_t()
     _check(_lib.rvq_embed_tokens_backward_workspace_size(T, L, K, V, D, ctypes.byref(out)))
@@ -640,6 +647,7 @@ def rvq_adamw_init(params: Sequence[torch.Tensor], state_bits: int = 32, weight_
     return AdamWState(params, state_bits, decay, copies, m, v, m_scale, v_scale)
 
 
+@functools.lru_cache(maxsize=256)
 def rvq_adamw_workspace_size(count: int) -> int:
     out = ctypes.c_size_t()
     _check(_lib.rvq_adamw_workspace_size(count, ctypes.byref(out)))
