@@ -19,6 +19,14 @@
 //
 // The tensors' pointers travel as kernel arguments, kTable tensors a launch:
 // nothing is copied, allocated or kept between calls.
+//
+// Bound by memory, every element read and written once (the gradients twice
+// where the norm is asked for).  Bytes moved and time: 537 M fp32 parameters,
+// 32-bit states, clipped, with bf16 copies 18.3 GB, 3.44 ms, 5.3 TB/s; 537 M
+// bf16 parameters with 8-bit states 5.4 GB, 0.96 ms, 5.6 TB/s; 20 M fp32
+// parameters with 8-bit states, clipped, with copies 361 MB, 78 us.  96 tensors
+// of 200,003 elements: four launches of 2 to 6 us (41 us a call, most of it the
+// caller's side).  Streaming stores change nothing (within 1%).
 #include "learn.h"
 
 namespace rvq {
@@ -272,8 +280,8 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, c
 // quotients that are stored are the nearest fp32 values, so that the state is
 // the definition's to the bit.  With bf16 parameters (10 bytes) they are within
 // two units of that, and about one stored value in 10^6 is the neighbour on the
-// grid: there the arithmetic is as long as the traffic, and the steps for the
-// last place cost 8%.
+// grid: there the arithmetic is nearly as long as the traffic, and the last
+// place would cost 4% (945 and 985 us for 537 M).
 template <typename P, typename G>
 __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, const float *clip) {
   constexpr int N = kChunk / kThreads;

@@ -3,20 +3,31 @@
 //   dlevel[l][k] = sum of dout[t] over visual tokens t with ids[t][l] == k
 //   dtext[v]     = sum of dout[t] over text tokens t with ids[t][0] == v
 //
-// No float atomics: every destination row is summed in token order, so the
-// result depends on the inputs alone.
+// No float atomics: every destination row is summed in token order (a long
+// row in pieces, added in order), so the result depends on the inputs alone.
 //
 // embed_index_kernel lists, for each destination row, the tokens that add to
 // it.  A workgroup owns kRange consecutive rows of one table and reads that
 // table's column of the IDs twice: once to count (its rows, and the IDs below
 // them, which is where its part of the table's list begins), once to place.
 // Every wave has a piece of the tokens and a counter per row, so the lists
-// come out in token order.
+// come out in token order.  One launch and no scan over workgroups; its work
+// grows with (rows / kRange) x T, a few per cent of the sums'.
 //
 // embed_sum_kernel sums each row's tokens.  The list is also cut in segments
 // of equal length: a row with more tokens than a segment (a hot codeword, a
 // padding token) is summed segment by segment, and embed_join_kernel adds
 // the pieces in order.
+//
+// What bounds it: every row of the tables is written once, and a visual
+// token's row of dout is read once for each of its L levels.  Those reads miss
+// the L2 (a row is back L levels later) and share the fabric with the writes.
+// 39,731 tokens of 4096 bf16, 131,072 rows of fp32: 2.15 GB written and 2.35
+// GB read in 690 us, 6.5 TB/s; dout read once would leave 370 us.  Tried and
+// slower there: slabs of 64 to 512 bytes, one an XCD, that its L2 can hold
+// (1.1 to 1.4 ms: eight to 32 lanes a row are bound by their control, and the
+// stream of results evicts the slab).  Kernels of that call: by-table IDs 5
+// us, index 35 us, sums 690 us, join 10 us.
 #include "learn.h"
 
 namespace rvq {
@@ -26,23 +37,39 @@ namespace {
 constexpr int kRange = 512;        // destination rows of one index workgroup
 constexpr int kBatch = 8;          // loads in flight: ID batches of a wave, rows of a sum
 constexpr int kFlight = 4;         // rows of dout in flight while as many are added
-constexpr int kShort = 256;
+constexpr int kShort = 256;        // tokens; see segment_length
+// Columns of dout taken together: what the 256 MB Infinity Cache keeps beside
+// the streams (39,731 x 4096 bf16, 325 MB: 776 us in one panel, 753 in panels
+// of 160 MB, 747 of 100 MB, 749 of 60 MB).
 constexpr int64_t kPanelBytes = (int64_t)100 << 20;
-constexpr int kKeysFrom = 2048;   // tokens
-constexpr int kFewTokens = 8192;  // up to here four waves an index workgroup, else sixteen
-constexpr int kFewHits = 12;       // of a wave's 64 IDs: rows told apart one by one, else bit by bit
+// From here on the IDs are laid out by table first: a launch of 4 to 5 us (2,048
+// tokens of 8 levels: index 12.2 us without, 8.4 us with; 5,003 of 16: 26 and 18).
+constexpr int kKeysFrom = 2048;
+// Up to here an index workgroup has four waves, of which eight fit a compute
+// unit, beyond it sixteen (5,003 tokens, 514 workgroups: 27 and 35 us; 39,731
+// tokens, 256 workgroups: 84 and 44 us).
+constexpr int kFewTokens = 8192;
+// Up to so many of a wave's 64 IDs in the workgroup's rows are told apart one by
+// one (about 8 instructions each), more of them bit by bit (80): 37 and 45 us
+// where four of 64 are (39,731 tokens of 8 levels of 8,192).
+constexpr int kFewHits = 12;
 constexpr int kNone = INT32_MIN;   // not an ID of this table
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 1 << 22;
 
 // Length of a segment of the list.  A row of at most this many tokens is
-// summed by one wave in one go, at about 0.2 us a token; sequences of up to
-// kShort tokens have no longer rows, and so no third launch.
+// summed by one wave in one go, at about 0.2 us a token (160 tokens of a row of
+// 2324: 54 us with segments of 256, 26 us of 64); sequences of up to kShort
+// tokens are spared the third launch.  No more than 2048 segments, as each is
+// looked at whether or not a long row is in it.
 int64_t segment_length(int64_t T, int64_t positions) {
   if (T <= kShort) return kShort;
   const int64_t h = round_up(ceil_div(positions, 2048), 64);
   return h < 64 ? 64 : h;
 }
+
+// an ID of this table, kNone among them only as any other out-of-range ID
+__device__ __forceinline__ int id_or_bad(int id) { return id == kNone ? -1 : id; }
 
 // Which tables' gradients are wanted, and where their lists lie: T positions
 // for each level, then T for the text table.
@@ -81,8 +108,8 @@ __global__ __launch_bounds__(kThreads) void embed_keys_kernel(EmbedGradArgs a, T
   if (t >= tb.T) return;
   const bool visual = a.is_visual == nullptr || a.is_visual[t] != 0;
   const int32_t *id = a.ids + t * a.L;
-  for (int l = 0; l < tb.L; ++l) a.keys[l * tb.T + t] = visual ? id[l] : kNone;
-  if (tb.V > 0) a.keys[tb.L * tb.T + t] = visual ? kNone : id[0];
+  for (int l = 0; l < tb.L; ++l) a.keys[l * tb.T + t] = visual ? id_or_bad(id[l]) : kNone;
+  if (tb.V > 0) a.keys[tb.L * tb.T + t] = visual ? kNone : id_or_bad(id[0]);
 }
 
 template <int NW>  // waves of a workgroup
@@ -129,7 +156,7 @@ __global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, T
       mine[u] = t < t1 && (a.is_visual == nullptr || a.is_visual[t] != 0) != text;
     }
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) id[u] = mine[u] ? id[u] : kNone;
+    for (int u = 0; u < kBatch; ++u) id[u] = mine[u] ? id_or_bad(id[u]) : kNone;
   };
 
   int id[kBatch];
@@ -489,8 +516,11 @@ EmbedGradLayout embed_grad_layout(int64_t T, int L, int K, int64_t V, int D) {
 template <typename T, typename G>
 static hipError_t launch_sums(const EmbedGradArgs &a, const Tables &tb, hipStream_t s) {
   const int64_t pieces = ceil_div(a.D, kPiece<T>);
-  // rows a wave takes in turn: enough to pay for looking its list up, few
-  // enough for several waves a SIMD
+  // Rows a wave takes in turn: four to pay for looking its list up, where that
+  // leaves 8192 waves (75 k rows of 384 bf16, all but 16 without a token: 24 us,
+  // one row each 51 us), more of them only beyond 65536 x 4 waves' worth, so that
+  // the last round of waves is short (263 k rows of 1280 in three slabs: 12 rows
+  // 165 us, 24 rows 193, 48 rows 212).
 #define RVQ_SUM(W, TINY)                                                                        \
   do {                                                                                      \
     const int64_t slabs = ceil_div(pieces, W);                                              \

@@ -11,6 +11,13 @@
 // pieces each: a part of a wave for narrow rows (several rows a wave), a wave
 // up to 192 pieces, else a workgroup.  Rows of more than 2048 pieces (8192
 // fp32 or 16384 bf16 elements) are read again for each pass over them.
+//
+// Measured (bytes read and written): 39,731 x 4096 bf16 with residual 220 us,
+// 5.9 TB/s; 39,731 x 1152 bf16 78 us, 4.7 TB/s (84 us with a workgroup a row);
+// 3001 x 1155 fp32 7.7 us; one row of 4096 3.8 us, the time of a launch.
+// Gradient, 39,731 x 4096 bf16 with dsum and dweight: 235 + 5 us, 5.5 TB/s.
+// Streaming stores gain 4% of the norm and 1% of its gradient, and take the
+// rows out of the caches, where the next layer looks for them: not used.
 #include "learn.h"
 
 namespace rvq {
@@ -229,7 +236,8 @@ hipError_t launch_rms_norm(const NormArgs &a, bool x_bf16, hipStream_t s) {
 //   dx = r (g - u mean(g u)) + dsum with g = dy w, u = h r;  dw = sum over rows of dy u
 // One pass: a workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its
 // part of dw in registers; the parts are added in order by a second launch.
-// The number of parts depends on n and d alone, so the result does too.
+// The number of parts depends on n, d and the type alone, so the result does
+// too.
 
 namespace {
 
@@ -253,9 +261,10 @@ int64_t norm_grad_parts(int64_t n, int d, bool bf16) {
 }
 
 // kMaxParts workgroups of four waves are as many as fit at once with 128
-// registers: a second round of fewer would cost as much as the first.  All of
-// a row's loads are issued before its sum; more waves hide the rest (holding
-// the next row too was 2% slower).
+// registers: a second round of fewer would cost as much as the first (39,731 x
+// 4096 bf16: 1024 workgroups 232 us, 1280 300 us; with 129 registers, three
+// to a compute unit, 325 us).  All of a row's loads are issued before its sum;
+// more waves hide the rest (holding the next row too was 2% slower).
 template <typename T, int W, int P, bool DW>
 __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a) {
   constexpr int N = kPiece<T>, R = kThreads / W;

@@ -83,6 +83,25 @@ def test_embed_grad_one_kind_of_token(rvq, dev):
     assert torch.all(level == 0) and torch.all(text == 0)
 
 
+def test_embed_grad_counts_every_out_of_range_id(rvq, dev):
+    for T in (40, 5000):                      # IDs read in place, and laid out by table first
+        ids = torch.zeros((T, 3), dtype=torch.int32, device=dev)
+        odd = [-1, -2 ** 31, 2 ** 31 - 1, 7, -2 ** 31 + 1]
+        for i, v in enumerate(odd):
+            ids[3 * i, i % 3] = v
+        vis = torch.ones(T, dtype=torch.uint8, device=dev)
+        vis[30:36] = 0
+        ids[30:32, 0] = torch.tensor([-2 ** 31, 4], dtype=torch.int32, device=dev)
+        ids[32:36, 0] = 3
+        ids[30:36, 1:] = -5                   # not read: text tokens have one ID
+        bad = torch.zeros(1, dtype=torch.int32, device=dev)
+        dout = torch.ones((T, 8), device=dev)
+        level, text = rvq.rvq_embed_tokens_backward(dout, ids, 7, vis, 4, bad_ids=bad)
+        assert int(bad) == len(odd) + 2
+        assert torch.all(level.sum((1, 2)) == 8 * (T - 6) - 8 * torch.tensor([2, 2, 1], device=dev))
+        assert torch.all(text[3] == 4) and torch.all(text[:3] == 0)
+
+
 def test_embed_grad_accumulates(rvq, dev):
     for gdt, T in ((F32, 3000), (BF16, 200), (F32, 0)):
         L, K, V, D = 3, 25, 400, 50
