@@ -45,10 +45,13 @@ constexpr int64_t kPanelBytes = (int64_t)100 << 20;
 // From here on the IDs are laid out by table first: a launch of 4 to 5 us (2,048
 // tokens of 8 levels: index 12.2 us without, 8.4 us with; 5,003 of 16: 26 and 18).
 constexpr int kKeysFrom = 2048;
-// Up to here an index workgroup has four waves, of which eight fit a compute
-// unit, beyond it sixteen (5,003 tokens, 514 workgroups: 27 and 35 us; 39,731
-// tokens, 256 workgroups: 84 and 44 us).
+// An index workgroup has sixteen waves, or four: where there are more than the
+// 512 workgroups of sixteen that the device holds and up to kFewTokens tokens
+// (5,003 tokens, 514 workgroups: 35 us with sixteen waves, 27 with four; 39,731
+// tokens, 256 workgroups: 44 and 84), and for the shortest sequences (the call
+// of 256 tokens 11.5 and 10.7 us, of 600 17.0 and 15.7).
 constexpr int kFewTokens = 8192;
+constexpr int kVeryFewTokens = 1024;
 // Up to so many of a wave's 64 IDs in the workgroup's rows are told apart one by
 // one (about 8 instructions each), more of them bit by bit (80): 37 and 45 us
 // where four of 64 are (39,731 tokens of 8 levels of 8,192).
@@ -549,7 +552,7 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, bool x_bf16, bool g_bf16, h
   if (tb.rows == 0) return hipSuccess;
   const int64_t units = (int64_t)tb.L * ceil_div(tb.K, kRange) + ceil_div(tb.V, kRange);
   if (tb.keys) embed_keys_kernel<<<dim3((unsigned)ceil_div(a.T, kThreads)), kThreads, 0, s>>>(a, tb);
-  if (a.T <= kFewTokens)
+  if (a.T <= kVeryFewTokens || (a.T <= kFewTokens && units > 512))
     embed_index_kernel<4><<<dim3((unsigned)units), 256, 0, s>>>(a, tb);
   else
     embed_index_kernel<16><<<dim3((unsigned)units), 1024, 0, s>>>(a, tb);
