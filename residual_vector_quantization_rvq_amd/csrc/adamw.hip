@@ -23,9 +23,9 @@
 // Bound by memory, every element read and written once (the gradients twice
 // where the norm is asked for).  Bytes moved and time: 537 M fp32 parameters,
 // 32-bit states, clipped, with bf16 copies 18.3 GB, 3.44 ms, 5.3 TB/s; 537 M
-// bf16 parameters with 8-bit states 5.4 GB, 0.96 ms, 5.6 TB/s; 20 M fp32
+// bf16 parameters with 8-bit states 5.4 GB, 0.98 ms, 5.5 TB/s; 20 M fp32
 // parameters with 8-bit states, clipped, with copies 361 MB, 78 us.  96 tensors
-// of 200,003 elements: four launches of 2 to 6 us (41 us a call, most of it the
+// of 200,003 elements: three launches of 5 to 6 us (41 us a call, most of it the
 // caller's side).  Streaming stores change nothing (within 1%).
 #include "learn.h"
 
@@ -70,7 +70,17 @@ struct Consts {
   uint32_t key;      // of the rounding bits: mixed from seed and step
   bool stochastic;
 };
-static_assert(sizeof(Table) + sizeof(Consts) + 16 <= 4096 && sizeof(NormTable) + 16 <= 4096,
+// Where a step has its gradients' factor from: the partial sums themselves,
+// where they are few (each workgroup adds them up, which saves a launch), the
+// clip kernel's result, or (neither) grad_scale.
+struct Clip {
+  const double *part;
+  int64_t parts;
+  const float *factor;
+  float *grad_norm;   // with part: written by the launch's first workgroup
+};
+constexpr int64_t kFewParts = 1024;
+static_assert(sizeof(Table) + sizeof(Consts) + sizeof(Clip) + 16 <= 4096 && sizeof(NormTable) + 16 <= 4096,
               "kernel arguments");
 
 // 32 bits mixed from 32: xor of the high half, odd multipliers from the
@@ -85,22 +95,20 @@ __host__ __device__ inline uint32_t mix(uint32_t x) {
 __device__ __forceinline__ uint32_t tensor_bits(uint32_t key, int tensor) {
   return mix(key + (uint32_t)tensor);
 }
-__device__ __forceinline__ uint32_t round_bits(uint32_t base, int64_t i) {
-  return mix(base + (uint32_t)i * 0x9E3779B1u + (uint32_t)(i >> 32) * 0x3504F333u);
+// element i's bits are mix(word), word + kWordStep the next element's
+constexpr uint32_t kWordStep = 0x9E3779B1u;
+__device__ __forceinline__ uint32_t round_word(uint32_t base, int64_t i) {
+  return base + (uint32_t)i * kWordStep + (uint32_t)(i >> 32) * 0x3504F333u;
 }
 
-// |v| <= 448 rounded to the e4m3 grid at random, into byte `Byte` of `w`.  The
+// |v| <= 448 (or a few units of the last place above it: both roundings bring
+// that to 448) rounded to the e4m3 grid at random, into byte `Byte` of `w`.  The
 // instruction adds the upper 20 of the random bits under the three bits of
 // the mantissa that stay; below 2^-6 the grid is that of 2^-6, and the bits
 // stand for the same share of its step.
 template <int Byte>
 __device__ __forceinline__ int random_f8(float v, uint32_t random, int w) {
   return __builtin_amdgcn_cvt_sr_fp8_f32(v, (int)random, w, Byte);
-}
-// the largest magnitude divided by its 448th may come out a unit above 448; a
-// NaN stays one
-__device__ __forceinline__ float at_most_448(float v) {
-  return fabsf(v) > kF8Max ? copysignf(kF8Max, v) : v;
 }
 __device__ __forceinline__ float round_bf16(float v, uint32_t random16) {
   return __uint_as_float((__float_as_uint(v) + random16) & 0xffff0000u);
@@ -216,30 +224,52 @@ __global__ __launch_bounds__(kThreads) void adamw_norm_kernel(NormTable t, doubl
   }
 }
 
-// The norm, and the factor of every gradient: NaN where the norm is not
-// finite, which leaves the parameters and states as they are.
-__global__ __launch_bounds__(1024) void adamw_clip_kernel(const double *part, int64_t n, Consts k,
-                                                          float *clip, float *grad_norm) {
-  __shared__ double red[16];
+namespace {
+
+// The norm of all gradients out of the workgroups' sums, added by a workgroup
+// of T threads in an order that depends on their number alone.
+template <int T>
+__device__ __forceinline__ float norm_of(const double *part, int64_t n, float grad_scale) {
+  __shared__ double red[T / 64];
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+  for (int64_t i = threadIdx.x; i < n; i += T) s += part[i];
   s = wave_sum_f64(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
+  double v = 0.0;
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) v += red[w];
+  return (float)(sqrt(v) * (double)fabsf(grad_scale));
+}
+// The factor of every gradient: NaN where the norm is not finite, which leaves
+// the parameters and states as they are.
+__device__ __forceinline__ float factor_of(float norm, const Consts &k) {
+  const float f = k.max_norm / (norm + 1e-6f);
+  return !(norm < INFINITY) ? NAN : k.max_norm > 0.f ? k.grad_scale * fminf(f, 1.f) : k.grad_scale;
+}
+// for every thread of a workgroup of the step
+__device__ __forceinline__ float step_factor(const Clip &c, const Consts &k) {
+  if (!c.part) return c.factor ? *c.factor : k.grad_scale;
+  const float norm = norm_of<kThreads>(c.part, c.parts, k.grad_scale);
+  if (c.grad_norm && blockIdx.x == 0 && threadIdx.x == 0) *c.grad_norm = norm;
+  return factor_of(norm, k);
+}
+
+}  // namespace
+
+__global__ __launch_bounds__(1024) void adamw_clip_kernel(const double *part, int64_t n, Consts k,
+                                                          float *factor, float *grad_norm) {
+  const float norm = norm_of<1024>(part, n, k.grad_scale);
   if (threadIdx.x == 0) {
-    double v = 0.0;
-    for (int w = 0; w < 16; ++w) v += red[w];
-    const float norm = (float)(sqrt(v) * (double)fabsf(k.grad_scale));
     if (grad_norm) *grad_norm = norm;
-    const float f = k.max_norm / (norm + 1e-6f);
-    *clip = !(norm < INFINITY) ? NAN : k.max_norm > 0.f ? k.grad_scale * fminf(f, 1.f) : k.grad_scale;
+    *factor = factor_of(norm, k);
   }
 }
 
 // 32-bit states: two pieces of four elements a lane, all of whose loads are
 // issued before the first is used.
 template <typename P, typename G>
-__global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, const float *clip) {
+__global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, Clip clip) {
   constexpr int N = 4, J = kChunk / (kThreads * N);
   const int at = entry_of(t, blockIdx.x);
   const Entry &e = t.e[at];
@@ -255,18 +285,19 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, c
     load_n<N>((const float *)e.m + i, left[j], m[j]);
     load_n<N>((const float *)e.v + i, left[j], v[j]);
   }
-  const float c = clip ? *clip : k.grad_scale;
+  const float c = step_factor(clip, k);
   if (!(c == c)) return;
   const uint32_t base = tensor_bits(k.key, t.first + at);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int64_t i = i0 + j * kThreads * N;
+    const uint32_t word = round_word(base, i);  // a piece does not reach over a multiple of 2^32
 #pragma unroll
     for (int q = 0; q < N; ++q) {
       moments(g[j][q] * c, m[j][q], v[j][q], k);
       p[j][q] = updated(p[j][q], m[j][q], __builtin_amdgcn_sqrtf(v[j][q]), k, e.decay);
       if (sizeof(P) == 2 && k.stochastic)
-        p[j][q] = round_bf16(p[j][q], ((round_bits(base, i + q) >> 21) << 5) + 16);
+        p[j][q] = round_bf16(p[j][q], ((mix(word + q * kWordStep) >> 21) << 5) + 16);
     }
     store_n<N>((P *)e.p + i, left[j], p[j]);
     store_n<N>((float *)e.m + i, left[j], m[j]);
@@ -275,22 +306,22 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, c
   }
 }
 
-// 8-bit states: a half wave per block of kBlock elements, eight a lane.
-// With fp32 parameters (16 bytes an element and more) the root and the
-// quotients that are stored are the nearest fp32 values, so that the state is
-// the definition's to the bit.  With bf16 parameters (10 bytes) they are within
-// two units of that, and about one stored value in 10^6 is the neighbour on the
-// grid: there the arithmetic is nearly as long as the traffic, and the last
-// place would cost 4% (945 and 985 us for 537 M).
+// 8-bit states: a half wave per block of kBlock elements, eight a lane.  The
+// root and the quotients that are stored are the nearest fp32 values, so that
+// the state is the definition's to the bit: one that is a unit off is stored as
+// the neighbour on the grid about once in 10^6 values, 6 to 12% away.  That
+// costs 1% where parameters are bf16 (966 and 978 us for 537 M; arithmetic is
+// nearly as long as 10 bytes of traffic there), elsewhere nothing.
 template <typename P, typename G>
-__global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, const float *clip) {
+__global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Clip clip) {
   constexpr int N = kChunk / kThreads;
   static_assert(N == 8 && kBlock == 32 * N, "a half wave holds a block");
-  constexpr bool kNearest = sizeof(P) == 4;
   const int at = entry_of(t, blockIdx.x);
   const Entry &e = t.e[at];
   const int64_t i = (int64_t)(blockIdx.x - e.chunk0) * kChunk + threadIdx.x * N, block = i / kBlock;
-  if (block * kBlock >= e.n) return;  // the whole half wave
+  float c = 0.f;
+  if (clip.part) c = step_factor(clip, k);  // a barrier: before any lane leaves
+  if (block * kBlock >= e.n) return;        // the whole half wave
   const int left = (int)(e.n - i < 0 ? 0 : e.n - i < N ? e.n - i : N);
   float p[N], g[N], m[N], v[N];
   load_n<N>((const P *)e.p + i, left, p);
@@ -298,10 +329,11 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, co
   load_f8x8((const uint8_t *)e.m + i, left, m);
   load_f8x8((const uint8_t *)e.v + i, left, v);
   const float sm = e.ms[block], sv = e.vs[block];
-  const float c = clip ? *clip : k.grad_scale;
+  if (!clip.part) c = step_factor(clip, k);
   if (!(c == c)) return;
   const uint32_t base = tensor_bits(k.key, t.first + at);
   float mtop = 0.f, rtop = 0.f;
+  const uint32_t word = round_word(base, i);
   uint32_t bits[N];
 #pragma unroll
   for (int q = 0; q < N; ++q) {
@@ -309,12 +341,12 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, co
     v[q] *= sv;
     v[q] *= v[q];
     moments(g[q] * c, m[q], v[q], k);
-    v[q] = kNearest ? nearest_sqrt(v[q]) : __builtin_amdgcn_sqrtf(v[q]);  // the root from here on
+    v[q] = nearest_sqrt(v[q]);  // the root from here on
     p[q] = updated(p[q], m[q], v[q], k, e.decay);
     mtop = fmaxf(mtop, fabsf(m[q]));
     rtop = fmaxf(rtop, v[q]);
     if (k.stochastic) {
-      bits[q] = round_bits(base, i + q);
+      bits[q] = mix(word + q * kWordStep);
       if (sizeof(P) == 2) p[q] = round_bf16(p[q], ((bits[q] >> 21) << 5) + 16);
     }
   }
@@ -325,8 +357,8 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, co
   const float im = 1.f / nsm, iv = 1.f / nsv;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
-    m[q] = at_most_448(kNearest ? nearest_quotient(m[q], nsm, im) : m[q] * im);
-    v[q] = at_most_448(kNearest ? nearest_quotient(v[q], nsv, iv) : v[q] * iv);
+    m[q] = nearest_quotient(m[q], nsm, im);
+    v[q] = nearest_quotient(v[q], nsv, iv);
   }
   u32x2 qm, qv;
   if (k.stochastic) {
@@ -388,7 +420,8 @@ void for_each_table(const rvq_adamw_tensor *t, int count, int size, Fill fill, L
 }
 
 template <typename P, typename G>
-void launch_step(const rvq_adamw_tensor *t, const AdamArgs &a, const Consts &k, hipStream_t s) {
+void launch_step(const rvq_adamw_tensor *t, const AdamArgs &a, const Consts &k, Clip clip,
+                 hipStream_t s) {
   for_each_table<Table>(
       t, a.count, kTable,
       [&](Entry &e, const rvq_adamw_tensor &x) {
@@ -403,9 +436,10 @@ void launch_step(const rvq_adamw_tensor *t, const AdamArgs &a, const Consts &k, 
       },
       [&](const Table &tab) {
         if (a.eight)
-          adamw_8_kernel<P, G><<<dim3(tab.chunks), kThreads, 0, s>>>(tab, k, a.clip);
+          adamw_8_kernel<P, G><<<dim3(tab.chunks), kThreads, 0, s>>>(tab, k, clip);
         else
-          adamw_32_kernel<P, G><<<dim3(tab.chunks), kThreads, 0, s>>>(tab, k, a.clip);
+          adamw_32_kernel<P, G><<<dim3(tab.chunks), kThreads, 0, s>>>(tab, k, clip);
+        clip.grad_norm = nullptr;  // written by the first launch
       });
 }
 
@@ -427,14 +461,22 @@ int64_t launch_norm(const rvq_adamw_tensor *t, const AdamArgs &a, hipStream_t s)
 hipError_t launch_adamw(const rvq_adamw_tensor *t, const AdamArgs &a, hipStream_t s) {
   const Consts k = {a.b1, a.c1, a.b2, a.c2, a.eps, a.lr1, a.rk2, a.grad_scale, a.max_norm, a.key,
                     a.stochastic};
+  Clip clip = {nullptr, 0, nullptr, nullptr};
   if (a.clip) {
     const int64_t parts = a.g_bf16 ? launch_norm<uint16_t>(t, a, s) : launch_norm<float>(t, a, s);
-    adamw_clip_kernel<<<1, 1024, 0, s>>>(a.part, parts, k, a.clip, a.grad_norm);
+    if (parts > 0 && parts <= kFewParts) {
+      clip = {a.part, parts, nullptr, a.grad_norm};
+    } else {
+      adamw_clip_kernel<<<1, 1024, 0, s>>>(a.part, parts, k, a.clip, a.grad_norm);
+      clip.factor = a.clip;
+    }
   }
   if (a.p_bf16) {
-    if (a.g_bf16) launch_step<uint16_t, uint16_t>(t, a, k, s); else launch_step<uint16_t, float>(t, a, k, s);
+    if (a.g_bf16) launch_step<uint16_t, uint16_t>(t, a, k, clip, s);
+    else launch_step<uint16_t, float>(t, a, k, clip, s);
   } else {
-    if (a.g_bf16) launch_step<float, uint16_t>(t, a, k, s); else launch_step<float, float>(t, a, k, s);
+    if (a.g_bf16) launch_step<float, uint16_t>(t, a, k, clip, s);
+    else launch_step<float, float>(t, a, k, clip, s);
   }
   return hipGetLastError();
 }

@@ -195,6 +195,38 @@ def test_adamw_rounding_at_random(rvq, dev):
         assert abs(r.mean().item() - root) <= 6 * step / 2 / r.numel() ** 0.5 + step * 2 ** -11 + 1e-5 * root
 
 
+def test_adamw_rounding_bits_depend_on_seed_step_place_and_element_alone(rvq, dev):
+    # the same tensor at place 70 of a call, among small and among large ones
+    # (other launches, other workgroups), and on a second run
+    g0 = torch.Generator(device=dev).manual_seed(1)
+    p0, g = torch.randn(5000, generator=g0, device=dev), torch.randn(5000, generator=g0, device=dev)
+    outs = []
+    for others in (1, 3000, 0, 3000):
+        p = [torch.zeros(others, device=dev) for _ in range(70)] + [p0.to(BF16).float()] + [torch.zeros(9, device=dev)]
+        st = rvq.rvq_adamw_init(p, 8)
+        rvq.rvq_adamw_step(st, [torch.zeros_like(x) for x in p[:70]] + [g, torch.zeros(9, device=dev)], 7, 0.1, seed=5)
+        outs.append([x.view(torch.uint8).clone() for x in (st.m[70], st.v[70], st.m_scale[70], p[70])])
+    for o in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+def test_adamw_norm_of_few_and_of_many_workgroups(rvq, dev):
+    # up to 1024 workgroups' sums are added in the step itself, more by a launch
+    # of their own; empty tensors first, and a call of nothing but empty ones
+    for n in (1, 2048 * 1024 - 5, 2048 * 1024 + 1, 5000000):
+        for bits in (32, 8):
+            p = [torch.zeros(0, device=dev), torch.zeros(n, device=dev)]
+            g = [torch.zeros(0, device=dev), torch.full((n,), 0.5, device=dev)]
+            st = rvq.rvq_adamw_init(p, bits)
+            norm = rvq.rvq_adamw_step(st, g, 1, 0.1, max_norm=0.25 * n ** 0.5)
+            assert abs(float(norm) - 0.5 * n ** 0.5) <= 16 * ref.U * 0.5 * n ** 0.5
+            m = st.m[1].double() if bits == 32 else st.m[1].double() * float(st.m_scale[1][0])
+            # the factor is 1/2 (1e-6 less the smaller the norm): m = 0.1 * 0.25
+            assert torch.all((m - 0.025).abs() <= 0.025 * (1e-5 + 1e-5 / n ** 0.5)), (n, bits)
+    st = rvq.rvq_adamw_init([torch.zeros(0, device=dev)])
+    assert float(rvq.rvq_adamw_step(st, [torch.zeros(0, device=dev)], 1, 0.1, max_norm=1.0)) == 0.0
+
+
 def test_adamw_8_bit_states_follow_32_bit_ones(rvq, dev):
     # a noisy quadratic: 300 steps of both; the 8-bit run has to end about as
     # near the minimum (within twice the 32-bit run's distance)
