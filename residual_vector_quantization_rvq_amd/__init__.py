@@ -574,13 +574,14 @@ class AdamWState:
         self.param_dtype = params[0].dtype
         self._numels = [p.numel() for p in params]
         self._table = (_AdamWTensor * len(params))()
-        self._grads = np.frombuffer(self._table, np.uint64).reshape(len(params), -1)[:, 1]
-        none = [None] * len(params)
-        for t, p, a, b, sa, sb, c, w in zip(self._table, params, m, v, m_scale or none,
-                                            v_scale or none, copies or none, weight_decay):
-            t.param, t.m, t.v = p.data_ptr(), a.data_ptr(), b.data_ptr()
-            t.m_scale, t.v_scale, t.copy = _address(sa), _address(sb), _address(c)
-            t.numel, t.weight_decay = p.numel(), w
+        words = np.frombuffer(self._table, np.uint64).reshape(len(params), -1)
+        for column, ts in ((0, params), (2, self.m), (3, self.v), (4, self.m_scale), (5, self.v_scale),
+                           (6, self.copies)):
+            if ts is not None:
+                words[:, column] = [t.data_ptr() for t in ts]
+        words[:, 7] = self._numels
+        words.view(np.float32)[:, 16] = weight_decay
+        self._grads = words[:, 1]
         self._workspace = torch.empty(rvq_adamw_workspace_size(len(params)), dtype=torch.uint8,
                                       device=self.device)
 
@@ -606,8 +607,9 @@ def rvq_adamw_init(params: Sequence[torch.Tensor], state_bits: int = 32, weight_
     dev, dt = params[0].device, params[0].dtype
     _dtype_code(dt)
     for i, p in enumerate(params):
-        _need_cuda(f"params[{i}]", p, dev)
-        if p.dtype != dt:
+        if not (isinstance(p, torch.Tensor) and p.is_cuda and p.device == dev and p.is_contiguous()):
+            _need_cuda(f"params[{i}]", p, dev)
+        if p.dtype is not dt:
             raise ValueError(f"params[{i}] is {p.dtype}, expected {dt}")
     sdt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
 
@@ -618,7 +620,9 @@ def rvq_adamw_init(params: Sequence[torch.Tensor], state_bits: int = 32, weight_
         if len(given) != len(params):
             raise ValueError(f"{name} must have one tensor per parameter")
         for i, (t, p) in enumerate(zip(given, params)):
-            _need_shape(f"{name}[{i}]", t, shape(p), dtype, dev)
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape(p) and
+                    t.device == dev and t.is_contiguous()):
+                _need_shape(f"{name}[{i}]", t, shape(p), dtype, dev)
         return given
 
     def same(p):
