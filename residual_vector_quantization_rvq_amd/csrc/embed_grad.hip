@@ -27,7 +27,7 @@
 // slower there: slabs of 64 to 512 bytes, one an XCD, that its L2 can hold
 // (1.1 to 1.4 ms: eight to 32 lanes a row are bound by their control, and the
 // stream of results evicts the slab).  Kernels of that call: by-table IDs 5
-// us, index 35 us, sums 690 us, join 10 us.
+// us, index 30 us, sums 690 us, join 10 us.
 #include "learn.h"
 
 namespace rvq {
@@ -138,39 +138,51 @@ __global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, T
   if (threadIdx.x == 0) below_sum = 0;
   __syncthreads();
 
-  const int64_t piece = round_up(ceil_div(tb.T, kIndexWaves), 64);
-  const int64_t t0 = wave * piece < tb.T ? wave * piece : tb.T;
-  const int64_t t1 = t0 + piece < tb.T ? t0 + piece : tb.T;
+  // 32-bit token numbers and byte offsets (T (L + 1) <= 2^30, checked on the
+  // host): the loops below are bound by their instructions
+  const int T = (int)tb.T;
+  const int piece = (int)round_up(ceil_div(tb.T, kIndexWaves), 64);
+  const int t0 = wave * piece < T ? wave * piece : T;
+  const int t1 = t0 + piece < T ? t0 + piece : T;
+  const uint32_t u0 = (uint32_t)r0, rows = (uint32_t)(r1 - r0);
+  const int32_t *keys = a.keys + region;
   // IDs of kBatch x 64 tokens in this table; kNone for a token of the other kind
-  const auto load_ids = [&](int64_t tw, int (&id)[kBatch]) {
-    if (tb.keys) {
+  int id[kBatch];
+  const auto load_ids = [&](int tw) {
+    if (tb.keys && tw + kBatch * 64 <= t1) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) id[u] = keys[(uint32_t)(tw + u * 64 + lane)];
+    } else if (tb.keys) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t t = tw + u * 64 + lane;
-        id[u] = t < t1 ? a.keys[region + t] : kNone;
+        const int t = tw + u * 64 + lane;
+        id[u] = t < t1 ? keys[(uint32_t)t] : kNone;
       }
-      return;
-    }
-    bool mine[kBatch];
+    } else {
+      bool mine[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t t = tw + u * 64 + lane;
-      id[u] = t < t1 ? a.ids[t * a.L + l] : 0;
-      mine[u] = t < t1 && (a.is_visual == nullptr || a.is_visual[t] != 0) != text;
-    }
+      for (int u = 0; u < kBatch; ++u) {
+        const int t = tw + u * 64 + lane;
+        id[u] = t < t1 ? a.ids[(uint32_t)t * (uint32_t)a.L + (uint32_t)l] : 0;
+        mine[u] = t < t1 && (a.is_visual == nullptr || a.is_visual[t] != 0) != text;
+      }
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) id[u] = mine[u] ? id_or_bad(id[u]) : kNone;
+      for (int u = 0; u < kBatch; ++u) id[u] = mine[u] ? id_or_bad(id[u]) : kNone;
+    }
   };
 
-  int id[kBatch];
   int below = 0, bad = 0;
-  for (int64_t tw = t0; tw < t1; tw += kBatch * 64) {
-    load_ids(tw, id);
+  for (int tw = t0; tw < t1; tw += kBatch * 64) {
+    load_ids(tw);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      below += id[u] >= 0 && id[u] < r0;
-      bad += (id[u] < 0 && id[u] != kNone) || id[u] >= limit;
-      if (id[u] >= r0 && id[u] < r1) atomicAdd(&cnt[wave][id[u] - r0], 1);
+      below += (uint32_t)id[u] < u0;
+      const uint32_t k = (uint32_t)id[u] - u0;
+      if (k < rows) atomicAdd(&cnt[wave][k], 1);
+    }
+    if (range == 0) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) bad += (uint32_t)id[u] >= (uint32_t)limit && id[u] != kNone;
     }
   }
 #pragma unroll
@@ -180,7 +192,7 @@ __global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, T
   }
   if (lane == 0) {
     if (below) atomicAdd(&below_sum, below);
-    if (bad && range == 0 && a.bad) atomicAdd(a.bad, (uint32_t)bad);
+    if (bad && a.bad) atomicAdd(a.bad, (uint32_t)bad);
   }
   __syncthreads();
 
@@ -230,19 +242,19 @@ __global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, T
   if (r1 == limit)
     for (int64_t i = total + (int64_t)threadIdx.x; i < region + tb.T; i += kIndexThreads) a.row[i] = -1;
 
-  for (int64_t tw = t0; tw < t1; tw += kBatch * 64) {
-    load_ids(tw, id);
+  for (int tw = t0; tw < t1; tw += kBatch * 64) {
+    load_ids(tw);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const bool hit = id[u] >= r0 && id[u] < r1;
+      const uint32_t k = (uint32_t)id[u] - u0;
+      const bool hit = k < rows;
       const unsigned long long hits = __ballot(hit);
       if (hits == 0) continue;
-      const int k = hit ? id[u] - r0 : 0;
       unsigned long long same = 0;  // lanes of the same row
       if (__popcll(hits) <= kFewHits) {  // row by row
         for (unsigned long long rest = hits; rest;) {
-          const int of = __builtin_amdgcn_readlane(k, __ffsll((long long)rest) - 1);
-          const unsigned long long m = __ballot(hit && k == of);
+          const uint32_t of = (uint32_t)__builtin_amdgcn_readlane((int)k, __ffsll((long long)rest) - 1);
+          const unsigned long long m = __ballot(k == of);  // of is below rows: a hit
           if (k == of) same = m;
           rest &= ~m;
         }
@@ -260,8 +272,8 @@ __global__ __launch_bounds__(NW * 64) void embed_index_kernel(EmbedGradArgs a, T
       at = __shfl(at, first, 64);
       if (hit) {
         at += __popcll(same & ((1ull << lane) - 1));
-        a.token[at] = (int)(tw + u * 64 + lane);
-        a.row[at] = (int)(row0 + k);
+        a.token[at] = tw + u * 64 + lane;
+        a.row[at] = (int)row0 + (int)k;
       }
     }
   }
