@@ -314,8 +314,9 @@ rvq_status rvq_embed_tokens(const int32_t *ids, const uint8_t *is_visual, int64_
  *                another overlap.
  * y            : device, [n][d] in y_dtype.  RVQ_F8E4M3: row i holds
  *                e4m3(y / y_scale[i]), nearest even, with
- *                y_scale[i] = max(max|y| / 448, 2^-100) (NaN where the row
- *                holds NaN or infinity).  May be x itself if the types agree.
+ *                y_scale[i] = max(max|y| / 448, 2^-100) (NaN where a value of
+ *                the row's y is NaN or infinite, by x, residual or weight).
+ *                May be x itself if the types agree.
  * y_scale      : device, [n] fp32, required for RVQ_F8E4M3, else ignored.
  * rstd         : device, [n] fp32: r of every row, for the gradient; or NULL.
  * Limits: n <= 2^25, d <= 2^20.

@@ -43,19 +43,28 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
   }
   return v;
 }
+// The largest magnitude of a row, as its bits: whole numbers in the same order,
+// with infinity and then NaN above every finite value, so that neither is lost.
+__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(fabsf(v)); }
 template <int W>
-__device__ __forceinline__ float row_max(float v, float *red) {
+__device__ __forceinline__ uint32_t row_max(uint32_t v, float *red) {
 #pragma unroll
-  for (int off = (W < 64 ? W : 64) / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  for (int off = (W < 64 ? W : 64) / 2; off >= 1; off >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off, 64));
   if constexpr (W > 64) {
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = __uint_as_float(v);
     __syncthreads();
-    v = red[0];
+    v = __float_as_uint(red[0]);
 #pragma unroll
-    for (int w = 1; w < W / 64; ++w) v = fmaxf(v, red[w]);
+    for (int w = 1; w < W / 64; ++w) v = max(v, __float_as_uint(red[w]));
   }
   return v;
+}
+// An 8-bit row's scale out of that; NaN where a value of the row is not finite,
+// which its e4m3 bytes cannot say.
+__device__ __forceinline__ float row_scale(uint32_t top) {
+  const float t = __uint_as_float(top);
+  return t < INFINITY ? fmaxf(t * kF8Unit, kScaleMin) : NAN;
 }
 
 template <int N>
@@ -131,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
     ss = row_sum<W>(ss, red);
     const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
     if (a.rstd && lane == 0) a.rstd[row] = r;
-    float top = 0.f;
+    uint32_t top = 0;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = (p * W + lane) * N;
@@ -141,7 +150,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         h[p][e] = h[p][e] * r * w[e];
-        top = fmaxf(top, fabsf(h[p][e]));
+        top = max(top, magnitude_bits(h[p][e]));
       }
       if (a.y_type == RVQ_BF16)
         store_n<N>((uint16_t *)a.y + at + c, a.d - c, h[p]);
@@ -149,9 +158,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
         store_n<N>((float *)a.y + at + c, a.d - c, h[p]);
     }
     if (a.y_type == RVQ_F8E4M3) {
-      top = row_max<W>(top, red);
-      // a row that holds NaN or infinity gets the scale NaN
-      const float scale = fmaxf(top * kF8Unit, kScaleMin) + (ss - ss);
+      const float scale = row_scale(row_max<W>(top, red)) + (ss - ss);  // NaN, too, where the squares overflow
       const float inv = 1.f / scale;
       if (lane == 0) a.scale[row] = scale;
 #pragma unroll
@@ -190,10 +197,9 @@ __global__ __launch_bounds__(kThreads) void rms_norm_wide_kernel(NormArgs a) {
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = r;
     float inv = 1.f;
     if (a.y_type == RVQ_F8E4M3) {
-      float top = 0.f;
-      for (int i = threadIdx.x; i < a.d; i += kThreads) top = fmaxf(top, fabsf(h_of(i) * r * w_of(i)));
-      top = row_max<kThreads>(top, red);
-      const float scale = fmaxf(top * kF8Unit, kScaleMin) + (ss - ss);
+      uint32_t top = 0;
+      for (int i = threadIdx.x; i < a.d; i += kThreads) top = max(top, magnitude_bits(h_of(i) * r * w_of(i)));
+      const float scale = row_scale(row_max<kThreads>(top, red)) + (ss - ss);
       inv = 1.f / scale;
       if (threadIdx.x == 0) a.scale[row] = scale;
     }
