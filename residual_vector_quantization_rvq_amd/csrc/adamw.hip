@@ -184,11 +184,6 @@ __device__ __forceinline__ float nearest_sqrt(float v) {
   const float r = __builtin_fmaf(-s, s, v);
   return v > 0x1p-120f ? __builtin_fmaf(r, 0.5f * y, s) : 0.f;
 }
-// the nearest fp32 to x / d, inv the nearest to 1 / d
-__device__ __forceinline__ float nearest_quotient(float x, float d, float inv) {
-  const float q = x * inv;
-  return __builtin_fmaf(__builtin_fmaf(-q, d, x), inv, q);
-}
 
 }  // namespace
 

@@ -36,6 +36,13 @@ __device__ __forceinline__ float f8_to_f32(uint8_t b) {
   return __builtin_amdgcn_cvt_f32_fp8((int)b, 0);
 }
 __device__ __forceinline__ float clamp_f8(float v) { return fminf(fmaxf(v, -kF8Max), kF8Max); }
+// The nearest fp32 to x / d, inv the nearest to 1 / d: an e4m3 value turns on
+// the quotient's last place (x * inv is stored as the neighbour on the grid
+// about once in 10^6 values, 6 to 12% away).
+__device__ __forceinline__ float nearest_quotient(float x, float d, float inv) {
+  const float q = x * inv;
+  return __builtin_fmaf(__builtin_fmaf(-q, d, x), inv, q);
+}
 
 // ---- element access; bf16 is held as its 16 bits ----
 __device__ __forceinline__ float load_f32(const float *p, int64_t i) { return p[i]; }

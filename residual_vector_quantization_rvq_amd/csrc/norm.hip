@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
         const int c = (p * W + lane) * N;
         if (c >= a.d) continue;
 #pragma unroll
-        for (int e = 0; e < N; ++e) h[p][e] = clamp_f8(h[p][e] * inv);
+        for (int e = 0; e < N; ++e) h[p][e] = clamp_f8(nearest_quotient(h[p][e], scale, inv));
         store_f8_n<N>((uint8_t *)a.y + at + c, a.d - c, h[p]);
       }
     }
@@ -195,11 +195,11 @@ __global__ __launch_bounds__(kThreads) void rms_norm_wide_kernel(NormArgs a) {
     ss = row_sum<kThreads>(ss, red);
     const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = r;
-    float inv = 1.f;
+    float scale = 1.f, inv = 1.f;
     if (a.y_type == RVQ_F8E4M3) {
       uint32_t top = 0;
       for (int i = threadIdx.x; i < a.d; i += kThreads) top = max(top, magnitude_bits(h_of(i) * r * w_of(i)));
-      const float scale = row_scale(row_max<kThreads>(top, red)) + (ss - ss);
+      scale = row_scale(row_max<kThreads>(top, red)) + (ss - ss);
       inv = 1.f / scale;
       if (threadIdx.x == 0) a.scale[row] = scale;
     }
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_wide_kernel(NormArgs a) {
       const float y = h * r * w_of(i);
       if (a.sum) store_f32((T *)a.sum, at + i, h);
       if (a.y_type == RVQ_F8E4M3)
-        ((uint8_t *)a.y)[at + i] = f32_to_f8(clamp_f8(y * inv));
+        ((uint8_t *)a.y)[at + i] = f32_to_f8(clamp_f8(nearest_quotient(y, scale, inv)));
       else if (a.y_type == RVQ_BF16)
         store_f32((uint16_t *)a.y, at + i, y);
       else

@@ -44,3 +44,20 @@ def test_norm_8_bit_rows_show_a_weight_that_is_not_finite(rvq, dev, dtype, d):
             assert torch.isnan(out.y.float() * out.scale[:, None])[:, at].all()
     # finite weights: the scale is the row's
     assert torch.isfinite(rvq.rvq_rms_norm(x, torch.ones(d, device=dev), out_dtype=F8).scale).all()
+
+
+@pytest.mark.parametrize("dtype,n,d", [(F32, 20000, 64), (F32, 6000, 1152), (F32, 300, 20001), (BF16, 3000, 4096),
+                                       (BF16, 300, 30000)])
+def test_norm_8_bit_values_are_those_of_the_quotient(rvq, dev, dtype, n, d):
+    # y in fp32 is what the 8-bit rows are made of: their bytes have to be the
+    # quotients' (in fp32, correctly rounded, as the CPU divides) to the bit
+    x = norm_tests._rows(n, d, dtype, d, dev)
+    w = 1 + 0.2 * norm_tests._rows(1, d, F32, 5, dev, False)[0]
+    y = rvq.rvq_rms_norm(x, w, out_dtype=F32).y.cpu()
+    out = rvq.rvq_rms_norm(x, w, out_dtype=F8)
+    scale = out.scale.cpu()
+    top = y.abs().amax(1)
+    assert torch.all((scale.double() - top.double() / 448).abs() <= 2 * ref.U * scale.double())
+    want = (y / scale[:, None]).clamp(-448, 448).to(F8).view(torch.uint8)
+    off = int((want != out.y.cpu().view(torch.uint8)).sum())
+    assert off == 0, f"{off} of {n * d} bytes"
