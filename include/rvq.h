@@ -302,7 +302,8 @@ rvq_status rvq_embed_tokens(const int32_t *ids, const uint8_t *is_visual, int64_
 /*
  * RMS norm of rows, with the residual's addition and an 8-bit output:
  *   h = x + residual (or x),  r = 1 / sqrt(mean(h^2) + eps),  y = h r weight,
- * in fp32; each output is rounded once (y uses the unrounded h).
+ * in fp32; each output is rounded once (y uses the unrounded h).  h has to be
+ * within fp32's range, its squares need not be.
  *
  * x, residual  : device, [n][d] rows in x_dtype (RVQ_F32 or RVQ_BF16);
  *                residual may be NULL.

@@ -16,13 +16,13 @@ inline size_t dtype_bytes(rvq_dtype t) { return t == RVQ_F32 ? 4 : t == RVQ_BF16
 inline bool float_or_bf16(rvq_dtype t) { return t == RVQ_F32 || t == RVQ_BF16; }
 
 // ---- 8-bit values: e4m3, largest 448, with fp32 scales ----
-constexpr float kF8Max = 448.f;
 constexpr float kF8Unit = 1.f / 448.f;  // scales: the largest value times this
 // The smallest scale: a block of zeros (or of values below 2^-91) divides by
 // it and not by zero.
 constexpr float kScaleMin = 0x1p-100f;
 
-// four fp32 values as e4m3 bytes, rounded to nearest even; |v| <= 448
+// four fp32 values as e4m3 bytes, rounded to nearest even; |v| <= 448 or a few
+// units of the last place above it, which rounding brings to 448; NaN stays NaN
 __device__ __forceinline__ uint32_t pack_f8x4(float a, float b, float c, float d) {
   int w = 0;
   w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
@@ -35,7 +35,6 @@ __device__ __forceinline__ uint8_t f32_to_f8(float a) {
 __device__ __forceinline__ float f8_to_f32(uint8_t b) {
   return __builtin_amdgcn_cvt_f32_fp8((int)b, 0);
 }
-__device__ __forceinline__ float clamp_f8(float v) { return fminf(fmaxf(v, -kF8Max), kF8Max); }
 // The nearest fp32 to x / d, inv the nearest to 1 / d: an e4m3 value turns on
 // the quotient's last place (x * inv is stored as the neighbour on the grid
 // about once in 10^6 values, 6 to 12% away).
@@ -194,7 +193,7 @@ __device__ __forceinline__ void stream_n(uint16_t *p, const float (&v)[N]) {
     __builtin_nontemporal_store(q, (u32x2_at2 *)p);
   }
 }
-// e4m3 bytes of values within +-448
+// e4m3 bytes, of values as for pack_f8x4
 template <int N>
 __device__ __forceinline__ void store_f8_n(uint8_t *p, int left, const float (&v)[N]) {
   if (left >= N) {

@@ -79,6 +79,15 @@ __device__ __forceinline__ void load_weight(const void *w, bool bf16, int c, int
   }
 }
 
+// A row's mean of squares plus eps that fp32 does not hold, or holds in less
+// than full precision: such a row is taken again with its values times
+// range_factor(), a power of two.  (r comes out for the values as multiplied;
+// times the factor it is the row's.)  2^-80: 2^20 squares of the largest value add
+// up to 2^116, and one that can overflow with 2^20 others is 2^-52 or more.  Only
+// rows with values beyond 10^16, or an eps below 2^-100, get there.
+__device__ __forceinline__ bool out_of_range(float mean) { return !(mean < INFINITY && mean > 0x1p-100f); }
+__device__ __forceinline__ float range_factor(float mean) { return mean < 1.f ? 0x1p70f : 0x1p-80f; }
+
 // how a row of `pieces` is shared: W lanes, P pieces each
 #define RVQ_NORM_SHAPES(X) \
   X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(64, 2) X(64, 3) X(256, 1) X(256, 2) X(256, 4) X(256, 8)
@@ -95,8 +104,10 @@ Shape shape_of(int64_t pieces) {
 
 }  // namespace
 
+// Two pieces a lane of a workgroup: held to the 72 registers of seven waves (with
+// 74 and six, 39,731 x 4096 bf16 to 8 bits take 121 us and not 112).
 template <typename T, int W, int P>
-__global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(kThreads, W == 256 && P == 2 ? 7 : 1) void rms_norm_kernel(NormArgs a) {
   constexpr int N = kPiece<T>, R = kThreads / W;
   __shared__ float red[kThreads / 64];
   const int lane = threadIdx.x % W;
@@ -138,8 +149,23 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < N; ++e) ss += h[p][e] * h[p][e];
     ss = row_sum<W>(ss, red);
-    const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
-    if (a.rstd && lane == 0) a.rstd[row] = r;
+    float mean = ss / (float)a.d + a.eps, factor = 1.f;
+    if (out_of_range(mean)) {  // the same for the row's lanes
+      factor = range_factor(mean);
+      ss = 0.f;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          h[p][e] *= factor;
+          ss += h[p][e] * h[p][e];
+        }
+      ss = row_sum<W>(ss, red);
+      mean = ss / (float)a.d + a.eps * factor * factor;
+    }
+    const float r = 1.f / sqrtf(mean);
+    if (a.rstd && lane == 0) a.rstd[row] = r * factor;
+    const bool f8 = a.y_type == RVQ_F8E4M3;
     uint32_t top = 0;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -148,17 +174,18 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
       float w[N];
       load_weight<N>(a.weight, a.w_bf16, c, a.d - c, w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        h[p][e] = h[p][e] * r * w[e];
-        top = max(top, magnitude_bits(h[p][e]));
-      }
-      if (a.y_type == RVQ_BF16)
+      for (int e = 0; e < N; ++e) h[p][e] = h[p][e] * r * w[e];
+      if (f8) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) top = max(top, magnitude_bits(h[p][e]));
+      } else if (a.y_type == RVQ_BF16) {
         store_n<N>((uint16_t *)a.y + at + c, a.d - c, h[p]);
-      else if (a.y_type == RVQ_F32)
+      } else {
         store_n<N>((float *)a.y + at + c, a.d - c, h[p]);
+      }
     }
-    if (a.y_type == RVQ_F8E4M3) {
-      const float scale = row_scale(row_max<W>(top, red)) + (ss - ss);  // NaN, too, where the squares overflow
+    if (f8) {
+      const float scale = row_scale(row_max<W>(top, red));
       const float inv = 1.f / scale;
       if (lane == 0) a.scale[row] = scale;
 #pragma unroll
@@ -166,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
         const int c = (p * W + lane) * N;
         if (c >= a.d) continue;
 #pragma unroll
-        for (int e = 0; e < N; ++e) h[p][e] = clamp_f8(nearest_quotient(h[p][e], scale, inv));
+        for (int e = 0; e < N; ++e) h[p][e] = nearest_quotient(h[p][e], scale, inv);
         store_f8_n<N>((uint8_t *)a.y + at + c, a.d - c, h[p]);
       }
     }
@@ -187,28 +214,35 @@ __global__ __launch_bounds__(kThreads) void rms_norm_wide_kernel(NormArgs a) {
       return h;
     };
     const auto w_of = [&](int i) { return a.weight ? load_either(a.weight, a.w_bf16, i) : 1.f; };
-    float ss = 0.f;
-    for (int i = threadIdx.x; i < a.d; i += kThreads) {
-      const float h = h_of(i);
-      ss += h * h;
+    const auto mean_of = [&](float factor) {
+      float ss = 0.f;
+      for (int i = threadIdx.x; i < a.d; i += kThreads) {
+        const float h = h_of(i) * factor;
+        ss += h * h;
+      }
+      return row_sum<kThreads>(ss, red) / (float)a.d + a.eps * factor * factor;
+    };
+    float factor = 1.f, mean = mean_of(1.f);
+    if (out_of_range(mean)) {
+      factor = range_factor(mean);
+      mean = mean_of(factor);
     }
-    ss = row_sum<kThreads>(ss, red);
-    const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[row] = r;
+    const float r = 1.f / sqrtf(mean);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = r * factor;
     float scale = 1.f, inv = 1.f;
     if (a.y_type == RVQ_F8E4M3) {
       uint32_t top = 0;
-      for (int i = threadIdx.x; i < a.d; i += kThreads) top = max(top, magnitude_bits(h_of(i) * r * w_of(i)));
-      scale = row_scale(row_max<kThreads>(top, red)) + (ss - ss);
+      for (int i = threadIdx.x; i < a.d; i += kThreads) top = max(top, magnitude_bits(h_of(i) * factor * r * w_of(i)));
+      scale = row_scale(row_max<kThreads>(top, red));
       inv = 1.f / scale;
       if (threadIdx.x == 0) a.scale[row] = scale;
     }
     for (int i = threadIdx.x; i < a.d; i += kThreads) {
       const float h = h_of(i);
-      const float y = h * r * w_of(i);
+      const float y = h * factor * r * w_of(i);
       if (a.sum) store_f32((T *)a.sum, at + i, h);
       if (a.y_type == RVQ_F8E4M3)
-        ((uint8_t *)a.y)[at + i] = f32_to_f8(clamp_f8(nearest_quotient(y, scale, inv)));
+        ((uint8_t *)a.y)[at + i] = f32_to_f8(nearest_quotient(y, scale, inv));
       else if (a.y_type == RVQ_BF16)
         store_f32((uint16_t *)a.y, at + i, y);
       else

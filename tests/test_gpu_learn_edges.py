@@ -61,3 +61,36 @@ def test_norm_8_bit_values_are_those_of_the_quotient(rvq, dev, dtype, n, d):
     want = (y / scale[:, None]).clamp(-448, 448).to(F8).view(torch.uint8)
     off = int((want != out.y.cpu().view(torch.uint8)).sum())
     assert off == 0, f"{off} of {n * d} bytes"
+
+
+@pytest.mark.parametrize("dtype,d", [(F32, 5), (F32, 64), (F32, 500), (F32, 1155), (F32, 4096), (F32, 9000),
+                                     (BF16, 40), (BF16, 1152), (BF16, 4096), (BF16, 20001)])
+def test_norm_rows_whose_squares_leave_fp32(rvq, dev, dtype, d):
+    w = 1 + 0.2 * norm_tests._rows(1, d, F32, 5, dev, False)[0]
+    x = norm_tests._rows(12, d, F32, d, dev)
+    size = torch.tensor([1.0, 1e18, 3e19, 1e25, 1e30, 1e36, 1.0, 2e19, 1e35, 1e20, 1e19, 1e-3], device=dev)
+    x = (x * size[:, None]).to(dtype)
+    assert torch.isfinite(x).all()
+    for odt in (F32, BF16, F8):
+        norm_tests._check_norm(rvq, x, None, w, odt)
+    # with a residual, whose sum the norm takes
+    norm_tests._check_norm(rvq, x, (x.float() * 0.5).to(dtype), w, dtype)
+    # the largest values there are; in rows of their own, beside NaN and infinity
+    x = torch.full((4, d), MAX if dtype == F32 else 3.3895313892515355e38, device=dev).to(dtype)
+    x[1, 0], x[2, d - 1] = NAN, -INF
+    out = rvq.rvq_rms_norm(x, out_dtype=F32, need_rstd=True)
+    one = torch.ones(d, device=dev)
+    for row in (0, 3):
+        # 1 / sqrt(mean) is below fp32's normal values: a unit there is 2^-149
+        assert torch.all((out.y[row] - one).abs() <= 1e-6)
+        assert abs(out.rstd[row].item() * x[row, 0].item() - 1) <= 2.0 ** -21
+    assert torch.isnan(out.y[1]).all() and torch.isnan(out.y[2, d - 1])
+
+
+@pytest.mark.parametrize("d", [5, 300, 4096, 9000])
+def test_norm_rows_whose_squares_are_below_fp32(rvq, dev, d):
+    # an eps of fp32's smallest value and rows whose squares are about as large
+    x = norm_tests._rows(6, d, F32, d, dev, False)
+    x = x * torch.tensor([1.0, 1e-15, 1e-19, 1e-22, 1e-25, 0.0], device=dev)[:, None]
+    for odt in (F32, F8):
+        norm_tests._check_norm(rvq, x, None, None, odt, eps=2.0 ** -149)
