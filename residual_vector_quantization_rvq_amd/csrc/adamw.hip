@@ -178,12 +178,15 @@ __device__ __forceinline__ float updated(float p, float m, float root, const Con
 }
 
 // The nearest fp32 to sqrt(v), by one Newton step from the hardware's 1 /
-// sqrt(v); roots under 2^-60 are taken for zero (eps is at least 1e-12).
+// sqrt(v), for finite v; NaN stays NaN.  A v below kSmall, whose remainder fp32
+// does not hold, is taken for zero: small_sqrt is for those.
+constexpr float kSmall = 0x1p-96f;
 __device__ __forceinline__ float nearest_sqrt(float v) {
   const float y = __builtin_amdgcn_rsqf(v), s = v * y;
   const float r = __builtin_fmaf(-s, s, v);
-  return v > 0x1p-120f ? __builtin_fmaf(r, 0.5f * y, s) : 0.f;
+  return v < kSmall ? 0.f : __builtin_fmaf(r, 0.5f * y, s);
 }
+__device__ __forceinline__ float small_sqrt(float v) { return nearest_sqrt(v * 0x1p64f) * 0x1p-32f; }
 
 }  // namespace
 
@@ -329,13 +332,14 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
   const uint32_t base = tensor_bits(k.key, t.first + at);
   float mtop = 0.f, rtop = 0.f;
   const uint32_t word = round_word(base, i);
-  uint32_t bits[N];
+  uint32_t bits[N], least = UINT32_MAX;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
     m[q] *= sm;
     v[q] *= sv;
     v[q] *= v[q];
     moments(g[q] * c, m[q], v[q], k);
+    least = min(least, __float_as_uint(v[q]) - 1);  // zero does not count
     v[q] = nearest_sqrt(v[q]);  // the root from here on
     p[q] = updated(p[q], m[q], v[q], k, e.decay);
     mtop = fmaxf(mtop, fabsf(m[q]));
@@ -343,6 +347,25 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
     if (k.stochastic) {
       bits[q] = mix(word + q * kWordStep);
       if (sizeof(P) == 2) p[q] = round_bf16(p[q], ((bits[q] >> 21) << 5) + 16);
+    }
+  }
+  if (least < __float_as_uint(kSmall) - 1) {  // hardly ever: a lane's elements once more, with the roots of any v
+    mtop = rtop = 0.f;
+    load_n<N>((const P *)e.p + i, left, p);
+    load_n<N>((const G *)e.g + i, left, g);
+    load_f8x8((const uint8_t *)e.m + i, left, m);
+    load_f8x8((const uint8_t *)e.v + i, left, v);
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      m[q] *= sm;
+      v[q] *= sv;
+      v[q] *= v[q];
+      moments(g[q] * c, m[q], v[q], k);
+      v[q] = v[q] < kSmall ? small_sqrt(v[q]) : nearest_sqrt(v[q]);
+      p[q] = updated(p[q], m[q], v[q], k, e.decay);
+      mtop = fmaxf(mtop, fabsf(m[q]));
+      rtop = fmaxf(rtop, v[q]);
+      if (sizeof(P) == 2 && k.stochastic) p[q] = round_bf16(p[q], ((bits[q] >> 21) << 5) + 16);
     }
   }
   store_n<N>((P *)e.p + i, left, p);

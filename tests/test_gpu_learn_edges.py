@@ -94,3 +94,38 @@ def test_norm_rows_whose_squares_are_below_fp32(rvq, dev, d):
     x = x * torch.tensor([1.0, 1e-15, 1e-19, 1e-22, 1e-25, 0.0], device=dev)[:, None]
     for odt in (F32, F8):
         norm_tests._check_norm(rvq, x, None, None, odt, eps=2.0 ** -149)
+
+
+def _state8(st, i=0):
+    n = st.m[i].numel()
+    rep = lambda s: s.double().repeat_interleave(256)[:n]  # noqa: E731
+    return st.m[i].double() * rep(st.m_scale[i]), st.v[i].double() * rep(st.v_scale[i])
+
+
+def test_adamw_keeps_nan_in_8_bit_roots(rvq, dev):
+    for gdt in (F32, BF16):
+        for seed in (None, 3):
+            p, g = torch.ones(1000, device=dev), torch.ones(1000, device=dev, dtype=gdt)
+            g[300] = NAN
+            st = rvq.rvq_adamw_init([p], 8, 0.0)
+            rvq.rvq_adamw_step(st, [g], 1, 0.1, seed=seed)
+            m, r = _state8(st)
+            for x in (p, m, r):
+                bad = torch.isnan(x)
+                assert bad[300] and int(bad.sum()) == 1
+            rvq.rvq_adamw_step(st, [torch.ones_like(g)], 2, 0.1, seed=seed)
+            m, r = _state8(st)
+            assert torch.isnan(p[300]) and torch.isnan(m[300]) and torch.isnan(r[300])
+            assert int(torch.isnan(p).sum()) == 1
+
+
+def test_adamw_stores_small_8_bit_roots(rvq, dev):
+    # v = 1e-3 * 4^-k in fp32 (a unit is 2^-149 from k = 59 on)
+    for k in (40, 58, 60, 62, 64, 66):
+        g = torch.full((256,), 2.0 ** -k, device=dev)
+        st = rvq.rvq_adamw_init([torch.zeros(256, device=dev)], 8)
+        rvq.rvq_adamw_step(st, [g], 1, 0.1)
+        _, r = _state8(st)
+        want = (1.0 - 0.999) ** 0.5 * 2.0 ** -k
+        # the moment is off by a unit or two of 2^-149 and 4 U, its root by half as much
+        assert torch.all((r - want).abs() <= want * (2.0 ** -149 / want ** 2 + 6 * ref.U)), k
