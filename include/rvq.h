@@ -394,7 +394,10 @@ rvq_status rvq_embed_tokens_backward(const void *dout, rvq_dtype dout_dtype, con
  * held as e4m3 values with an fp32 scale for every 256 consecutive elements
  * of the tensor: m = m[i] m_scale[i / 256], sqrt(v) = v[i] v_scale[i / 256],
  * where a scale is max(largest magnitude of the 256 / 448, 2^-100).  All
- * zeros is a valid start of both.
+ * zeros is a valid start of both.  Squares may leave fp32: sqrt(v) of 8-bit
+ * states has fp32's whole range, and a v of 32-bit states is held at the
+ * largest fp32 at most.  A moment that is not finite (of such a gradient) is
+ * stored as NaN in 8 bits and leaves the scale to the other elements.
  *
  * Rounding.  8-bit states and bf16 parameters are rounded to nearest even, or
  * where `stochastic` is nonzero at random (up with the probability of the

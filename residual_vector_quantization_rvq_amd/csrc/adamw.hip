@@ -114,16 +114,23 @@ __device__ __forceinline__ float round_bf16(float v, uint32_t random16) {
   return __uint_as_float((__float_as_uint(v) + random16) & 0xffff0000u);
 }
 
-// the largest of the 32 lanes of a half wave
-__device__ __forceinline__ float half_wave_max(float v) {
-#define RVQ_ROR(N) \
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + N, 0xf, 0xf, false)))
+// op over the 32 lanes of a half wave
+template <typename Op>
+__device__ __forceinline__ int over_half_wave(int v, Op op) {
+#define RVQ_ROR(N) v = op(v, __builtin_amdgcn_mov_dpp(v, 0x120 + N, 0xf, 0xf, false))
   RVQ_ROR(8);
   RVQ_ROR(4);
   RVQ_ROR(2);
   RVQ_ROR(1);
 #undef RVQ_ROR
-  return fmaxf(v, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401f)));  // lane ^ 16
+  return op(v, __builtin_amdgcn_ds_swizzle(v, 0x401f));  // lane ^ 16
+}
+__device__ __forceinline__ float half_wave_max(float v) {
+  return __int_as_float(over_half_wave(
+      __float_as_int(v), [](int a, int b) { return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b))); }));
+}
+__device__ __forceinline__ uint32_t half_wave_max(uint32_t v) {
+  return (uint32_t)over_half_wave((int)v, [](int a, int b) { return (int)max((uint32_t)a, (uint32_t)b); });
 }
 
 // 8 e4m3 bytes at p; `left` of them exist (the others read as zero)
@@ -178,15 +185,32 @@ __device__ __forceinline__ float updated(float p, float m, float root, const Con
 }
 
 // The nearest fp32 to sqrt(v), by one Newton step from the hardware's 1 /
-// sqrt(v), for finite v; NaN stays NaN.  A v below kSmall, whose remainder fp32
-// does not hold, is taken for zero: small_sqrt is for those.
-constexpr float kSmall = 0x1p-96f;
+// sqrt(v), for v of 2^-96 (whose remainder fp32 still holds) and up; smaller
+// ones count as zero, and infinity and NaN give NaN.
 __device__ __forceinline__ float nearest_sqrt(float v) {
   const float y = __builtin_amdgcn_rsqf(v), s = v * y;
   const float r = __builtin_fmaf(-s, s, v);
-  return v < kSmall ? 0.f : __builtin_fmaf(r, 0.5f * y, s);
+  return v < 0x1p-96f ? 0.f : __builtin_fmaf(r, 0.5f * y, s);
 }
-__device__ __forceinline__ float small_sqrt(float v) { return nearest_sqrt(v * 0x1p64f) * 0x1p-32f; }
+// A factor for roots of an element with the larger of its old root and gradient
+// given: its square is within fp32 then, and a power of two changes no digit.
+constexpr float kRootUnit = 0x1p32f, kLargeUnit = 0x1p-70f;
+__device__ __forceinline__ float root_unit(float largest) {
+  return largest < 0x1p31f ? kRootUnit : kLargeUnit;
+}
+
+// An element's step where squares leave fp32, in the unit u: vu is the old and
+// then the new v times u^2, root the new root times u.  Returns the new parameter.
+__device__ __forceinline__ float large_step(float p, float g, float m, float &vu, float &root, float u,
+                                            const Consts &k, float decay) {
+  Consts ku = k;
+  ku.eps *= u;
+  m *= u;
+  moments(g * u, m, vu, ku);
+  root = nearest_sqrt(vu);
+  return updated(p, m, root, ku, decay);
+}
+constexpr float kLargest = 0x1.fffffep127f;
 
 }  // namespace
 
@@ -290,11 +314,29 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, C
   for (int j = 0; j < J; ++j) {
     const int64_t i = i0 + j * kThreads * N;
     const uint32_t word = round_word(base, i);  // a piece does not reach over a multiple of 2^32
+    float top = 0.f;
 #pragma unroll
     for (int q = 0; q < N; ++q) {
       moments(g[j][q] * c, m[j][q], v[j][q], k);
       p[j][q] = updated(p[j][q], m[j][q], __builtin_amdgcn_sqrtf(v[j][q]), k, e.decay);
-      if (sizeof(P) == 2 && k.stochastic)
+      top = fmaxf(top, v[j][q]);
+    }
+    if (top == INFINITY) {
+      // Squares beyond fp32: once more, in a smaller unit; a finite v is held at
+      // the largest fp32 at most.
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        if (v[j][q] != INFINITY) continue;
+        float vu = ((const float *)e.v)[i + q] * kLargeUnit * kLargeUnit, root;
+        p[j][q] = large_step(load_f32((const P *)e.p, i + q), g[j][q] * c, ((const float *)e.m)[i + q], vu, root,
+                             kLargeUnit, k, e.decay);
+        v[j][q] = vu * (1.f / kLargeUnit) * (1.f / kLargeUnit);
+        if (v[j][q] == INFINITY && vu < INFINITY) v[j][q] = kLargest;
+      }
+    }
+    if (sizeof(P) == 2 && k.stochastic) {
+#pragma unroll
+      for (int q = 0; q < N; ++q)
         p[j][q] = round_bf16(p[j][q], ((mix(word + q * kWordStep) >> 21) << 5) + 16);
     }
     store_n<N>((P *)e.p + i, left[j], p[j]);
@@ -330,48 +372,68 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
   if (!clip.part) c = step_factor(clip, k);
   if (!(c == c)) return;
   const uint32_t base = tensor_bits(k.key, t.first + at);
-  float mtop = 0.f, rtop = 0.f;
+  float mtop = 0.f;
+  uint32_t rtop = 0;
   const uint32_t word = round_word(base, i);
-  uint32_t bits[N], least = UINT32_MAX;
+  uint32_t bits[N];
+  // Roots times kRootUnit, and v times its square: nothing in fp32's range is
+  // too small then, and where v times that overflows the root is NaN.
+  Consts ku = k;
+  ku.c2 *= kRootUnit * kRootUnit;
+  ku.rk2 *= 1.f / kRootUnit;
+  const float svu = sv * kRootUnit;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
     m[q] *= sm;
-    v[q] *= sv;
+    v[q] *= svu;
     v[q] *= v[q];
-    moments(g[q] * c, m[q], v[q], k);
-    least = min(least, __float_as_uint(v[q]) - 1);  // zero does not count
+    moments(g[q] * c, m[q], v[q], ku);
     v[q] = nearest_sqrt(v[q]);  // the root from here on
-    p[q] = updated(p[q], m[q], v[q], k, e.decay);
+    p[q] = updated(p[q], m[q], v[q], ku, e.decay);
     mtop = fmaxf(mtop, fabsf(m[q]));
-    rtop = fmaxf(rtop, v[q]);
+    rtop = max(rtop, __float_as_uint(v[q]) & 0x7fffffffu);  // NaN is the largest
     if (k.stochastic) {
       bits[q] = mix(word + q * kWordStep);
       if (sizeof(P) == 2) p[q] = round_bf16(p[q], ((bits[q] >> 21) << 5) + 16);
     }
   }
-  if (least < __float_as_uint(kSmall) - 1) {  // hardly ever: a lane's elements once more, with the roots of any v
-    mtop = rtop = 0.f;
-    load_n<N>((const P *)e.p + i, left, p);
-    load_n<N>((const G *)e.g + i, left, g);
-    load_f8x8((const uint8_t *)e.m + i, left, m);
-    load_f8x8((const uint8_t *)e.v + i, left, v);
+  float nsm = half_wave_max(mtop), nsv = __uint_as_float(half_wave_max(rtop)), unit = kRootUnit;
+  if (!(nsv < INFINITY)) {
+    // A gradient or root beyond 2^31, infinity or NaN in the block: its elements
+    // once more, each in a unit of its own.  What is not finite is stored as NaN,
+    // and its block's scales are the others'.
+    unit = 1.f;
+#pragma unroll 1
+    for (int at = 0; at < N; ++at) {  // not unrolled: hardly ever run, and it would take the registers of two waves
+      const float gq = at < left ? load_f32((const G *)e.g, i + at) * c : 0.f;
+      const float m0 = at < left ? f8_to_f32(((const uint8_t *)e.m)[i + at]) * sm : 0.f;
+      const float r0 = at < left ? f8_to_f32(((const uint8_t *)e.v)[i + at]) * sv : 0.f;
+      const float u = root_unit(fmaxf(r0, fabsf(gq)));
+      float vu = (r0 * u) * (r0 * u), root;
+      float pq = large_step(at < left ? load_f32((const P *)e.p, i + at) : 0.f, gq, m0, vu, root, u, k, e.decay);
+      if (sizeof(P) == 2 && k.stochastic) pq = round_bf16(pq, ((mix(word + at * kWordStep) >> 21) << 5) + 16);
+      root = fminf(root * (1.f / u), kLargest) + (root - root);  // above it by rounding alone
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        p[q] = q == at ? pq : p[q];
+        v[q] = q == at ? root : v[q];
+      }
+    }
+    mtop = 0.f;
+    float top = 0.f;
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      m[q] *= sm;
-      v[q] *= sv;
-      v[q] *= v[q];
-      moments(g[q] * c, m[q], v[q], k);
-      v[q] = v[q] < kSmall ? small_sqrt(v[q]) : nearest_sqrt(v[q]);
-      p[q] = updated(p[q], m[q], v[q], k, e.decay);
+      if (!(fabsf(m[q]) < INFINITY)) m[q] = NAN;
       mtop = fmaxf(mtop, fabsf(m[q]));
-      rtop = fmaxf(rtop, v[q]);
-      if (sizeof(P) == 2 && k.stochastic) p[q] = round_bf16(p[q], ((bits[q] >> 21) << 5) + 16);
+      top = fmaxf(top, v[q]);
     }
+    nsm = half_wave_max(mtop);
+    nsv = half_wave_max(top);
   }
   store_n<N>((P *)e.p + i, left, p);
   if (e.copy) store_n<N>(e.copy + i, left, p);
-  const float nsm = fmaxf(half_wave_max(mtop) * kF8Unit, kScaleMin);
-  const float nsv = fmaxf(half_wave_max(rtop) * kF8Unit, kScaleMin);
+  nsm = fmaxf(nsm * kF8Unit, kScaleMin);
+  nsv = fmaxf(nsv * kF8Unit, kScaleMin * unit);
   const float im = 1.f / nsm, iv = 1.f / nsv;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
@@ -402,7 +464,7 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
   store_8_bytes((uint8_t *)e.v + i, left, qv);
   if ((threadIdx.x & 31) == 0) {
     e.ms[block] = nsm;
-    e.vs[block] = nsv;
+    e.vs[block] = nsv * (1.f / unit);
   }
 }
 

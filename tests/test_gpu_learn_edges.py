@@ -129,3 +129,69 @@ def test_adamw_stores_small_8_bit_roots(rvq, dev):
         want = (1.0 - 0.999) ** 0.5 * 2.0 ** -k
         # the moment is off by a unit or two of 2^-149 and 4 U, its root by half as much
         assert torch.all((r - want).abs() <= want * (2.0 ** -149 / want ** 2 + 6 * ref.U)), k
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("pdt,gdt", [(F32, F32), (F32, BF16), (BF16, BF16)], ids=["ff", "fb", "bb"])
+def test_adamw_gradients_whose_squares_leave_fp32(rvq, dev, bits, pdt, gdt):
+    # without a norm: the definition is finite, and so has every element to be
+    for seed in (None, 5):
+        for top in (1e18, 3e19, 6e20, 1e25, 1e32, 3e38):
+            t = adamw_tests._tensors([3000, 5, 2048], pdt, gdt, bits, dev, seed=11, copies=True)
+            for g in t["g"]:
+                g[::7] = (g[::7].double() * (top / 0.6)).clamp(-3.3e38, 3.3e38).to(gdt)
+                g[4] = top
+                assert torch.isfinite(g).all()
+            _check_saturating(rvq, t, bits, pdt, seed)
+    # the state itself past that range, and no gradient
+    t = adamw_tests._tensors([1000], pdt, gdt, bits, dev, seed=12)
+    t["g"][0].zero_()
+    if bits == 8:
+        t["vs"][0][1], t["ms"][0][1] = 1e34, 1e33
+    else:
+        t["v"][0][300:500], t["m"][0][300:500] = 3e38, 1e18
+    _check_saturating(rvq, t, bits, pdt, None)
+
+
+def _check_saturating(rvq, t, bits, pdt, seed):
+    """_check of the step's own tests with v held at fp32's largest value at most."""
+    before = [(p.clone(), *adamw_tests._moments(t, bits, i)) for i, p in enumerate(t["p"])]
+    st = rvq.rvq_adamw_init(t["p"], bits, adamw_tests.DECAY, t["copies"], t["m"], t["v"], t["ms"], t["vs"])
+    rvq.rvq_adamw_step(st, t["g"], 3, adamw_tests.LR, adamw_tests.BETAS, adamw_tests.EPS, seed=seed)
+    torch.cuda.synchronize()
+    for i, (p0, m0, v0) in enumerate(before):
+        p, m, v, upd = ref.adamw(p0, t["g"][i], m0, v0, 3, adamw_tests.LR, adamw_tests.BETAS, adamw_tests.EPS,
+                                 adamw_tests.DECAY)
+        pb = 4 * ref.U * p0.double().abs() + 24 * ref.U * upd.abs()
+        if pdt == BF16:
+            pb = pb + (1 if seed is None else 2) * ref.BF16_HALF * (1 + 2 ** -7) * p.abs()
+        ref.close(t["p"][i], p, pb, f"p[{i}]")
+        if t["copies"]:
+            assert torch.equal(t["copies"][i], t["p"][i].to(BF16)), f"copy[{i}]"
+        mb = 4 * ref.U * (m0.abs() + t["g"][i].double().abs())
+        if bits == 32:
+            ref.close(t["m"][i], m, mb, f"m[{i}]")
+            ref.close(t["v"][i], v.clamp(max=MAX), 6 * ref.U * v.clamp(max=MAX), f"v[{i}]")
+            continue
+        for q, scale, x, xb in ((t["m"][i], t["ms"][i], m, mb),
+                                (t["v"][i], t["vs"][i], v.sqrt(), 6 * ref.U * v.sqrt())):
+            peak = ref.blocks(x).abs().amax(1) / 448
+            ref.close(scale, peak.clamp(min=ref.SCALE_MIN), ref.blocks(xb).amax(1) / 448 + 4 * ref.U * peak,
+                      f"scale[{i}]")
+            per = scale.double().repeat_interleave(256)[:x.numel()]
+            y = (x / per).clamp(-448, 448)
+            # up to a whole step of the grid: a root beside an m that is not zero is not stored as zero
+            ref.close(q.float(), y, ref.f8_step(y) * (1 + 2 ** -8) + xb / per + 4 * ref.U * y.abs(), f"state[{i}]")
+
+
+def test_adamw_infinite_gradient_stays_alone(rvq, dev):
+    for bits in (32, 8):
+        for seed in (None, 3):
+            p, g = torch.ones(600, device=dev), torch.ones(600, device=dev)
+            g[300], g[400] = INF, -INF
+            st = rvq.rvq_adamw_init([p], bits, 0.0)
+            rvq.rvq_adamw_step(st, [g], 1, 0.1, seed=seed)
+            rvq.rvq_adamw_step(st, [torch.ones_like(g)], 2, 0.1, seed=seed)
+            bad = torch.isnan(p)
+            assert bad[300] and bad[400] and int(bad.sum()) == 2, (bits, seed)
+            assert torch.allclose(p[~bad], torch.full_like(p[~bad], 0.8), rtol=0.02)
