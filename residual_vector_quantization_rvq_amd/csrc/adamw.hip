@@ -207,7 +207,7 @@ __device__ __forceinline__ float large_step(float p, float g, float m, float &vu
   ku.eps *= u;
   m *= u;
   moments(g * u, m, vu, ku);
-  root = nearest_sqrt(vu);
+  root = vu < INFINITY ? nearest_sqrt(vu) : vu;
   return updated(p, m, root, ku, decay);
 }
 constexpr float kLargest = 0x1.fffffep127f;

@@ -195,3 +195,16 @@ def test_adamw_infinite_gradient_stays_alone(rvq, dev):
             bad = torch.isnan(p)
             assert bad[300] and bad[400] and int(bad.sum()) == 2, (bits, seed)
             assert torch.allclose(p[~bad], torch.full_like(p[~bad], 0.8), rtol=0.02)
+
+
+def test_adamw_infinite_32_bit_v_leaves_the_decay(rvq, dev):
+    # a state from elsewhere: m / infinity is 0
+    for pdt in (F32, BF16):
+        p, v = torch.ones(300, device=dev, dtype=pdt), torch.ones(300, device=dev)
+        v[100] = INF
+        st = rvq.rvq_adamw_init([p], 32, 0.5, m=[torch.zeros(300, device=dev)], v=[v])
+        for g in (1.0, 1e30):
+            p.fill_(1.0)
+            rvq.rvq_adamw_step(st, [torch.full((300,), g, device=dev)], 2, 0.5)
+            assert p[100].item() == 0.75 and st.v[0][100].item() == INF
+            assert torch.isfinite(p).all() and torch.all(p[:100].float() < 0.75)
