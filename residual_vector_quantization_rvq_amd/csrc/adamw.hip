@@ -214,8 +214,9 @@ constexpr float kLargest = 0x1.fffffep127f;
 
 }  // namespace
 
-// Sums of squares of the gradients: eight of a lane in fp32, the rest in fp64.
-// A workgroup takes consecutive chunks.
+// Sums of squares of the gradients, in fp64: in fp32 an element above 1.8e19 would
+// make a finite norm infinite and the step be skipped, and those below 1e-23
+// would be lost.  A workgroup takes consecutive chunks.
 template <typename G>
 __global__ __launch_bounds__(kThreads) void adamw_norm_kernel(NormTable t, double *part) {
   __shared__ double red[kThreads / 64];
@@ -230,10 +231,8 @@ __global__ __launch_bounds__(kThreads) void adamw_norm_kernel(NormTable t, doubl
     if (i < e.n) {
       float g[8];
       load_n<8>((const G *)e.g + i, (int)(e.n - i < 8 ? e.n - i : 8), g);
-      float c = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) c += g[j] * g[j];
-      s += (double)c;
+      for (int j = 0; j < 8; ++j) s = __builtin_fma((double)g[j], (double)g[j], s);
     }
   }
   s = wave_sum_f64(s);

@@ -208,3 +208,22 @@ def test_adamw_infinite_32_bit_v_leaves_the_decay(rvq, dev):
             rvq.rvq_adamw_step(st, [torch.full((300,), g, device=dev)], 2, 0.5)
             assert p[100].item() == 0.75 and st.v[0][100].item() == INF
             assert torch.isfinite(p).all() and torch.all(p[:100].float() < 0.75)
+
+
+@pytest.mark.parametrize("gdt", [F32, BF16], ids=["f", "b"])
+def test_adamw_norm_of_gradients_whose_squares_leave_fp32(rvq, dev, gdt):
+    for size in (1e-35, 1e-30, 1e-24, 1e-20, 1.0, 1e19, 1e25, 1e36):
+        g = (torch.randn(70001, generator=torch.Generator(device=dev).manual_seed(1), device=dev) * size).to(gdt)
+        want = float(g.double().square().sum().sqrt())
+        p = torch.zeros(70001, device=dev)
+        st = rvq.rvq_adamw_init([p], 32)
+        norm = rvq.rvq_adamw_step(st, [g], 1, 0.1, eps=1e-12, max_norm=1.0)
+        if want > 3.4e38:
+            assert float(norm) == INF and torch.all(p == 0)
+            continue
+        # fp32's own unit where the norm is below 2^-126
+        assert abs(float(norm) - want) <= 16 * ref.U * want + 2.0 ** -149, size
+        f = min(1.0, 1.0 / (want + 1e-6))
+        want_m = 0.1 * g.double() * f
+        # f is below fp32's normal values from a norm of 2^126 on
+        ref.close(st.m[0], want_m, (16 * ref.U + 2.0 ** -149 / f) * want_m.abs() + 2.0 ** -148, f"m {size}")
