@@ -110,8 +110,14 @@ template <int Byte>
 __device__ __forceinline__ int random_f8(float v, uint32_t random, int w) {
   return __builtin_amdgcn_cvt_sr_fp8_f32(v, (int)random, w, Byte);
 }
-__device__ __forceinline__ float round_bf16(float v, uint32_t random16) {
+// v rounded to bf16 at random: of a NaN, only one with zeros in the places that go,
+// out of whose significand the bits cannot carry
+__device__ __forceinline__ float round_number_bf16(float v, uint32_t random16) {
   return __uint_as_float((__float_as_uint(v) + random16) & 0xffff0000u);
+}
+// ... of any NaN
+__device__ __forceinline__ float round_bf16(float v, uint32_t random16) {
+  return v == v ? round_number_bf16(v, random16) : v;
 }
 
 // op over the 32 lanes of a half wave
@@ -393,11 +399,12 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
     rtop = max(rtop, __float_as_uint(v[q]) & 0x7fffffffu);  // NaN is the largest
     if (k.stochastic) {
       bits[q] = mix(word + q * kWordStep);
-      if (sizeof(P) == 2) p[q] = round_bf16(p[q], ((bits[q] >> 21) << 5) + 16);
+      // a NaN of the gradient or a scale is seen to below, those of e4m3 and bf16 have zeros
+      if (sizeof(P) == 2) p[q] = round_number_bf16(p[q], ((bits[q] >> 21) << 5) + 16);
     }
   }
   float nsm = half_wave_max(mtop), nsv = __uint_as_float(half_wave_max(rtop)), unit = kRootUnit;
-  if (!(nsv < INFINITY)) {
+  if (!(nsv < INFINITY && sm == sm)) {
     // A gradient or root beyond 2^31, infinity or NaN in the block: its elements
     // once more, each in a unit of its own.  What is not finite is stored as NaN,
     // and its block's scales are the others'.

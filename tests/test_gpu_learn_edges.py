@@ -227,3 +227,37 @@ def test_adamw_norm_of_gradients_whose_squares_leave_fp32(rvq, dev, gdt):
         want_m = 0.1 * g.double() * f
         # f is below fp32's normal values from a norm of 2^126 on
         ref.close(st.m[0], want_m, (16 * ref.U + 2.0 ** -149 / f) * want_m.abs() + 2.0 ** -148, f"m {size}")
+
+
+def test_adamw_rounds_nan_to_nan(rvq, dev):
+    # NaN with every bit of the significand set (memory that was filled with
+    # ones), which random bits added to it would carry out of
+    words = torch.tensor([0x7fffffff, -1, 0x7fc00000, 0x7f800001, -0x800000 + 1, 0x7fff8000], dtype=torch.int32)
+    nans = words.view(F32).to(dev)
+    assert torch.isnan(nans).all()
+    n = 64 * nans.numel()
+    for bits in (32, 8):
+        for seed in (1, 2):
+            p = torch.ones(2 * n, dtype=BF16, device=dev)
+            g = torch.ones(2 * n, device=dev)
+            g[:n] = nans.repeat(64)
+            st = rvq.rvq_adamw_init([p], bits, 0.0)
+            rvq.rvq_adamw_step(st, [g], 1, 0.1, seed=seed)
+            assert torch.isnan(p[:n]).all() and torch.isfinite(p[n:]).all(), bits
+            # and of a parameter
+            p = torch.full((n,), -1, dtype=torch.int16, device=dev).view(BF16)
+            st = rvq.rvq_adamw_init([p], bits, 0.0)
+            rvq.rvq_adamw_step(st, [torch.ones(n, device=dev)], 1, 0.1, seed=seed)
+            assert torch.isnan(p).all()
+            # and of a state
+            if bits == 32:
+                continue
+            code = torch.tensor([0x7f, 0xff], dtype=torch.uint8).view(F8).to(dev)
+            for mv, scale in ((code, 1.0), (torch.ones(2, device=dev).to(F8), nans[1])):
+                p = torch.ones(512, dtype=BF16, device=dev)
+                one = lambda: torch.ones(2, device=dev)  # noqa: E731
+                m = mv.view(torch.uint8).repeat(256).view(F8)
+                v = torch.ones(512, device=dev).to(F8)
+                st = rvq.rvq_adamw_init([p], 8, 0.0, m=[m], v=[v], m_scale=[one() * scale], v_scale=[one()])
+                rvq.rvq_adamw_step(st, [torch.ones(512, device=dev)], 2, 0.1, seed=seed)
+                assert torch.isnan(p).all()
