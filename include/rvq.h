@@ -394,7 +394,11 @@ rvq_status rvq_embed_tokens_backward(const void *dout, rvq_dtype dout_dtype, con
  * held as e4m3 values with an fp32 scale for every 256 consecutive elements
  * of the tensor: m = m[i] m_scale[i / 256], sqrt(v) = v[i] v_scale[i / 256],
  * where a scale is max(largest magnitude of the 256 / 448, 2^-100).  All
- * zeros is a valid start of both.  Squares may leave fp32: sqrt(v) of 8-bit
+ * zeros is a valid start of both.  Where m is not stored as 0, a sqrt(v) above 0
+ * is not either: it becomes at least the smallest e4m3 value, 2^-9 of its scale.
+ * (lr m / eps is a step without bounds: a state that a caller builds should
+ * keep to that too.)
+ * Squares may leave fp32: sqrt(v) of 8-bit
  * states has fp32's whole range, and a v of 32-bit states is held at the
  * largest fp32 at most.  A moment that is not finite (of such a gradient) is
  * stored as NaN in 8 bits and leaves the scale to the other elements.
@@ -402,7 +406,8 @@ rvq_status rvq_embed_tokens_backward(const void *dout, rvq_dtype dout_dtype, con
  * Rounding.  8-bit states and bf16 parameters are rounded to nearest even, or
  * where `stochastic` is nonzero at random (up with the probability of the
  * remainder), from bits that depend on (seed, step, tensor's place in the
- * call, element) only.  With beta2 = 0.999, 8-bit states need it: one step
+ * call, element) only; roots below the smallest e4m3 value take m's bits, so that
+ * they are seldom raised.  With beta2 = 0.999, 8-bit states need it: one step
  * moves sqrt(v) by far less than half a step of its grid.
  */
 typedef struct rvq_adamw_tensor {

@@ -110,6 +110,14 @@ template <int Byte>
 __device__ __forceinline__ int random_f8(float v, uint32_t random, int w) {
   return __builtin_amdgcn_cvt_sr_fp8_f32(v, (int)random, w, Byte);
 }
+// v[q0 .. q0 + 3] with the bits of each
+template <int N, typename Bits>
+__device__ __forceinline__ uint32_t random_f8x4(const float (&v)[N], int q0, Bits bits) {
+  int w = random_f8<0>(v[q0], bits(q0), 0);
+  w = random_f8<1>(v[q0 + 1], bits(q0 + 1), w);
+  w = random_f8<2>(v[q0 + 2], bits(q0 + 2), w);
+  return (uint32_t)random_f8<3>(v[q0 + 3], bits(q0 + 3), w);
+}
 // v rounded to bf16 at random: of a NaN, only one with zeros in the places that go,
 // out of whose significand the bits cannot carry
 __device__ __forceinline__ float round_number_bf16(float v, uint32_t random16) {
@@ -118,6 +126,20 @@ __device__ __forceinline__ float round_number_bf16(float v, uint32_t random16) {
 // ... of any NaN
 __device__ __forceinline__ float round_bf16(float v, uint32_t random16) {
   return v == v ? round_number_bf16(v, random16) : v;
+}
+
+// The least e4m3 value: a root above 0 is stored as it and not as 0 where its m
+// is not stored as 0.  The two are rounded apart, and m / 0 would make the next
+// step lr m / eps: over 10^6 times lr in blocks with elements 10^4 times larger.
+constexpr float kF8Least = 0x1p-9f;
+template <int N>
+__device__ __forceinline__ uint32_t raise_roots(uint32_t qm, uint32_t qv, const float (&v)[N], int q0) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t byte = 0x7fu << (8 * b);
+    if ((qm & byte) && !(qv & byte) && v[q0 + b] > 0.f) qv |= 1u << (8 * b);
+  }
+  return qv;
 }
 
 // op over the 32 lanes of a half wave
@@ -396,7 +418,7 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
     v[q] = nearest_sqrt(v[q]);  // the root from here on
     p[q] = updated(p[q], m[q], v[q], ku, e.decay);
     mtop = fmaxf(mtop, fabsf(m[q]));
-    rtop = max(rtop, __float_as_uint(v[q]) & 0x7fffffffu);  // NaN is the largest
+    rtop = max(rtop, __float_as_uint(v[q]));  // of either sign, NaN is above the rest
     if (k.stochastic) {
       bits[q] = mix(word + q * kWordStep);
       // a NaN of the gradient or a scale is seen to below, those of e4m3 and bf16 have zeros
@@ -447,23 +469,30 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
     v[q] = nearest_quotient(v[q], nsv, iv);
   }
   u32x2 qm, qv;
+  const auto m_bits = [&](int q) { return (bits[q] << 22) | 0x200000u; };
+  const auto v_bits = [&](int q) { return ((bits[q] << 11) & 0xffe00000u) | 0x100000u; };
   if (k.stochastic) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      int wm = 0, wv = 0;
-#define RVQ_RANDOM(B)                                                                       \
-  wm = random_f8<B>(m[4 * h + B], (bits[4 * h + B] << 22) | 0x200000u, wm);                 \
-  wv = random_f8<B>(v[4 * h + B], ((bits[4 * h + B] << 11) & 0xffe00000u) | 0x100000u, wv);
-      RVQ_RANDOM(0) RVQ_RANDOM(1) RVQ_RANDOM(2) RVQ_RANDOM(3)
-#undef RVQ_RANDOM
-      qm[h] = (uint32_t)wm;
-      qv[h] = (uint32_t)wv;
+      qm[h] = random_f8x4(m, 4 * h, m_bits);
+      qv[h] = random_f8x4(v, 4 * h, v_bits);
     }
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       qm[h] = pack_f8x4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]);
       qv[h] = pack_f8x4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+    }
+  }
+  float least = v[0];
+#pragma unroll
+  for (int q = 1; q < N; ++q) least = fminf(least, v[q]);
+  if (least < kF8Least) {  // only such a root can have become 0
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (k.stochastic)
+        qv[h] = random_f8x4(v, 4 * h, [&](int q) { return v[q] < kF8Least ? m_bits(q) : v_bits(q); });
+      qv[h] = raise_roots(qm[h], qv[h], v, 4 * h);
     }
   }
   store_8_bytes((uint8_t *)e.m + i, left, qm);

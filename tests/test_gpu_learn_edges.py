@@ -261,3 +261,57 @@ def test_adamw_rounds_nan_to_nan(rvq, dev):
                 st = rvq.rvq_adamw_init([p], 8, 0.0, m=[m], v=[v], m_scale=[one() * scale], v_scale=[one()])
                 rvq.rvq_adamw_step(st, [torch.ones(512, device=dev)], 2, 0.1, seed=seed)
                 assert torch.isnan(p).all()
+
+
+@pytest.mark.parametrize("seed", [7, None], ids=["random", "nearest"])
+@pytest.mark.parametrize("small,gone", [(1e-4, 0.99), (1e-5, 0.0), (1e-5, 0.5), (1e-6, 0.0), (1e-8, 0.5)])
+def test_adamw_8_bit_steps_are_bounded_in_blocks_of_unlike_magnitudes(rvq, dev, seed, small, gone):
+    # One element a block has gradients of standard deviation 1, the others of
+    # `small`; a share `gone` of the steps has none.  With exact moments and as
+    # many steps behind it, |m| / sqrt(v) is at most (Cauchy-Schwarz)
+    # sqrt(0.1^2 / 0.001 / (1 - 0.81 / 0.999)) = 7.27.  Storing may add one
+    # step of m's grid, and leaves the root at least the smallest step of its
+    # own where m is not zero: at most 7.27 times the ratio of the two scales,
+    # itself at most 7.27, more; and either grid's rounding is 1/8 of a value.
+    blocks, steps = 64, 300
+    g0 = torch.Generator(device=dev).manual_seed(3)
+    std = torch.full((blocks, 256), small, device=dev)
+    std[:, 0] = 1.0
+    p = torch.zeros(blocks * 256, device=dev)
+    st = rvq.rvq_adamw_init([p], 8, 0.0)
+    worst = torch.zeros((), device=dev)
+    for t in range(1, steps + 1):
+        g = torch.randn((blocks, 256), generator=g0, device=dev) * std
+        g *= torch.rand((blocks, 1), generator=g0, device=dev) >= gone
+        old = p.clone()
+        rvq.rvq_adamw_step(st, [g.view(-1)], t, 1.0, eps=1e-12, seed=None if seed is None else seed + t)
+        # the bias corrections' quotient is at most its limit, 1, from the first step on
+        worst = torch.maximum(worst, (p - old).abs().max())
+    assert float(worst) <= 2 * 7.27 * 1.125 ** 2, float(worst)
+    m, r = st.m[0].float(), st.v[0].float()
+    assert torch.all(r[m != 0] > 0)
+
+
+def test_adamw_8_bit_roots_stay_above_zero_beside_m(rvq, dev):
+    # The first element of a block grows: the others' roots come to 2.7e-4 of the
+    # new scale, under half the smallest e4m3 value, their m to many steps.  In the
+    # second block m is zero: the same roots may become 0.  In the third they
+    # are 0 already, by no rounding of the step's, and stay so.
+    m, v = torch.zeros(768, device=dev), torch.full((768,), 2.0 ** -9, device=dev)
+    m[:256], m[512:], v[512:] = 1.0, 1.0, 0.0
+    m[::256], v[::256] = 448.0, 448.0
+    for seed in (None, 1, 2):
+        p = torch.zeros(768, device=dev)
+        g = torch.zeros(768, device=dev)
+        g[::256] = 1e5
+        one = lambda: torch.ones(3, device=dev)  # noqa: E731
+        st = rvq.rvq_adamw_init([p], 8, 0.0, m=[m.to(F8)], v=[v.to(F8)], m_scale=[one()], v_scale=[one()])
+        rvq.rvq_adamw_step(st, [g], 5, 0.0, seed=seed)
+        root = st.v[0].float()
+        assert torch.all(st.m[0].float()[1:256] > 0)
+        assert torch.all(root[1:256] == 2.0 ** -9)
+        assert torch.all(root[513:] == 0)
+        if seed is None:
+            assert torch.all(root[257:512] == 0)
+        else:  # 0.140 of them go up
+            assert abs(float((root[257:512] > 0).double().mean()) - 0.140) <= 6 * 0.0217
