@@ -503,17 +503,18 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
   }
 }
 
-// a launch of the norm takes kNormTable tensors, or fewer of over 2^34
-// elements together: no more launches than tensors
-size_t adam_part_count(int count) { return (size_t)(count > 0 ? count : 1) * kNormGroups; }
+// every launch of the norm but the last takes kNormTable tensors
+size_t adam_part_count(int count) { return (size_t)(count > 0 ? ceil_div(count, kNormTable) : 1) * kNormGroups; }
 
 namespace {
 
-// Consecutive tables of all tensors, one launch(table) each; of at most
-// kMaxChunks workgroups, the most that one tensor has (2^34 elements).
+// Consecutive tables of all tensors, one launch(table) each, of at most `most`
+// chunks.  A step has a workgroup for each: kMaxChunks, as many as one tensor has
+// (2^34 elements).  The norm's workgroups take many each.
 constexpr int64_t kMaxChunks = (int64_t)1 << 23;
+static_assert(kNormTable * kMaxChunks < (int64_t)1 << 32, "chunk0 is 32-bit");
 template <typename TableT, typename Fill, typename Launch>
-void for_each_table(const rvq_adamw_tensor *t, int count, int size, Fill fill, Launch launch) {
+void for_each_table(const rvq_adamw_tensor *t, int count, int size, int64_t most, Fill fill, Launch launch) {
   for (int first = 0; first < count;) {
     TableT tab;
     tab.first = first;
@@ -521,7 +522,7 @@ void for_each_table(const rvq_adamw_tensor *t, int count, int size, Fill fill, L
     int i = 0;
     for (; i < size && first + i < count; ++i) {
       const int64_t n = t[first + i].numel, more = ceil_div(n, kChunk);
-      if (i > 0 && chunks + more > kMaxChunks) break;
+      if (i > 0 && chunks + more > most) break;
       fill(tab.e[i], t[first + i]);
       tab.e[i].n = n;
       tab.e[i].chunk0 = (uint32_t)chunks;
@@ -538,7 +539,7 @@ template <typename P, typename G>
 void launch_step(const rvq_adamw_tensor *t, const AdamArgs &a, const Consts &k, Clip clip,
                  hipStream_t s) {
   for_each_table<Table>(
-      t, a.count, kTable,
+      t, a.count, kTable, kMaxChunks,
       [&](Entry &e, const rvq_adamw_tensor &x) {
         e.p = x.param;
         e.g = x.grad;
@@ -562,7 +563,7 @@ template <typename G>
 int64_t launch_norm(const rvq_adamw_tensor *t, const AdamArgs &a, hipStream_t s) {
   int64_t parts = 0;
   for_each_table<NormTable>(
-      t, a.count, kNormTable, [&](NormEntry &e, const rvq_adamw_tensor &x) { e.g = x.grad; },
+      t, a.count, kNormTable, kNormTable * kMaxChunks, [&](NormEntry &e, const rvq_adamw_tensor &x) { e.g = x.grad; },
       [&](const NormTable &tab) {
         const unsigned groups = tab.chunks < (unsigned)kNormGroups ? tab.chunks : kNormGroups;
         adamw_norm_kernel<G><<<dim3(groups), kThreads, 0, s>>>(tab, a.part + parts);

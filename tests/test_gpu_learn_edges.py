@@ -315,3 +315,19 @@ def test_adamw_8_bit_roots_stay_above_zero_beside_m(rvq, dev):
             assert torch.all(root[257:512] == 0)
         else:  # 0.140 of them go up
             assert abs(float((root[257:512] > 0).double().mean()) - 0.140) <= 6 * 0.0217
+
+
+def test_adamw_norm_over_several_launches(rvq, dev):
+    # more tensors than a launch of the norm takes, more workgroups' sums than a step adds itself
+    g0 = torch.Generator().manual_seed(8)
+    for count, top in ((400, 60), (500, 9000), (161, 40000)):
+        sizes = [int(x) for x in torch.randint(0, top, (count,), generator=g0)]
+        sizes[7] = 5000000
+        g = [torch.full((n,), 0.5, device=dev) for n in sizes]
+        p = [torch.zeros(n, device=dev) for n in sizes]
+        st = rvq.rvq_adamw_init(p)
+        norm = rvq.rvq_adamw_step(st, g, 1, 0.1, max_norm=1e9)
+        want = 0.5 * sum(sizes) ** 0.5
+        assert abs(float(norm) - want) <= 16 * ref.U * want
+        for x in st.m:
+            assert torch.all((x - 0.05).abs() <= 1e-8)

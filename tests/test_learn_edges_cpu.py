@@ -1,0 +1,24 @@
+"""Host-side checks of the calls that train the token embedding, beside those of
+test_learn_abi_cpu.py (no GPU needed)."""
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "residual_vector_quantization_rvq_amd", "librvq.so")
+
+
+@pytest.fixture(scope="module")
+def rvq():
+    if not os.path.exists(LIB):
+        import __graft_entry__
+        __graft_entry__._builder().build()
+    import residual_vector_quantization_rvq_amd as m
+    return m
+
+
+def test_adamw_workspace_is_that_of_its_launches(rvq):
+    # a launch of the norm takes 160 tensors and leaves 2,048 sums of 8 bytes
+    for count in (0, 1, 96, 160, 161, 10000, 1000000):
+        launches = max(1, -(-count // 160))
+        assert launches * 16384 <= rvq.rvq_adamw_workspace_size(count) <= launches * 16384 + 1024
