@@ -582,8 +582,6 @@ class AdamWState:
         words[:, 7] = self._numels
         words.view(np.float32)[:, 16] = weight_decay
         self._grads = words[:, 1]
-        self._workspace = torch.empty(rvq_adamw_workspace_size(len(params)), dtype=torch.uint8,
-                                      device=self.device)
 
 
 def rvq_adamw_init(params: Sequence[torch.Tensor], state_bits: int = 32, weight_decay=0.01,
@@ -689,13 +687,15 @@ def rvq_adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: int, 
         raise ValueError("max_norm must be positive")
     if need_norm or max_norm is not None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
-        ws, nbytes = state._workspace.data_ptr(), state._workspace.numel()
+        # of this call's stream: a buffer kept from another one could be given away under a running step
+        nbytes = rvq_adamw_workspace_size(len(table))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     opt = _AdamWOptions(lr, betas[0], betas[1], eps, step, grad_scale,
                         0.0 if max_norm is None else max_norm, 0 if seed is None else 1,
                         0 if seed is None else seed & 0xFFFFFFFF)
     _on_device(dev, _lib.rvq_adamw_step, ctypes.addressof(table), len(table),
                _dtype_code(state.param_dtype), gcode, state.state_bits, ctypes.byref(opt),
-               _address(norm), ws, nbytes, _raw_stream(dev))
+               _address(norm), _address(ws), nbytes, _raw_stream(dev))
     return norm
 
 

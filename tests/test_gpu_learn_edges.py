@@ -331,3 +331,21 @@ def test_adamw_norm_over_several_launches(rvq, dev):
         assert abs(float(norm) - want) <= 16 * ref.U * want
         for x in st.m:
             assert torch.all((x - 0.05).abs() <= 1e-8)
+
+
+def test_adamw_state_holds_no_buffer_of_its_own(rvq, dev):
+    # what a step works in belongs to the step's stream: a buffer that the state
+    # had made on its own stream would be given away when the state is dropped,
+    # whatever still ran elsewhere
+    p = [torch.zeros(300, device=dev)]
+    st = rvq.rvq_adamw_init(p, 8)
+    known = {t.data_ptr() for ts in (st.params, st.m, st.v, st.m_scale, st.v_scale) for t in ts}
+    held = [t for x in vars(st).values() for t in (x if isinstance(x, (tuple, list)) else [x])
+            if isinstance(t, torch.Tensor)]
+    assert {t.data_ptr() for t in held} <= known
+    side = torch.cuda.Stream(device=dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(side):
+        norm = rvq.rvq_adamw_step(st, [torch.ones(300, device=dev)], 1, 0.1, max_norm=1.0)
+    side.synchronize()
+    assert abs(float(norm) - 300 ** 0.5) <= 1e-4
