@@ -14,10 +14,11 @@
 // come out in token order.  One launch and no scan over workgroups; its work
 // grows with (rows / kRange) x T, a few per cent of the sums'.
 //
-// embed_sum_kernel sums each row's tokens.  The list is also cut in segments
-// of equal length: a row with more tokens than a segment (a hot codeword, a
-// padding token) is summed segment by segment, and embed_join_kernel adds
-// the pieces in order.
+// embed_sum_kernel sums each row's tokens.  Each table's part of the list is also
+// cut in segments of equal length: a row with more tokens than a segment (a hot
+// codeword, a padding token) is summed segment by segment, and embed_join_kernel
+// adds the pieces in order.  Where a row is cut depends on its table's IDs alone,
+// whichever other tables are asked for.
 //
 // What bounds it: every row of the tables is written once, and a visual
 // token's row of dout is read once for each of its L levels.  Those reads miss
@@ -63,11 +64,12 @@ constexpr int kMaxGroups = 1 << 22;
 // Length of a segment of the list.  A row of at most this many tokens is
 // summed by one wave in one go, at about 0.2 us a token (160 tokens of a row of
 // 2324: 54 us with segments of 256, 26 us of 64); sequences of up to kShort
-// tokens are spared the third launch.  No more than 2048 segments, as each is
-// looked at whether or not a long row is in it.
-int64_t segment_length(int64_t T, int64_t positions) {
+// tokens are spared the third launch.  About 2048 segments at most, as each is
+// looked at whether or not a long row is in it.  By the IDs' shape, and not by the
+// tables that are asked for: a row's sum is cut the same way for all of them.
+int64_t segment_length(int64_t T, int L) {
   if (T <= kShort) return kShort;
-  const int64_t h = round_up(ceil_div(positions, 2048), 64);
+  const int64_t h = round_up(ceil_div(T * (L + 1), 2048), 64);
   return h < 64 ? 64 : h;
 }
 
@@ -80,21 +82,25 @@ struct Tables {
   int L, K;        // L = 0: no level gradients
   int64_t V;       // 0: no text gradient
   int64_t T;
-  int64_t rows, positions, seg, segments;
+  int64_t rows, positions;
+  int64_t seg, parts, segments;  // segments: parts of each table, or none at all
   bool keys;       // the IDs are laid out by table first
 };
 
-Tables tables_of(int64_t T, int L, int K, int64_t V) {
+// L levels' tables and the text table of IDs of L_ids levels
+Tables tables_of(int64_t T, int L_ids, int L, int K, int64_t V) {
   Tables t;
   t.L = L;
   t.K = K;
   t.V = V;
   t.T = T;
   t.rows = (int64_t)L * K + V;
-  t.positions = (L + (V > 0 ? 1 : 0)) * T;
-  t.seg = segment_length(T, t.positions);
+  const int tables = L + (V > 0 ? 1 : 0);
+  t.positions = tables * T;
+  t.seg = segment_length(T, L_ids);
+  t.parts = ceil_div(T, t.seg);
   // a row has at most T tokens: none is long if T is not
-  t.segments = T > t.seg ? ceil_div(t.positions, t.seg) : 0;
+  t.segments = T > t.seg ? tables * t.parts : 0;
   // the layout is a launch of its own, which short sequences do not win back
   t.keys = T > kKeysFrom;
   return t;
@@ -352,6 +358,13 @@ struct Piece {
   }
 };
 
+// positions [p0, p1) of segment s
+__device__ __forceinline__ void segment_at(const Tables &tb, int64_t s, int64_t &p0, int64_t &p1) {
+  const int64_t table = (uint32_t)s / (uint32_t)tb.parts, part = s - table * tb.parts;
+  p0 = table * tb.T + part * tb.seg;
+  p1 = part + 1 < tb.parts ? p0 + tb.seg : (table + 1) * tb.T;
+}
+
 template <typename G>
 __device__ __forceinline__ G *row_of(const EmbedGradArgs &a, const Tables &tb, int64_t row) {
   const int64_t levels = (int64_t)tb.L * tb.K;
@@ -399,8 +412,8 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Ta
     G *o = nullptr;         // the row that is being summed
     float *part = nullptr;  // instead of it: a long row's piece
     if (u < 2 * tb.segments) {
-      const int64_t p0 = (u >> 1) * tb.seg;
-      const int64_t p1 = p0 + tb.seg < tb.positions ? p0 + tb.seg : tb.positions;
+      int64_t p0, p1;
+      segment_at(tb, u >> 1, p0, p1);
       const int ra = a.row[p0], row = u & 1 ? a.row[p1 - 1] : ra;
       if (row < 0 || (u & 1 && row == ra) || a.place[row].y <= tb.seg) continue;
       const int64_t b = a.place[row].x, e = b + a.place[row].y;
@@ -501,7 +514,8 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Ta
 template <typename G>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a, Tables tb) {
   const int64_t s = blockIdx.x;
-  const int64_t p0 = s * tb.seg, p1 = p0 + tb.seg < tb.positions ? p0 + tb.seg : tb.positions;
+  int64_t p0, p1;
+  segment_at(tb, s, p0, p1);
   const int row = a.row[p1 - 1];
   if (row < 0 || a.place[row].y <= tb.seg || a.place[row].x < p0) return;
   const int64_t end = (int64_t)a.place[row].x + a.place[row].y;
@@ -510,13 +524,14 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a, T
   const int c = blockIdx.y * kThreads + threadIdx.x;
   if (c >= a.D) return;
   float v = a.part[first * a.D + c];
-  for (int64_t q = s + 1; q * tb.seg < end; ++q) v += a.part[2 * q * a.D + c];
+  int64_t q = s + 1;  // the segments of the row's table
+  for (p1 = p0 + tb.seg; p1 < end; p1 += tb.seg, ++q) v += a.part[2 * q * a.D + c];
   if (a.accumulate) v += load_f32(o, c);
   store_f32(o, c, v);
 }
 
-EmbedGradLayout embed_grad_layout(int64_t T, int L, int K, int64_t V, int D) {
-  const Tables tb = tables_of(T, L, K, V);
+EmbedGradLayout embed_grad_layout(int64_t T, int L_ids, int L, int K, int64_t V, int D) {
+  const Tables tb = tables_of(T, L_ids, L, K, V);
   EmbedGradLayout w;
   w.place = 0;
   w.token = w.place + al256((size_t)tb.rows * sizeof(int2));
@@ -560,7 +575,7 @@ static hipError_t launch_sums(const EmbedGradArgs &a, const Tables &tb, hipStrea
 }
 
 hipError_t launch_embed_grad(const EmbedGradArgs &a, bool x_bf16, bool g_bf16, hipStream_t s) {
-  const Tables tb = tables_of(a.T, a.dlevel ? a.L : 0, a.K, a.dtext ? a.V : 0);
+  const Tables tb = tables_of(a.T, a.L, a.dlevel ? a.L : 0, a.K, a.dtext ? a.V : 0);
   if (tb.rows == 0) return hipSuccess;
   const int64_t units = (int64_t)tb.L * ceil_div(tb.K, kRange) + ceil_div(tb.V, kRange);
   if (tb.keys) embed_keys_kernel<<<dim3((unsigned)ceil_div(a.T, kThreads)), kThreads, 0, s>>>(a, tb);

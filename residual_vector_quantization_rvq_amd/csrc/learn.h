@@ -263,7 +263,8 @@ struct EmbedGradArgs {
 struct EmbedGradLayout {
   size_t place, token, row, part, keys, total;
 };
-EmbedGradLayout embed_grad_layout(int64_t T, int L, int K, int64_t V, int D);
+// L: the level tables that are asked for (all L_ids or none)
+EmbedGradLayout embed_grad_layout(int64_t T, int L_ids, int L, int K, int64_t V, int D);
 hipError_t launch_embed_grad(const EmbedGradArgs &a, bool x_bf16, bool g_bf16, hipStream_t s);
 
 struct AdamArgs {

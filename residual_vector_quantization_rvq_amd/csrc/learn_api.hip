@@ -147,9 +147,9 @@ rvq_status rvq_embed_tokens_backward_workspace_size(int64_t T, int32_t L, int32_
   RVQ_TRY(check_tables(T, L, K, V, D));
   if (!bytes) return fail(RVQ_ERR_INVALID_ARGUMENT, "bytes must not be NULL");
   // whichever tables a call asks for
-  size_t most = embed_grad_layout(T, L, K, V, D).total;
-  const size_t levels = embed_grad_layout(T, L, K, 0, D).total;
-  const size_t text = V > 0 ? embed_grad_layout(T, 0, K, V, D).total : 0;
+  size_t most = embed_grad_layout(T, L, L, K, V, D).total;
+  const size_t levels = embed_grad_layout(T, L, L, K, 0, D).total;
+  const size_t text = V > 0 ? embed_grad_layout(T, L, 0, K, V, D).total : 0;
   if (levels > most) most = levels;
   if (text > most) most = text;
   *bytes = most;
@@ -181,7 +181,7 @@ rvq_status rvq_embed_tokens_backward(const void *dout, rvq_dtype dout_dtype, con
   if (workspace_bytes < want)
     return fail(RVQ_ERR_WORKSPACE_TOO_SMALL,
                 "embedding gradient workspace needs %zu bytes (got %zu)", want, workspace_bytes);
-  const EmbedGradLayout w = embed_grad_layout(T, dlevel ? L : 0, K, dtext ? V : 0, D);
+  const EmbedGradLayout w = embed_grad_layout(T, L, dlevel ? L : 0, K, dtext ? V : 0, D);
   char *ws = (char *)workspace;
   EmbedGradArgs a = {dout, ids, is_visual, T, L, K, D, V, dlevel, dtext, accumulate != 0, bad_ids,
                      (int2 *)(ws + w.place),

@@ -349,3 +349,21 @@ def test_adamw_state_holds_no_buffer_of_its_own(rvq, dev):
         norm = rvq.rvq_adamw_step(st, [torch.ones(300, device=dev)], 1, 0.1, max_norm=1.0)
     side.synchronize()
     assert abs(float(norm) - 300 ** 0.5) <= 1e-4
+
+
+def test_embed_grad_bits_do_not_depend_on_which_tables_are_asked_for(rvq, dev):
+    # rows longer than a segment of the list, in both tables, with random values
+    for T, L, K, V, D, dtype, gdt in ((3000, 3, 7, 5, 72, BF16, F32), (9001, 5, 40, 11, 40, F32, F32),
+                                      (60000, 8, 9, 3, 16, F32, F32), (5000, 2, 6, 4, 264, BF16, BF16)):
+        dout, ids, vis = embed_tests._problem(T, L, K, V, D, dtype, dev, text=0.5, hot=0.3, whole=False)
+        level, text = rvq.rvq_embed_tokens_backward(dout, ids, K, vis, V, gdt)
+        only, _ = rvq.rvq_embed_tokens_backward(dout, ids, K, vis, V, gdt, need_text=False)
+        _, alone = rvq.rvq_embed_tokens_backward(dout, ids, K, vis, V, gdt, need_level=False)
+        none, _ = rvq.rvq_embed_tokens_backward(dout, ids, K, vis, 0, gdt)
+        raw = lambda t: t.contiguous().view(torch.uint8)  # noqa: E731
+        assert torch.equal(raw(only), raw(level)) and torch.equal(raw(none), raw(level)), (T, "level")
+        assert torch.equal(raw(alone), raw(text)), (T, "text")
+        if gdt == F32:
+            wl, wt, al, at, _ = ref.embed_grad(dout, ids, vis, L, K, V)
+            ref.close(level, wl, T * ref.U * al, "level")
+            ref.close(text, wt, T * ref.U * at, "text")
