@@ -381,6 +381,13 @@ def _address(t: Optional[torch.Tensor]) -> Optional[int]:
 _CODES = {torch.float32: RVQ_F32, torch.bfloat16: RVQ_BF16}
 
 
+def _need_sizes(**sizes: int) -> None:
+    """Sizes that the library takes as 32-bit numbers (ctypes would cut them off)."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} must be below 2^31 (got {v})")
+
+
 def _need_like(name: str, t: torch.Tensor, x: torch.Tensor) -> None:
     """t has x's shape, type and device and is contiguous."""
     if not (isinstance(t, torch.Tensor) and t.dtype is x.dtype and t.shape == x.shape and
@@ -430,6 +437,8 @@ def rvq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
     if x.dim() != 2:
         raise ValueError("x must be [n, d]")
     dev, (n, d) = x.device, x.shape
+    if d >= 2 ** 31:
+        _need_sizes(d=d)
     code = _dtype_code(x.dtype)
     if residual is not None:
         _need_like("residual", residual, x)
@@ -455,6 +464,7 @@ def rvq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
 
 @functools.lru_cache(maxsize=256)
 def rvq_rms_norm_backward_workspace_size(n: int, d: int) -> int:
+    _need_sizes(d=d)
     out = ctypes.c_size_t()
     _check(_lib.rvq_rms_norm_backward_workspace_size(n, d, ctypes.byref(out)))
     return out.value
@@ -475,6 +485,8 @@ def rvq_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     if dy.dim() != 2:
         raise ValueError("dy must be [n, d]")
     n, d = dy.shape
+    if d >= 2 ** 31:
+        _need_sizes(d=d)
     code = _dtype_code(dy.dtype)
     _need_like("h", h, dy)
     _need_shape("rstd", rstd, (n,), torch.float32, dev)
@@ -498,6 +510,7 @@ def rvq_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
 
 @functools.lru_cache(maxsize=256)
 def rvq_embed_tokens_backward_workspace_size(T: int, L: int, K: int, V: int, D: int) -> int:
+    _need_sizes(L=L, K=K, V=V, D=D)
     out = ctypes.c_size_t()
     _check(_lib.rvq_embed_tokens_backward_workspace_size(T, L, K, V, D, ctypes.byref(out)))
     return out.value
@@ -523,6 +536,7 @@ def rvq_embed_tokens_backward(dout: torch.Tensor, ids: torch.Tensor, K: int,
         raise ValueError("dout must be [T, D] and ids int32 [T, L]")
     T, D = dout.shape
     L = ids.shape[1]
+    nbytes = rvq_embed_tokens_backward_workspace_size(T, L, K, V, D)
     need_text = need_text and V > 0
     if not need_level and not need_text:
         raise ValueError("no table's gradient is asked for")
@@ -535,7 +549,6 @@ def rvq_embed_tokens_backward(dout: torch.Tensor, ids: torch.Tensor, K: int,
             raise ValueError("is_visual must be uint8 or bool [T]")
     if bad_ids is not None:
         _need_shape("bad_ids", bad_ids, (1,), torch.int32, dev)
-    nbytes = rvq_embed_tokens_backward_workspace_size(T, L, K, V, D)
     for name, wanted, given, shape in (("level_grad", need_level, level_grad, (L, K, D)),
                                        ("text_grad", need_text, text_grad, (V, D))):
         if given is not None:
@@ -651,6 +664,7 @@ def rvq_adamw_init(params: Sequence[torch.Tensor], state_bits: int = 32, weight_
 
 @functools.lru_cache(maxsize=256)
 def rvq_adamw_workspace_size(count: int) -> int:
+    _need_sizes(count=count)
     out = ctypes.c_size_t()
     _check(_lib.rvq_adamw_workspace_size(count, ctypes.byref(out)))
     return out.value

@@ -367,3 +367,17 @@ def test_embed_grad_bits_do_not_depend_on_which_tables_are_asked_for(rvq, dev):
             wl, wt, al, at, _ = ref.embed_grad(dout, ids, vis, L, K, V)
             ref.close(level, wl, T * ref.U * al, "level")
             ref.close(text, wt, T * ref.U * at, "text")
+
+
+def test_learning_calls_refuse_sizes_past_32_bits(rvq, dev):
+    wide = torch.empty((0, 2 ** 32 + 8), device=dev)
+    rstd, ids = torch.empty(0, device=dev), torch.empty((0, 2), dtype=torch.int32, device=dev)
+    dout = torch.empty((0, 8), device=dev)
+    for call in (lambda: rvq.rvq_rms_norm(wide), lambda: rvq.rvq_rms_norm_backward(wide, wide, rstd),
+                 lambda: rvq.rvq_rms_norm_backward(wide, wide, rstd, need_dweight=False),
+                 lambda: rvq.rvq_embed_tokens_backward(wide, ids, 3, V=4, need_level=False),
+                 lambda: rvq.rvq_embed_tokens_backward(dout, ids, 2 ** 32 + 5, V=4, need_level=False),
+                 lambda: rvq.rvq_embed_tokens_backward(dout, ids, -2 ** 32 + 5, V=4, need_level=False),
+                 lambda: rvq.rvq_embed_tokens_backward(dout, ids, 5, V=2 ** 64 + 4, need_level=False)):
+        with pytest.raises((ValueError, rvq.RVQError)):
+            call()

@@ -22,3 +22,14 @@ def test_adamw_workspace_is_that_of_its_launches(rvq):
     for count in (0, 1, 96, 160, 161, 10000, 1000000):
         launches = max(1, -(-count // 160))
         assert launches * 16384 <= rvq.rvq_adamw_workspace_size(count) <= launches * 16384 + 1024
+
+
+def test_sizes_past_32_bits_are_refused(rvq):
+    # ctypes would hand their low bits to the library
+    for call in (lambda: rvq.rvq_rms_norm_backward_workspace_size(4, 2 ** 32 + 8),
+                 lambda: rvq.rvq_embed_tokens_backward_workspace_size(4, 2, 2 ** 32 + 3, 0, 8),
+                 lambda: rvq.rvq_embed_tokens_backward_workspace_size(4, 2, 3, 0, 2 ** 32 + 8),
+                 lambda: rvq.rvq_embed_tokens_backward_workspace_size(4, 2, 3, 2 ** 64 + 4, 8),
+                 lambda: rvq.rvq_adamw_workspace_size(2 ** 32 + 1)):
+        with pytest.raises((ValueError, rvq.RVQError)):
+            call()
