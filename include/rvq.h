@@ -422,9 +422,9 @@ typedef struct rvq_adamw_tensor {
 } rvq_adamw_tensor;
 
 typedef struct rvq_adamw_options {
-    double lr, beta1, beta2, eps;  /* eps >= 1e-12 */
+    double lr, beta1, beta2, eps;  /* lr / (1 - beta1^step) within fp32, eps >= 1e-12 */
     int64_t step;                  /* 1 for the first */
-    double grad_scale;             /* 1 for none */
+    double grad_scale;             /* 1 for none; within fp32 */
     double max_norm;               /* <= 0: no clipping */
     int32_t stochastic;
     uint32_t seed;

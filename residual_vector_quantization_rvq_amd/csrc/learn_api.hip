@@ -219,8 +219,13 @@ rvq_status rvq_adamw_step(const rvq_adamw_tensor *tensors, int32_t count, rvq_dt
     return fail(RVQ_ERR_INVALID_ARGUMENT, "eps must be finite and at least 1e-12 (got %g)", o.eps);
   if (o.step < 1)
     return fail(RVQ_ERR_INVALID_ARGUMENT, "step must be >= 1 (got %lld)", (long long)o.step);
-  if (!std::isfinite(o.grad_scale) || !std::isfinite(o.max_norm))
-    return fail(RVQ_ERR_INVALID_ARGUMENT, "grad_scale and max_norm must be finite");
+  if (!std::isfinite((float)o.grad_scale) || !std::isfinite(o.max_norm))
+    return fail(RVQ_ERR_INVALID_ARGUMENT, "grad_scale and max_norm must be finite, grad_scale in fp32");
+  // as the kernels take them, in fp32
+  const float lr1 = (float)(o.lr / (1.0 - std::pow(o.beta1, (double)o.step)));
+  const float rk2 = (float)(1.0 / std::sqrt(1.0 - std::pow(o.beta2, (double)o.step)));
+  if (!std::isfinite(lr1) || !std::isfinite(rk2))
+    return fail(RVQ_ERR_INVALID_ARGUMENT, "lr / (1 - beta1^step) must be within fp32");
   const size_t ps = dtype_bytes(param_dtype), ss = state_bits == 8 ? 1 : 4;
   bool any = false;
   for (int32_t i = 0; i < count; ++i) {
@@ -267,10 +272,11 @@ rvq_status rvq_adamw_step(const rvq_adamw_tensor *tensors, int32_t count, rvq_dt
   a.c2 = (float)(1.0 - o.beta2);
   a.eps = (float)o.eps;
   a.lr = o.lr;
-  a.lr1 = (float)(o.lr / (1.0 - std::pow(o.beta1, (double)o.step)));
-  a.rk2 = (float)(1.0 / std::sqrt(1.0 - std::pow(o.beta2, (double)o.step)));
+  a.lr1 = lr1;
+  a.rk2 = rk2;
   a.grad_scale = (float)o.grad_scale;
   a.max_norm = (float)o.max_norm;
+  if (o.max_norm > 0.0 && a.max_norm == 0.f) a.max_norm = 0x1p-149f;  // 0 would be no clipping
   a.stochastic = o.stochastic != 0;
   a.key = adam_key((uint32_t)o.seed, (uint32_t)o.step);
   a.grad_norm = grad_norm;

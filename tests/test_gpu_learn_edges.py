@@ -381,3 +381,15 @@ def test_learning_calls_refuse_sizes_past_32_bits(rvq, dev):
                  lambda: rvq.rvq_embed_tokens_backward(dout, ids, 5, V=2 ** 64 + 4, need_level=False)):
         with pytest.raises((ValueError, rvq.RVQError)):
             call()
+
+
+def test_adamw_options_outside_fp32(rvq, dev):
+    p, g = torch.ones(10, device=dev), torch.ones(10, device=dev)
+    st = rvq.rvq_adamw_init([p], 32, 0.0)
+    for bad in (dict(grad_scale=1e39), dict(lr=1e38, betas=(0.9999, 0.999)), dict(lr=1e40)):
+        with pytest.raises(rvq.RVQError) as e:
+            rvq.rvq_adamw_step(st, [g], **{**dict(step=1, lr=0.1), **bad})
+        assert e.value.status == 1
+    # a positive max_norm below fp32's smallest value clips all the same
+    rvq.rvq_adamw_step(st, [g], 1, 0.1, max_norm=1e-60)
+    assert float(st.m[0].abs().max()) <= 1e-44

@@ -1,5 +1,6 @@
 """Host-side checks of the calls that train the token embedding, beside those of
 test_learn_abi_cpu.py (no GPU needed)."""
+import ctypes
 import os
 
 import pytest
@@ -33,3 +34,18 @@ def test_sizes_past_32_bits_are_refused(rvq):
                  lambda: rvq.rvq_adamw_workspace_size(2 ** 32 + 1)):
         with pytest.raises((ValueError, rvq.RVQError)):
             call()
+
+
+def test_adamw_options_outside_fp32(rvq):
+    lib = rvq.raw_library()
+
+    def call(**kw):
+        o = dict(lr=0.1, beta1=0.9, beta2=0.99, eps=1e-8, step=1, grad_scale=1.0, max_norm=0.0, stochastic=0, seed=0)
+        o.update(kw)
+        opt = rvq._AdamWOptions(*o.values())
+        return lib.rvq_adamw_step(None, 0, 0, 0, 32, ctypes.byref(opt), None, None, 0, None)
+    for bad in (dict(grad_scale=1e39), dict(grad_scale=-1e39), dict(lr=1e39), dict(lr=1e38, beta1=0.9999)):
+        assert call(**bad) == 1, bad
+    for ok in (dict(grad_scale=3e38), dict(lr=1e37), dict(max_norm=1e-60, lr=0.0)):
+        # nothing to do, so nothing is launched (max_norm asks for a workspace first)
+        assert call(**ok) == (1 if "max_norm" in ok else 0), ok
