@@ -17,6 +17,10 @@ Learning the token embedding:
   rvq_rms_norm_backward(dy, h, rstd, weight)  -> (dx, dweight)
   rvq_embed_tokens_backward(dout, ids, K)     -> (level_grad [L, K, D], text_grad [V, D])
   rvq_adamw_init(params) -> state;  rvq_adamw_step(state, grads, step, lr)
+
+Results belong to no autograd graph.  The calls that learn take a tensor that
+requires a gradient under torch.no_grad() only (as in the forward and backward of
+a torch.autograd.Function), so that no gradient is lost without a word.
 """
 from __future__ import annotations
 
@@ -378,6 +382,13 @@ def _address(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _refuse_grad() -> None:
+    """For tensors that require a gradient, which would end here, unseen by autograd."""
+    if torch.is_grad_enabled():
+        raise ValueError("a tensor requires a gradient, which this call does not record: call it under "
+                         "torch.no_grad() (with its backward call) or on detached tensors")
+
+
 _CODES = {torch.float32: RVQ_F32, torch.bfloat16: RVQ_BF16}
 
 
@@ -447,6 +458,9 @@ def rvq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
     elif residual is not None:
         sum_out = torch.empty_like(x)
     wcode = _need_weight(weight, d, dev)
+    if (x.requires_grad or weight is not None and weight.requires_grad or
+            residual is not None and residual.requires_grad):
+        _refuse_grad()
     odt = x.dtype if out_dtype is None else out_dtype
     f8 = odt is torch.float8_e4m3fn
     ocode = RVQ_F8E4M3 if f8 else _dtype_code(odt)
@@ -497,6 +511,9 @@ def rvq_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
         out = torch.empty_like(dy)
     else:
         _need_like("out", out, dy)
+    if (dy.requires_grad or h.requires_grad or weight is not None and weight.requires_grad or
+            dsum is not None and dsum.requires_grad):
+        _refuse_grad()
     dweight, ws, nbytes = None, None, 0
     if need_dweight:
         dweight = torch.empty(d, dtype=torch.float32, device=dev)
@@ -540,6 +557,8 @@ def rvq_embed_tokens_backward(dout: torch.Tensor, ids: torch.Tensor, K: int,
     need_text = need_text and V > 0
     if not need_level and not need_text:
         raise ValueError("no table's gradient is asked for")
+    if dout.requires_grad:
+        _refuse_grad()
     code, gcode = _dtype_code(dout.dtype), _dtype_code(grad_dtype)
     if is_visual is not None:
         _need_cuda("is_visual", is_visual, dev)

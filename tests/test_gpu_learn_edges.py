@@ -393,3 +393,25 @@ def test_adamw_options_outside_fp32(rvq, dev):
     # a positive max_norm below fp32's smallest value clips all the same
     rvq.rvq_adamw_step(st, [g], 1, 0.1, max_norm=1e-60)
     assert float(st.m[0].abs().max()) <= 1e-44
+
+
+def test_learning_calls_refuse_tensors_that_want_a_gradient(rvq, dev):
+    x, rstd = torch.ones((4, 32), device=dev), torch.ones(4, device=dev)
+    ids = torch.zeros((4, 2), dtype=torch.int32, device=dev)
+    want = lambda t: t.clone().requires_grad_()  # noqa: E731
+    w = torch.ones(32, device=dev)
+    calls = (lambda: rvq.rvq_rms_norm(want(x)), lambda: rvq.rvq_rms_norm(x, want(w)),
+             lambda: rvq.rvq_rms_norm(x, residual=want(x)), lambda: rvq.rvq_rms_norm_backward(want(x), x, rstd),
+             lambda: rvq.rvq_rms_norm_backward(x, want(x), rstd, w), lambda: rvq.rvq_rms_norm_backward(x, x, rstd, want(w)),
+             lambda: rvq.rvq_rms_norm_backward(x, x, rstd, dsum=want(x)),
+             lambda: rvq.rvq_embed_tokens_backward(want(x), ids, 3))
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    with torch.no_grad():
+        for call in calls:
+            call()
+    rvq.rvq_rms_norm(want(x).detach())
+    # parameters of an optimizer want gradients as a matter of course
+    p = torch.nn.Parameter(torch.ones(8, device=dev))
+    rvq.rvq_adamw_step(rvq.rvq_adamw_init([p]), [torch.ones(8, device=dev)], 1, 0.1)
