@@ -415,3 +415,37 @@ def test_learning_calls_refuse_tensors_that_want_a_gradient(rvq, dev):
     # parameters of an optimizer want gradients as a matter of course
     p = torch.nn.Parameter(torch.ones(8, device=dev))
     rvq.rvq_adamw_step(rvq.rvq_adamw_init([p]), [torch.ones(8, device=dev)], 1, 0.1)
+
+
+# launch forms that the other cases do not reach
+FORMS = [
+    # four waves an index workgroup with the IDs laid out by table: 2,048 < T <= 8,192, more than 512 workgroups
+    (3000, 16, 16384, 1001, 8), (8192, 16, 16384, 40, 4), (2049, 1, 300000, 7, 12),
+    # several rows in turn for a part of a wave (W < 64), rows longer than a segment among them
+    (1000, 2, 70000, 9, 8), (3000, 4, 40000, 1000, 24), (900, 1, 140000, 11, 128), (1500, 8, 20000, 100, 200),
+    # more than four rows a wave
+    (900, 3, 200000, 5, 520),
+    # three slabs of columns in panels of two and one, and five in panels
+    (41000, 1, 50, 3, 1300), (50000, 2, 30, 40, 2500),
+]
+
+
+@pytest.mark.parametrize("case", FORMS, ids=lambda c: "T%d_L%d_K%d_V%d_D%d" % c)
+def test_embed_grad_launch_forms(rvq, dev, case):
+    T, L, K, V, D = case
+    for dtype, gdt in ((BF16, F32), (F32, BF16)):
+        dout, ids, vis = embed_tests._problem(T, L, K, V, D, dtype, dev)
+        # hot rows: a table's first, one in the middle of a group of rows, and two next to each other
+        hot = torch.rand(T, generator=torch.Generator(device=dev).manual_seed(2), device=dev)
+        for k, at in enumerate((0, K // 2 + 1, K // 2 + 2, min(5, K - 1))):
+            ids[(hot >= 0.12 * k) & (hot < 0.12 * (k + 1))] = at
+        if V:
+            ids[vis == 0, 0] = (ids[vis == 0, 0] % V).int()
+        embed_tests._check_exact(rvq, dout, ids, vis, K, V, gdt)
+        # added to what is there
+        wl, wt, _, _, _ = ref.embed_grad(dout, ids, vis, L, K, V)
+        l0, t0 = torch.full((L, K, D), 2.0, device=dev, dtype=gdt), torch.full((V, D), -1.0, device=dev, dtype=gdt)
+        level, text = rvq.rvq_embed_tokens_backward(dout, ids, K, vis, V, gdt, level_grad=l0, text_grad=t0,
+                                                    accumulate=True)
+        assert torch.equal(level, (wl + 2.0).to(gdt)) and torch.equal(text, (wt - 1.0).to(gdt))
+        del wl, wt, l0, t0, level, text
