@@ -43,19 +43,21 @@ constexpr int kShort = 256;        // tokens; see segment_length
 // the streams (39,731 x 4096 bf16, 325 MB: 776 us in one panel, 753 in panels
 // of 160 MB, 747 of 100 MB, 749 of 60 MB).
 constexpr int64_t kPanelBytes = (int64_t)100 << 20;
-// From here on the IDs are laid out by table first: a launch of 4 to 5 us (2,048
-// tokens of 8 levels: index 12.2 us without, 8.4 us with; 5,003 of 16: 26 and 18).
-constexpr int kKeysFrom = 2048;
+// Above it the IDs are laid out by table first, a launch of 4 to 5 us.  Index, and
+// layout with index: 2,049 tokens of 8 levels 9.2 and 11.5 us, 3,000 11.4 and 11.5,
+// 4,096 12.5 and 12.1; of 16 levels 2,049 15.3 and 14.7, 5,003 25.5 and 20.4.
+constexpr int kKeysAbove = 3072;
 // An index workgroup has sixteen waves, or four: where there are more than the
 // 512 workgroups of sixteen that the device holds and up to kFewTokens tokens
-// (5,003 tokens, 514 workgroups: 35 us with sixteen waves, 27 with four; 39,731
-// tokens, 256 workgroups: 44 and 84), and for the shortest sequences (the call
-// of 256 tokens 11.5 and 10.7 us, of 600 17.0 and 15.7).
-constexpr int kFewTokens = 8192;
-constexpr int kVeryFewTokens = 1024;
+// (514 workgroups: 4,096 tokens 14.7 us with sixteen waves and 13.1 with four, 5,003
+// 16.0 and 15.3, 7,000 17.4 and 18.4; 256 workgroups: 39,731 tokens 29 and 71), and
+// for the shortest sequences (256 tokens 6.2 and 5.8 us, 512 6.4 and 6.5).
+constexpr int kFewTokens = 6144;
+constexpr int kVeryFewTokens = 384;
 // Up to so many of a wave's 64 IDs in the workgroup's rows are told apart one by
-// one (about 8 instructions each), more of them bit by bit (80): 37 and 45 us
-// where four of 64 are (39,731 tokens of 8 levels of 8,192).
+// one (about 8 instructions each), more of them bit by bit (80).  All bit by bit:
+// 39,731 tokens of 8 levels of 8,192, four of 64 IDs, 37.6 us and not 29.2; all one
+// by one: 600 tokens of levels of 256, all of them, 12.6 us and not 6.8.
 constexpr int kFewHits = 12;
 constexpr int kNone = INT32_MIN;   // not an ID of this table
 constexpr int kThreads = 256;
@@ -102,7 +104,7 @@ Tables tables_of(int64_t T, int L_ids, int L, int K, int64_t V) {
   // a row has at most T tokens: none is long if T is not
   t.segments = T > t.seg ? tables * t.parts : 0;
   // the layout is a launch of its own, which short sequences do not win back
-  t.keys = T > kKeysFrom;
+  t.keys = T > kKeysAbove;
   return t;
 }
 

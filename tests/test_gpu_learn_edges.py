@@ -419,8 +419,8 @@ def test_learning_calls_refuse_tensors_that_want_a_gradient(rvq, dev):
 
 # launch forms that the other cases do not reach
 FORMS = [
-    # four waves an index workgroup with the IDs laid out by table: 2,048 < T <= 8,192, more than 512 workgroups
-    (3000, 16, 16384, 1001, 8), (8192, 16, 16384, 40, 4), (2049, 1, 300000, 7, 12),
+    # more than 512 index workgroups: of four waves with the IDs read in place and laid out by table, of sixteen
+    (3000, 16, 16384, 1001, 8), (5003, 16, 16384, 1001, 8), (8192, 16, 16384, 40, 4), (2049, 1, 300000, 7, 12),
     # several rows in turn for a part of a wave (W < 64), rows longer than a segment among them
     (1000, 2, 70000, 9, 8), (3000, 4, 40000, 1000, 24), (900, 1, 140000, 11, 128), (1500, 8, 20000, 100, 200),
     # more than four rows a wave
