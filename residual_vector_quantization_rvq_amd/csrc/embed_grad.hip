@@ -85,7 +85,8 @@ struct Tables {
   int64_t V;       // 0: no text gradient
   int64_t T;
   int64_t rows, positions;
-  int64_t seg, parts, segments;  // segments: parts of each table, or none at all
+  int seg, parts, segments;  // segments: parts of each table, or none at all
+  uint32_t per_parts;        // 2^32 / parts, rounded up
   bool keys;       // the IDs are laid out by table first
 };
 
@@ -99,10 +100,11 @@ Tables tables_of(int64_t T, int L_ids, int L, int K, int64_t V) {
   t.rows = (int64_t)L * K + V;
   const int tables = L + (V > 0 ? 1 : 0);
   t.positions = tables * T;
-  t.seg = segment_length(T, L_ids);
-  t.parts = ceil_div(T, t.seg);
+  t.seg = (int)segment_length(T, L_ids);
+  t.parts = (int)ceil_div(T, t.seg);
   // a row has at most T tokens: none is long if T is not
   t.segments = T > t.seg ? tables * t.parts : 0;
+  t.per_parts = t.segments ? (uint32_t)ceil_div((int64_t)1 << 32, t.parts) : 0;
   // the layout is a launch of its own, which short sequences do not win back
   t.keys = T > kKeysAbove;
   return t;
@@ -360,11 +362,13 @@ struct Piece {
   }
 };
 
-// positions [p0, p1) of segment s
-__device__ __forceinline__ void segment_at(const Tables &tb, int64_t s, int64_t &p0, int64_t &p1) {
-  const int64_t table = (uint32_t)s / (uint32_t)tb.parts, part = s - table * tb.parts;
-  p0 = table * tb.T + part * tb.seg;
-  p1 = part + 1 < tb.parts ? p0 + tb.seg : (table + 1) * tb.T;
+// positions [p0, p1) of segment s, of which there are too few for the rounding of
+// per_parts to matter (segments x parts < 2^32)
+__device__ __forceinline__ void segment_at(const Tables &tb, int s, int &p0, int &p1) {
+  const int table = (int)__umulhi((uint32_t)s, tb.per_parts), from = (s - table * tb.parts) * tb.seg;
+  const int T = (int)tb.T, begin = table * T;
+  p0 = begin + from;
+  p1 = begin + (from + tb.seg < T ? from + tb.seg : T);
 }
 
 template <typename G>
@@ -414,13 +418,13 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Ta
     G *o = nullptr;         // the row that is being summed
     float *part = nullptr;  // instead of it: a long row's piece
     if (u < 2 * tb.segments) {
-      int64_t p0, p1;
-      segment_at(tb, u >> 1, p0, p1);
+      int p0, p1;
+      segment_at(tb, (int)(u >> 1), p0, p1);
       const int ra = a.row[p0], row = u & 1 ? a.row[p1 - 1] : ra;
       if (row < 0 || (u & 1 && row == ra) || a.place[row].y <= tb.seg) continue;
-      const int64_t b = a.place[row].x, e = b + a.place[row].y;
-      starts = (int)(b > p0 ? b : p0);
-      counts = (int)(e < p1 ? e : p1) - starts;
+      const int b = a.place[row].x, e = b + a.place[row].y;
+      starts = b > p0 ? b : p0;
+      counts = (e < p1 ? e : p1) - starts;
       part = a.part + u * a.D;
     } else {
       // rows row0 .. row0 + rows - 1, of one table
@@ -516,11 +520,11 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a, Ta
 template <typename G>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a, Tables tb) {
   const int64_t s = blockIdx.x;
-  int64_t p0, p1;
-  segment_at(tb, s, p0, p1);
+  int p0, p1;
+  segment_at(tb, (int)s, p0, p1);
   const int row = a.row[p1 - 1];
   if (row < 0 || a.place[row].y <= tb.seg || a.place[row].x < p0) return;
-  const int64_t end = (int64_t)a.place[row].x + a.place[row].y;
+  const int end = a.place[row].x + a.place[row].y;
   const int64_t first = a.place[row].x == p0 ? 2 * s : 2 * s + 1;
   G *o = row_of<G>(a, tb, row);
   const int c = blockIdx.y * kThreads + threadIdx.x;
