@@ -104,10 +104,11 @@ Shape shape_of(int64_t pieces) {
 
 }  // namespace
 
-// Two pieces a lane of a workgroup: held to the 72 registers of seven waves (with
-// 74 and six, 39,731 x 4096 bf16 to 8 bits take 121 us and not 112).
+// Two pieces a lane: held to the 72 registers of seven waves (with 74 and six,
+// 39,731 x 4096 bf16 to 8 bits take 121 us and not 112, 60,000 x 640 bf16 with
+// residual 67 and not 62).
 template <typename T, int W, int P>
-__global__ __launch_bounds__(kThreads, W == 256 && P == 2 ? 7 : 1) void rms_norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void rms_norm_kernel(NormArgs a) {
   constexpr int N = kPiece<T>, R = kThreads / W;
   __shared__ float red[kThreads / 64];
   const int lane = threadIdx.x % W;
