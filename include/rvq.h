@@ -344,7 +344,7 @@ rvq_status rvq_rms_norm_backward_workspace_size(int64_t n, int32_t d, size_t *by
  * dx           : device, [n][d] in dtype.  May be dy or dsum itself.
  * dweight      : device, [d] fp32, overwritten; NULL when not wanted (the
  *                workspace is then not used).  Summed in an order that
- *                depends on n and d only (bitwise reproducible).
+ *                depends on n, d and dtype only (bitwise reproducible).
  */
 rvq_status rvq_rms_norm_backward(const void *dy, const void *h, rvq_dtype dtype, int64_t n,
                                  int32_t d, const float *rstd, const void *weight,
@@ -430,7 +430,8 @@ typedef struct rvq_adamw_options {
     uint32_t seed;
 } rvq_adamw_options;
 
-/* Workspace bytes of rvq_adamw_step with max_norm or grad_norm. */
+/* Workspace bytes of rvq_adamw_step with max_norm or grad_norm (16 KB for every
+ * 160 tensors). */
 rvq_status rvq_adamw_workspace_size(int32_t count, size_t *bytes);
 
 /*
@@ -442,6 +443,11 @@ rvq_status rvq_adamw_workspace_size(int32_t count, size_t *bytes);
  *             no parameter and no state is written (the step is skipped).
  * workspace : device, >= rvq_adamw_workspace_size bytes, 256-byte aligned;
  *             used (and required) with max_norm > 0 or grad_norm only.
+ *
+ * In a captured graph: tensors and options travel as kernel arguments, so every
+ * replay repeats one step: its lr, step number, bias corrections and random bits
+ * (the same elements round up every time, which is no longer right on average).
+ * A training loop makes this call anew for each step, beside a graph of the rest.
  */
 rvq_status rvq_adamw_step(const rvq_adamw_tensor *tensors, int32_t count, rvq_dtype param_dtype,
                           rvq_dtype grad_dtype, int32_t state_bits,

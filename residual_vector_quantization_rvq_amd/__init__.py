@@ -590,7 +590,9 @@ class AdamWState:
     """Parameters of one type and their AdamW state (see rvq_adamw_init):
     tuples params, m, v and, with 8-bit states, m_scale, v_scale; copies or
     None.  Bound to these tensors' memory (which it keeps alive) and no copy of
-    it: to load a state, copy into them or make a new AdamWState."""
+    it: to load a state, copy into them or call rvq_adamw_init again.  A step
+    checks that the parameters still have that memory, not the others: storage
+    put in the place of theirs (``.data = ``) is not seen."""
 
     def __init__(self, params, state_bits, weight_decay, copies, m, v, m_scale, v_scale):
         import numpy as np
@@ -628,7 +630,8 @@ def rvq_adamw_init(params: Sequence[torch.Tensor], state_bits: int = 32, weight_
     per parameter.  copies: bf16 tensors that receive the updated parameters
     (fp32 masters).  m, v (and scales): states to go on with, e.g. from a
     checkpoint; zeros otherwise.  An 8-bit state holds m = m * m_scale and
-    sqrt(v) = v * v_scale, block by block."""
+    sqrt(v) = v * v_scale, block by block, and no zero in v beside an m that is
+    not zero (such an element steps by lr m / eps)."""
     params = list(params)
     if not params:
         raise ValueError("no parameters")
@@ -699,7 +702,9 @@ def rvq_adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: int, 
     device; need_norm returns it without clipping); a norm that is not finite
     leaves parameters and states as they are.  seed: round 8-bit states and
     bf16 parameters at random (needed for 8-bit states in training), from
-    bits of (seed, step, tensor, element); None rounds to nearest."""
+    bits of (seed, step, tensor, element); None rounds to nearest.  In a captured
+    graph every replay repeats this step's number, lr and random bits: a training
+    loop calls it anew for each step."""
     dev, table = state.device, state._table
     grads = list(grads)
     if len(grads) != len(table):

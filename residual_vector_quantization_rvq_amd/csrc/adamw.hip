@@ -15,7 +15,8 @@
 // So a step that is given a seed rounds at random, up with the probability of
 // the remainder, from bits that are a hash of (seed, step, tensor, element);
 // bf16 parameters, where lr times the update is often under half a step, are
-// rounded the same way.
+// rounded the same way.  Near the bottom of a block's grid m and the root go up or
+// down apart; a root is never stored as 0 beside an m that is not (kF8Least).
 //
 // The tensors' pointers travel as kernel arguments, kTable tensors a launch:
 // nothing is copied, allocated or kept between calls.
@@ -23,9 +24,9 @@
 // Bound by memory, every element read and written once (the gradients twice
 // where the norm is asked for).  Bytes moved and time: 537 M fp32 parameters,
 // 32-bit states, clipped, with bf16 copies 18.3 GB, 3.44 ms, 5.3 TB/s; 537 M
-// bf16 parameters with 8-bit states 5.4 GB, 0.98 ms, 5.5 TB/s; 20 M fp32
-// parameters with 8-bit states, clipped, with copies 361 MB, 78 us.  96 tensors
-// of 200,003 elements: three launches of 5 to 6 us (41 us a call, most of it the
+// bf16 parameters with 8-bit states 5.4 GB, 0.97 ms, 5.6 TB/s; 20 M fp32
+// parameters with 8-bit states, clipped, with copies 361 MB, 79 us.  96 tensors
+// of 200,003 elements: three launches of 5 to 6 us (42 us a call, most of it the
 // caller's side).  Streaming stores change nothing (within 1%).
 #include "learn.h"
 
@@ -376,9 +377,11 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, C
 // 8-bit states: a half wave per block of kBlock elements, eight a lane.  The
 // root and the quotients that are stored are the nearest fp32 values, so that
 // the state is the definition's to the bit: one that is a unit off is stored as
-// the neighbour on the grid about once in 10^6 values, 6 to 12% away.  That
-// costs 1% where parameters are bf16 (966 and 978 us for 537 M; arithmetic is
-// nearly as long as 10 bytes of traffic there), elsewhere nothing.
+// the neighbour on the grid about once in 10^6 values, 6 to 12% away.  Where
+// parameters are bf16, arithmetic is nearly as long as 10 bytes of traffic: what
+// is for rare elements alone is left to branches that a block without them does
+// not take (537 M: 970 us; small roots looked for and NaN kept element by element,
+// and the bits of low roots chosen so, cost 2% each).
 template <typename P, typename G>
 __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Clip clip) {
   constexpr int N = kChunk / kThreads;

@@ -210,12 +210,6 @@ __device__ __forceinline__ void store_f8_n(uint8_t *p, int left, const float (&v
   }
 }
 
-__device__ __forceinline__ float wave_max_f32(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
-}
-
 // ---- launchers ----
 struct NormArgs {
   const void *x, *residual;   // residual may be null

@@ -12,10 +12,12 @@
 // up to 192 pieces, else a workgroup.  Rows of more than 2048 pieces (8192
 // fp32 or 16384 bf16 elements) are read again for each pass over them.
 //
-// Measured (bytes read and written): 39,731 x 4096 bf16 with residual 220 us,
-// 5.9 TB/s; 39,731 x 1152 bf16 78 us, 4.7 TB/s (84 us with a workgroup a row);
-// 3001 x 1155 fp32 7.7 us; one row of 4096 3.8 us, the time of a launch.
-// Gradient, 39,731 x 4096 bf16 with dsum and dweight: 235 + 5 us, 5.5 TB/s.
+// Measured (bytes read and written): 39,731 x 4096 bf16 with residual 229 us,
+// 5.7 TB/s, to 8 bits 207 us, and without residual to 8 bits 112 us, 4.4 TB/s;
+// 39,731 x 1152 bf16 80 us, 4.6 TB/s (a workgroup a row was 8% slower); 3001 x
+// 1155 fp32 8.0 us: 289 pieces on 512 slots, and two rounds of workgroups; one row
+// of 4096 4.0 us, the time of a launch.  Gradient, 39,731 x 4096 bf16 with dsum and
+// dweight: 237 + 6 us, 5.3 TB/s.
 // Streaming stores gain 4% of the norm and 1% of its gradient, and take the
 // rows out of the caches, where the next layer looks for them: not used.
 #include "learn.h"
@@ -202,7 +204,9 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void rms_norm_kernel(Norm
 }
 
 // Rows too wide for registers: one workgroup per row, which is read again for
-// each pass over it.
+// each pass over it.  By elements, the simplest form that is right: no workload here
+// has rows of more than 8192.  8,000 x 20,480 bf16 with residual: 811 us, 1.6 TB/s
+// (gradient 798 us); 10,000 x 16,384, the widest that registers hold, 298 us.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void rms_norm_wide_kernel(NormArgs a) {
   __shared__ float red[kThreads / 64];
@@ -302,10 +306,15 @@ int64_t norm_grad_parts(int64_t n, int d, bool bf16) {
 }
 
 // kMaxParts workgroups of four waves are as many as fit at once with 128
-// registers: a second round of fewer would cost as much as the first (39,731 x
-// 4096 bf16: 1024 workgroups 232 us, 1280 300 us; with 129 registers, three
-// to a compute unit, 325 us).  All of a row's loads are issued before its sum;
-// more waves hide the rest (holding the next row too was 2% slower).
+// registers, as the shapes up to two pieces of bf16 or four of fp32 have: a second
+// round of fewer would cost as much as the first (39,731 x 4096 bf16: 1024
+// workgroups 232 us, 1280 300 us).  The wider bf16 shapes and the widest fp32 one
+// have more, and pay that round: 142 registers for three pieces of a wave's lanes
+// (768 workgroups at once), 173 and over 256 for four and eight of a workgroup's
+// (512, 256).  With dsum, with dweight and without: 39,731 x 1152 bf16 94 and 69 us
+// (3.9 and 5.4 TB/s), 20,000 x 8192 301 and 277, 10,000 x 16,384 415 and 263.  All of
+// a row's loads are issued before its sum; more waves hide the rest (holding the
+// next row too was 2% slower).
 template <typename T, int W, int P, bool DW>
 __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a) {
   constexpr int N = kPiece<T>, R = kThreads / W;
