@@ -221,11 +221,13 @@ __device__ __forceinline__ float nearest_sqrt(float v) {
   const float r = __builtin_fmaf(-s, s, v);
   return v < 0x1p-96f ? 0.f : __builtin_fmaf(r, 0.5f * y, s);
 }
-// A factor for roots of an element with the larger of its old root and gradient
-// given: its square is within fp32 then, and a power of two changes no digit.
-constexpr float kRootUnit = 0x1p32f, kLargeUnit = 0x1p-70f;
+// A factor for roots of an element whose old root and gradient are `largest` at
+// most.  Large squares lie between 2^16 and 2^124 then, so that (1 - b2) times
+// them, 2^-53 at least, is no v that counts as zero; small ones are 2^64 times what
+// they are.  A power of two changes no digit.
+constexpr float kRootUnit = 0x1p32f, kLargeUnit = 0x1p-66f;
 __device__ __forceinline__ float root_unit(float largest) {
-  return largest < 0x1p31f ? kRootUnit : kLargeUnit;
+  return largest < 0x1p29f ? kRootUnit : largest < 0x1p74f ? 0x1p-12f : kLargeUnit;
 }
 
 // An element's step where squares leave fp32, in the unit u: vu is the old and
@@ -430,7 +432,7 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
   }
   float nsm = half_wave_max(mtop), nsv = __uint_as_float(half_wave_max(rtop)), unit = kRootUnit;
   if (!(nsv < INFINITY && sm == sm)) {
-    // A gradient or root beyond 2^31, infinity or NaN in the block: its elements
+    // v times kRootUnit^2 beyond fp32, infinity or NaN in the block: its elements
     // once more, each in a unit of its own.  What is not finite is stored as NaN,
     // and its block's scales are the others'.
     unit = 1.f;

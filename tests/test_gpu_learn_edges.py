@@ -449,3 +449,19 @@ def test_embed_grad_launch_forms(rvq, dev, case):
                                                     accumulate=True)
         assert torch.equal(level, (wl + 2.0).to(gdt)) and torch.equal(text, (wt - 1.0).to(gdt))
         del wl, wt, l0, t0, level, text
+
+
+def test_adamw_large_gradients_of_a_slow_v(rvq, dev):
+    # with beta2 = 1 - 1e-7 the first v is 10^-7 of the square: not lost beside an
+    # element of the block that is 10^20 times larger
+    betas = (0.9, 1.0 - 1e-7)
+    for bits in (32, 8):
+        for size in (1e3, 3e9, 1e11, 1e14, 1e17, 1e20, 1e24, 1e28):
+            p = torch.ones(256, device=dev)
+            g = torch.full((256,), size, device=dev)
+            g[0] = 1e30
+            st = rvq.rvq_adamw_init([p], bits, 0.0)
+            rvq.rvq_adamw_step(st, [g], 1, 0.25, betas)
+            want, _, _, upd = ref.adamw(torch.ones(256, device=dev), g, torch.zeros_like(g), torch.zeros_like(g), 1, 0.25,
+                                        betas, 1e-8, 0.0)
+            ref.close(p, want, 4 * ref.U + 24 * ref.U * upd.abs(), f"{bits} {size}")
