@@ -23,12 +23,12 @@
 // What bounds it: every row of the tables is written once, and a visual
 // token's row of dout is read once for each of its L levels.  Those reads miss
 // the L2 (a row is back L levels later) and share the fabric with the writes.
-// 39,731 tokens of 4096 bf16, 131,072 rows of fp32: 2.15 GB written and 2.35
-// GB read in 683 us, 6.6 TB/s; dout read once would leave 370 us.  Tried and
+// 39,731 tokens of 4096 bf16, 131,072 rows of fp32: 2.15 GB written and 2.29
+// GB read in 681 us, 6.5 TB/s; dout read once would leave 370 us.  Tried and
 // slower there: slabs of 64 to 512 bytes, one an XCD, that its L2 can hold
 // (1.1 to 1.4 ms: eight to 32 lanes a row are bound by their control, and the
 // stream of results evicts the slab).  Kernels of that call: by-table IDs 5
-// us, index 29 us, sums 683 us, join 10 us.
+// us, index 29 us, sums 681 us, join 10 us.
 #include "learn.h"
 
 namespace rvq {
