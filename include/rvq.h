@@ -396,8 +396,8 @@ rvq_status rvq_embed_tokens_backward(const void *dout, rvq_dtype dout_dtype, con
  * where a scale is max(largest magnitude of the 256 / 448, 2^-100).  All
  * zeros is a valid start of both.  Where m is not stored as 0, a sqrt(v) above 0
  * is not either: it becomes at least the smallest e4m3 value, 2^-9 of its scale.
- * (lr m / eps is a step without bounds: a state that a caller builds should
- * keep to that too.)
+ * (lr m / eps is a step without bounds: a state that a caller builds has to
+ * keep to that too; a zero that comes beside an m is stepped by the formula alone.)
  * Squares may leave fp32: sqrt(v) of 8-bit
  * states has fp32's whole range, and a v of 32-bit states is held at the
  * largest fp32 at most.  A moment that is not finite (of such a gradient) is

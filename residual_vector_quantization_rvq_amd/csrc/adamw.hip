@@ -129,19 +129,13 @@ __device__ __forceinline__ float round_bf16(float v, uint32_t random16) {
   return v == v ? round_number_bf16(v, random16) : v;
 }
 
-// The least e4m3 value: a root above 0 is stored as it and not as 0 where its m
+// The least e4m3 value.  A root above 0 is stored as it and not as 0 where its m
 // is not stored as 0.  The two are rounded apart, and m / 0 would make the next
 // step lr m / eps: over 10^6 times lr in blocks with elements 10^4 times larger.
+// A state that comes with such a pair is stepped as it is, by the formula alone.
 constexpr float kF8Least = 0x1p-9f;
-template <int N>
-__device__ __forceinline__ uint32_t raise_roots(uint32_t qm, uint32_t qv, const float (&v)[N], int q0) {
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const uint32_t byte = 0x7fu << (8 * b);
-    if ((qm & byte) && !(qv & byte) && v[q0 + b] > 0.f) qv |= 1u << (8 * b);
-  }
-  return qv;
-}
+// e4m3 byte q of 8 is not 0, of either sign
+__device__ __forceinline__ bool byte_set(u32x2 w, int q) { return (w[q >> 2] >> (8 * (q & 3))) & 0x7f; }
 
 // op over the 32 lanes of a half wave
 template <typename Op>
@@ -163,13 +157,17 @@ __device__ __forceinline__ uint32_t half_wave_max(uint32_t v) {
 }
 
 // 8 e4m3 bytes at p; `left` of them exist (the others read as zero)
-__device__ __forceinline__ void load_f8x8(const uint8_t *p, int left, float (&v)[8]) {
+__device__ __forceinline__ u32x2 load_8_bytes(const uint8_t *p, int left) {
   u32x2 q = {0, 0};
   if (left >= 8) {
     q = *(const u32x2_at1 *)p;
   } else {
     for (int e = 0; e < left; ++e) q[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
   }
+  return q;
+}
+__device__ __forceinline__ void load_f8x8(const uint8_t *p, int left, float (&v)[8]) {
+  const u32x2 q = load_8_bytes(p, left);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[j], false);
@@ -489,16 +487,22 @@ __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Cl
       qv[h] = pack_f8x4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
     }
   }
-  float least = v[0];
+  // roots above 0 and below the least value: those alone can have become 0.  Zeros,
+  // of rows that nothing touched, are told apart at a second look.
+  uint32_t low = UINT32_MAX;  // the least root above 0, less 1 in its bits
 #pragma unroll
-  for (int q = 1; q < N; ++q) least = fminf(least, v[q]);
-  if (least < kF8Least) {  // only such a root can have become 0
+  for (int q = 0; q < N; ++q) low = min(low, __float_as_uint(v[q]) - 1);
+  if (low < __float_as_uint(kF8Least) - 1) {  // only a root below kF8Least can have become 0
+    const u32x2 m0 = load_8_bytes((const uint8_t *)e.m + i, left), v0 = load_8_bytes((const uint8_t *)e.v + i, left);
+    const auto paired = [&](int q) { return v[q] < kF8Least && (byte_set(v0, q) || !byte_set(m0, q)); };
+    if (k.stochastic) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (k.stochastic)
-        qv[h] = random_f8x4(v, 4 * h, [&](int q) { return v[q] < kF8Least ? m_bits(q) : v_bits(q); });
-      qv[h] = raise_roots(qm[h], qv[h], v, 4 * h);
+      for (int h = 0; h < 2; ++h)
+        qv[h] = random_f8x4(v, 4 * h, [&](int q) { return paired(q) ? m_bits(q) : v_bits(q); });
     }
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      if (paired(q) && v[q] > 0.f && byte_set(qm, q) && !byte_set(qv, q)) qv[q >> 2] |= 1u << (8 * (q & 3));
   }
   store_8_bytes((uint8_t *)e.m + i, left, qm);
   store_8_bytes((uint8_t *)e.v + i, left, qv);
