@@ -615,6 +615,18 @@ class AdamWState:
                 words[:, column] = [t.data_ptr() for t in ts]
         words[:, 7] = self._numels
         words.view(np.float32)[:, 16] = weight_decay
+        n = words[:, 7]
+        width, state = params[0].element_size(), 4 if state_bits == 32 else 1
+        spans = [(words[:, 0], n * width), (words[:, 2], n * state), (words[:, 3], n * state)]
+        if state_bits == 8:
+            spans += [(words[:, c], (n + 255) // 256 * 4) for c in (4, 5)]
+        if copies is not None:
+            spans.append((words[:, 6], 2 * n))
+        at, size = (np.concatenate(x).astype(np.int64) for x in zip(*spans))
+        at, size = at[size > 0], size[size > 0]
+        order = np.argsort(at)
+        if np.any(at[order][1:] < (at + size)[order][:-1]):
+            raise ValueError("parameters, states and copies must not share memory (a tied parameter is listed once)")
         self._grads = words[:, 1]
 
 

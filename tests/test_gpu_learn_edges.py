@@ -467,3 +467,24 @@ def test_adamw_large_gradients_of_a_slow_v(rvq, dev):
             want, _, _, upd = ref.adamw(torch.ones(256, device=dev), g, torch.zeros_like(g), torch.zeros_like(g), 1, 0.25,
                                         betas, 1e-8, 0.0)
             ref.close(p, want, 4 * ref.U + 24 * ref.U * upd.abs(), f"{bits} {size}")
+
+
+def test_adamw_refuses_tensors_that_share_memory(rvq, dev):
+    buf = torch.zeros(1000, device=dev)
+    f = lambda n: torch.zeros(n, device=dev)  # noqa: E731
+    for bits in (32, 8):
+        for params in ([buf, buf], [f(10), buf, f(10), buf[:10]], [buf[:600], buf[599:]], [buf.view(10, 100), buf[500:501]]):
+            with pytest.raises(ValueError):
+                rvq.rvq_adamw_init(params, bits)
+        rvq.rvq_adamw_init([buf[:600], buf[600:], buf[:0], buf[5:5]], bits)   # next to each other, and nothing at all
+    a, b = f(300), f(300)
+    for kw in (dict(m=[buf[:300]], v=[f(300)]), dict(m=[a], v=[a]), dict(m=[a], v=[b], copies=[buf[:150].view(BF16)]),
+               dict(copies=[a.view(BF16)[:300]], m=[b], v=[a])):
+        with pytest.raises(ValueError):
+            rvq.rvq_adamw_init([buf[:300]], 32, **kw)
+    rvq.rvq_adamw_init([buf[:300]], 32, m=[a], v=[b], copies=[buf[300:450].view(BF16)])
+    q = f(600).view(torch.uint8).view(F8)
+    s = f(8)
+    with pytest.raises(ValueError):
+        rvq.rvq_adamw_init([a], 8, m=[q[:300]], v=[q[300:600]], m_scale=[s[:2]], v_scale=[s[1:3]])
+    rvq.rvq_adamw_init([a], 8, m=[q[:300]], v=[q[300:600]], m_scale=[s[:2]], v_scale=[s[2:4]])
