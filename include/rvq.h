@@ -312,7 +312,7 @@ rvq_status rvq_embed_tokens(const int32_t *ids, const uint8_t *is_visual, int64_
  * eps          : > 0.
  * sum_out      : device, [n][d] in x_dtype: h, the residual stream that goes
  *                on; or NULL.  May be x or residual itself (in place), not
- *                another overlap.
+ *                another overlap (y least of all).
  * y            : device, [n][d] in y_dtype.  RVQ_F8E4M3: row i holds
  *                e4m3(y / y_scale[i]), nearest even, with
  *                y_scale[i] = max(max|y| / 448, 2^-100) (NaN where a value of

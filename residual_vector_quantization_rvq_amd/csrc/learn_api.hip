@@ -95,6 +95,8 @@ rvq_status rvq_rms_norm(const void *x, const void *residual, rvq_dtype x_dtype, 
   RVQ_TRY(may(residual, "residual", xs));
   RVQ_TRY(may(sum_out, "sum_out", xs));
   RVQ_TRY(need(y, "y", dtype_bytes(y_dtype)));
+  if (sum_out == y)
+    return fail(RVQ_ERR_INVALID_ARGUMENT, "sum_out and y must not be the same memory");
   if (y_dtype == RVQ_F8E4M3) RVQ_TRY(need(y_scale, "y_scale", 4));
   RVQ_TRY(may(rstd, "rstd", 4));
   NormArgs a = {x, residual, weight, weight_dtype == RVQ_BF16, sum_out, y, (int)y_dtype,

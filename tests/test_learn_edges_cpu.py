@@ -49,3 +49,9 @@ def test_adamw_options_outside_fp32(rvq):
     for ok in (dict(grad_scale=3e38), dict(lr=1e37), dict(max_norm=1e-60, lr=0.0)):
         # nothing to do, so nothing is launched (max_norm asks for a workspace first)
         assert call(**ok) == (1 if "max_norm" in ok else 0), ok
+
+
+def test_norm_refuses_one_place_for_sum_and_y(rvq):
+    # x, residual, x_dtype, n, d, weight, weight_dtype, eps, sum_out, y, y_dtype, y_scale, rstd, stream
+    args = [256, 256, 0, 4, 8, None, 0, 1e-6, 512, 512, 0, None, None, None]
+    assert rvq.raw_library().rvq_rms_norm(*args) == 1
