@@ -24,7 +24,7 @@
 // Bound by memory, every element read and written once (the gradients twice
 // where the norm is asked for).  Bytes moved and time: 537 M fp32 parameters,
 // 32-bit states, clipped, with bf16 copies 18.3 GB, 3.44 ms, 5.3 TB/s; 537 M
-// bf16 parameters with 8-bit states 5.4 GB, 0.97 ms, 5.6 TB/s; 20 M fp32
+// bf16 parameters with 8-bit states 5.4 GB, 0.97 to 1 ms by the card, 5.5 TB/s; 20 M fp32
 // parameters with 8-bit states, clipped, with copies 361 MB, 79 us.  96 tensors
 // of 200,003 elements: three launches of 5 to 6 us (42 us a call, most of it the
 // caller's side).  Streaming stores change nothing (within 1%).
@@ -380,8 +380,9 @@ __global__ __launch_bounds__(kThreads) void adamw_32_kernel(Table t, Consts k, C
 // the neighbour on the grid about once in 10^6 values, 6 to 12% away.  Where
 // parameters are bf16, arithmetic is nearly as long as 10 bytes of traffic: what
 // is for rare elements alone is left to branches that a block without them does
-// not take (537 M: 970 us; small roots looked for and NaN kept element by element,
-// and the bits of low roots chosen so, cost 2% each).
+// not take (537 M, on one card: 981 us with none of it, 996 as it is; small roots
+// looked for and NaN kept element by element, and the bits of low roots chosen so,
+// cost 2% each).
 template <typename P, typename G>
 __global__ __launch_bounds__(kThreads) void adamw_8_kernel(Table t, Consts k, Clip clip) {
   constexpr int N = kChunk / kThreads;
