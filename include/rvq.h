@@ -455,6 +455,191 @@ rvq_status rvq_adamw_step(const rvq_adamw_tensor *tensors, int32_t count, rvq_dt
                           size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The head of a model that takes and predicts token IDs.
+ *
+ * Rows of features or hidden states are layer-normed, 8-bit rows are multiplied
+ * with a table (8-bit values with a scale for each block of 128), and the logits
+ * that come out score the IDs: their log probabilities, entropy and best
+ * alternatives, or the distance from a teacher's best.  Each comes with its
+ * gradient, for one training step around a model; conventions are those of the
+ * calls above.  Pointers need only the alignment of their elements; 16-byte
+ * alignment is fastest.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Layer norm of rows, with the residual's addition and an 8-bit output:
+ *   h = x + residual (or x),  m = mean(h),  r = 1 / sqrt(mean((h - m)^2) + eps),
+ *   y = (h - m) r weight + bias,
+ * in fp32, the variance taken of the centred values; each output is rounded once
+ * (y uses the unrounded h).  h has to be within fp32's range, its squares need not.
+ *
+ * x, residual, sum_out, y, y_dtype, y_scale, eps : as for rvq_rms_norm.
+ * weight, bias : device, [d] in weight_dtype (RVQ_F32 or RVQ_BF16), or NULL for
+ *                ones and zeros.
+ * mean, rstd   : device, [n] fp32: m and r of every row, for the gradient; or NULL.
+ * Limits: n <= 2^25, d <= 2^20.
+ */
+rvq_status rvq_layer_norm(const void *x, const void *residual, rvq_dtype x_dtype, int64_t n,
+                          int32_t d, const void *weight, const void *bias, rvq_dtype weight_dtype,
+                          float eps, void *sum_out, void *y, rvq_dtype y_dtype, float *y_scale,
+                          float *mean, float *rstd, hipStream_t stream);
+
+/* Workspace bytes of rvq_layer_norm_backward with dweight or dbias. */
+rvq_status rvq_layer_norm_backward_workspace_size(int64_t n, int32_t d, size_t *bytes);
+
+/*
+ * Gradient of rvq_layer_norm.  With g = dy weight and u = (h - mean) rstd:
+ *   dx = rstd (g - mean(g) - u mean(g u)) + dsum,
+ *   dweight = sum over rows of dy u,   dbias = sum over rows of dy.
+ * dx is the gradient of x and of residual alike.
+ *
+ * dy, h, dsum, dx : as for rvq_rms_norm_backward.
+ * mean, rstd      : device, [n] fp32, from rvq_layer_norm.
+ * dweight, dbias  : device, [d] fp32, overwritten; either may be NULL (with both
+ *                   NULL the workspace is not used).  Summed in an order that
+ *                   depends on n, d and dtype only (bitwise reproducible).
+ */
+rvq_status rvq_layer_norm_backward(const void *dy, const void *h, rvq_dtype dtype, int64_t n,
+                                   int32_t d, const float *mean, const float *rstd,
+                                   const void *weight, rvq_dtype weight_dtype, const void *dsum,
+                                   void *dx, float *dweight, float *dbias, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* Scales of an 8-bit operand [rows][k] of rvq_matmul_f8. */
+typedef enum rvq_scale_layout {
+    RVQ_SCALE_ROW = 0,      /* [rows]: one a row (as the norms' 8-bit outputs have) */
+    RVQ_SCALE_ROW_128 = 1,  /* [rows][ceil(k / 128)]: one for 128 elements of a row */
+    RVQ_SCALE_128_128 = 2   /* [ceil(rows / 128)][ceil(k / 128)]: one for 128 x 128 */
+} rvq_scale_layout;
+
+/*
+ * 8-bit values (e4m3) with one scale for each block of 128:
+ *   scale = max(max|x| / 448, 2^-100) of the block (NaN where a value of it is NaN
+ *   or infinite),  q = e4m3(x / scale), nearest even.
+ *
+ * x         : device, [rows][cols] in x_dtype (RVQ_F32 or RVQ_BF16).
+ * layout    : RVQ_SCALE_ROW_128 or RVQ_SCALE_128_128, of q's rows.
+ * transpose : nonzero: q is x's transpose, [cols][rows], with blocks along its rows
+ *             (what the gradient of a weight contracts are the rows of x).
+ * q         : device, [rows][cols] (or [cols][rows]), rows q_stride bytes apart;
+ *             bytes between a row's end and the next row are left as they are.
+ * scale     : device, fp32, as layout says for q's rows and columns.
+ * Limits: rows, cols <= 2^30, rows cols <= 2^40.
+ */
+rvq_status rvq_quantize_f8(const void *x, rvq_dtype x_dtype, int64_t rows, int64_t cols,
+                           rvq_scale_layout layout, int32_t transpose, void *q, int64_t q_stride,
+                           float *scale, hipStream_t stream);
+
+/*
+ * Product of 8-bit operands:
+ *   out[i][j] = sum over blocks c of sa(i, c) sb(j, c) sum_{k in block c} a[i][k] b[j][k],
+ * both sums in fp32, one rounding to out_dtype.  The forward pass of a linear
+ * layer (a: rows, b: weight [n][k]) and, with transposed operands, both its gradients.
+ *
+ * a, b         : device, [m][k] and [n][k] e4m3, rows a_stride, b_stride bytes
+ *                apart (>= k).  Fastest with 16-byte aligned rows (address and stride
+ *                multiples of 16): then each row, the last too, has to be readable up
+ *                to a multiple of 16 bytes; what stands behind its end is not used.
+ * a_scale, b_scale : device, fp32, laid out as a_layout and b_layout say; a product
+ *                of two scales has to be within fp32.
+ * out          : device, [m][n] in out_dtype (RVQ_F32 or RVQ_BF16).  k == 0 gives zeros.
+ * Limits: m, n <= 2^30, m n <= 2^40, k <= 2^30.
+ */
+rvq_status rvq_matmul_f8(const void *a, int64_t a_stride, const float *a_scale,
+                         rvq_scale_layout a_layout, const void *b, int64_t b_stride,
+                         const float *b_scale, rvq_scale_layout b_layout, int64_t m, int64_t n,
+                         int64_t k, void *out, rvq_dtype out_dtype, hipStream_t stream);
+
+/* Workspace bytes of rvq_token_logprobs (0 for many rows). */
+rvq_status rvq_token_logprobs_workspace_size(int64_t n, int32_t V, int32_t top, size_t *bytes);
+
+/*
+ * Log probabilities of given tokens under softmax(logits / temperature), with the
+ * entropy and the best alternatives of each row.
+ *
+ * logits      : device, [n][V] in dtype (RVQ_F32 or RVQ_BF16).  -inf masks a token.
+ * ids         : device, [n] int32: the token of each row; or NULL.  -1: no token
+ *               (logprob 0); any other ID outside [0, V) also gives 0 and is counted
+ *               in *bad_ids.
+ * temperature : 1e-4 .. 1e4.
+ * logprob     : device, [n] fp32 (-inf of a masked token); required with ids.
+ * entropy     : device, [n] fp32, in nats; or NULL.
+ * stats       : device, [n][2] fp32: the row's largest logit M and log S, S = sum of
+ *               exp((logit - M) / temperature); the log of the row's sum of
+ *               exponentials is M / temperature + log S.
+ * top         : 0 .. 64 alternatives.
+ * top_logprob, top_ids : device, [n][top] fp32 and int32: the largest logits, larger
+ *               first and the lower ID first among equals; -inf and -1 behind the last
+ *               token that is not masked.  Not read with top == 0.
+ * bad_ids     : device uint32 counter (added to), or NULL.
+ * A row that holds NaN or +inf gives NaN (and IDs of -1); a row of nothing but -inf
+ * gives log probabilities of -inf and entropy 0.  Rows do not touch one another.
+ * Limits: n <= 2^25, 1 <= V <= 2^24.
+ */
+rvq_status rvq_token_logprobs(const void *logits, rvq_dtype dtype, int64_t n, int32_t V,
+                              const int32_t *ids, float temperature, float *logprob,
+                              float *entropy, float *stats, int32_t top, float *top_logprob,
+                              int32_t *top_ids, uint32_t *bad_ids, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradient of rvq_token_logprobs with respect to the logits:
+ *   dlogits[j] = (dlogprob ([j == id] - p_j) - dentropy p_j (log p_j + entropy)) / temperature
+ *
+ * logits, ids, temperature, stats, entropy : as given to and by the forward call;
+ *             entropy is read with dentropy only.
+ * dlogprob, dentropy : device, [n] fp32; either may be NULL, not both.  dlogprob
+ *             needs ids; rows without a valid ID take none.  Rows with both 0, and
+ *             rows of nothing but -inf, get zeros whatever their logits are.
+ * dlogits   : device, [n][V] in dtype.  May be logits itself, not another overlap.
+ */
+rvq_status rvq_token_logprobs_backward(const void *logits, rvq_dtype dtype, int64_t n, int32_t V,
+                                       const int32_t *ids, float temperature, const float *stats,
+                                       const float *dlogprob, const float *entropy,
+                                       const float *dentropy, void *dlogits, hipStream_t stream);
+
+/*
+ * Distillation loss of a teacher's top tokens, with p = softmax(logits / temperature):
+ *   tail == 0: q = softmax(teacher / temperature) over the row's entries
+ *              (teacher: logits, or log probabilities at temperature 1),
+ *              loss = sum over entries of q (log q - log p);
+ *   tail != 0: q = exp(teacher) (teacher: log probabilities at this temperature, as
+ *              rvq_token_logprobs gives them), and all other tokens are one more
+ *              outcome: rest = max(0, 1 - sum q), against the sum of their p.
+ *
+ * logits      : as for rvq_token_logprobs.
+ * teacher_ids : device, [n][k] int32.  -1: no entry; any other ID outside [0, V) is
+ *               left out and counted in *bad_ids; a repeated ID counts where it
+ *               comes first.
+ * teacher     : device, [n][k] fp32.
+ * k           : 1 .. 256.
+ * loss        : device, [n] fp32; 0 of a row without an entry (or, with tail == 0,
+ *               whose entries are all -inf), +inf where the teacher's weight meets a
+ *               masked token.
+ * stats       : device, [n][4] fp32, for the gradient.
+ * Limits: n <= 2^25, 1 <= V <= 2^24.
+ */
+rvq_status rvq_distill_loss(const void *logits, rvq_dtype dtype, int64_t n, int32_t V,
+                            const int32_t *teacher_ids, const float *teacher, int32_t k,
+                            int32_t tail, float temperature, float *loss, float *stats,
+                            uint32_t *bad_ids, hipStream_t stream);
+
+/*
+ * Gradient of rvq_distill_loss with respect to the logits, times dloss of the row:
+ *   dlogits[j] = dloss (p_j - q_j) / temperature  (q_j: of a token outside the entries 0
+ *   or, with tail, rest p_j / (sum of p over those tokens)).
+ *
+ * dloss    : device, [n] fp32.  A row of 0, one without an entry and one of nothing
+ *            but -inf get zeros whatever their logits are.
+ * dlogits  : device, [n][V] in dtype.  May be logits itself, not another overlap.
+ * All else as given to and by the forward call.
+ */
+rvq_status rvq_distill_loss_backward(const void *logits, rvq_dtype dtype, int64_t n, int32_t V,
+                                     const int32_t *teacher_ids, const float *teacher, int32_t k,
+                                     int32_t tail, float temperature, const float *stats,
+                                     const float *dloss, void *dlogits, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Resumable ID cache (host files).
  *
  * The visual tokenizer is fixed, so token IDs are computed ahead of time

@@ -18,6 +18,16 @@ Learning the token embedding:
   rvq_embed_tokens_backward(dout, ids, K)     -> (level_grad [L, K, D], text_grad [V, D])
   rvq_adamw_init(params) -> state;  rvq_adamw_step(state, grads, step, lr)
 
+The head of a model that takes and predicts token IDs:
+  rvq_layer_norm(x, weight, bias, eps, residual)      -> (y, scale, sum, mean, rstd)
+  rvq_layer_norm_backward(dy, h, mean, rstd, weight)  -> (dx, dweight, dbias)
+  rvq_quantize_f8(x, block_rows, transpose)           -> (q, scale)
+  rvq_matmul_f8(a, a_scale, b, b_scale)               -> a b^T [m, n]
+  rvq_token_logprobs(logits, ids, temperature, top)   -> (logprob, entropy, stats, top_logprob, top_ids)
+  rvq_token_logprobs_backward(logits, ids, stats, dlogprob)        -> dlogits
+  rvq_distill_loss(logits, teacher_ids, teacher)                   -> (loss, stats)
+  rvq_distill_loss_backward(logits, teacher_ids, teacher, stats, dloss) -> dlogits
+
 Results belong to no autograd graph.  The calls that learn take a tensor that
 requires a gradient under torch.no_grad() only (as in the forward and backward of
 a torch.autograd.Function), so that no gradient is lost without a word.
@@ -45,6 +55,10 @@ __all__ = [
     "rvq_rms_norm_backward", "rvq_embed_tokens_backward_workspace_size",
     "rvq_embed_tokens_backward", "AdamWState", "rvq_adamw_init", "rvq_adamw_workspace_size",
     "rvq_adamw_step",
+    "LayerNormResult", "rvq_layer_norm", "rvq_layer_norm_backward_workspace_size",
+    "rvq_layer_norm_backward", "rvq_quantize_f8", "rvq_matmul_f8", "TokenLogprobs",
+    "rvq_token_logprobs_workspace_size", "rvq_token_logprobs", "rvq_token_logprobs_backward",
+    "DistillLoss", "rvq_distill_loss", "rvq_distill_loss_backward",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -141,6 +155,25 @@ _lib.rvq_adamw_step.argtypes = [_p, _i32, ctypes.c_int, ctypes.c_int, _i32,
 for _f in ("rvq_rms_norm", "rvq_rms_norm_backward_workspace_size", "rvq_rms_norm_backward",
            "rvq_embed_tokens_backward_workspace_size", "rvq_embed_tokens_backward",
            "rvq_adamw_workspace_size", "rvq_adamw_step"):
+    getattr(_lib, _f).restype = ctypes.c_int
+_lib.rvq_layer_norm.argtypes = [_p, _p, ctypes.c_int, _i64, _i32, _p, _p, ctypes.c_int, _f32, _p, _p,
+                                ctypes.c_int, _p, _p, _p, _p]
+_lib.rvq_layer_norm_backward_workspace_size.argtypes = [_i64, _i32, _psz]
+_lib.rvq_layer_norm_backward.argtypes = [_p, _p, ctypes.c_int, _i64, _i32, _p, _p, _p, ctypes.c_int,
+                                         _p, _p, _p, _p, _p, _sz, _p]
+_lib.rvq_quantize_f8.argtypes = [_p, ctypes.c_int, _i64, _i64, ctypes.c_int, _i32, _p, _i64, _p, _p]
+_lib.rvq_matmul_f8.argtypes = [_p, _i64, _p, ctypes.c_int, _p, _i64, _p, ctypes.c_int, _i64, _i64, _i64,
+                               _p, ctypes.c_int, _p]
+_lib.rvq_token_logprobs_workspace_size.argtypes = [_i64, _i32, _i32, _psz]
+_lib.rvq_token_logprobs.argtypes = [_p, ctypes.c_int, _i64, _i32, _p, _f32, _p, _p, _p, _i32, _p, _p, _p,
+                                    _p, _sz, _p]
+_lib.rvq_token_logprobs_backward.argtypes = [_p, ctypes.c_int, _i64, _i32, _p, _f32, _p, _p, _p, _p, _p, _p]
+_lib.rvq_distill_loss.argtypes = [_p, ctypes.c_int, _i64, _i32, _p, _p, _i32, _i32, _f32, _p, _p, _p, _p]
+_lib.rvq_distill_loss_backward.argtypes = [_p, ctypes.c_int, _i64, _i32, _p, _p, _i32, _i32, _f32, _p, _p,
+                                           _p, _p]
+for _f in ("rvq_layer_norm", "rvq_layer_norm_backward_workspace_size", "rvq_layer_norm_backward",
+           "rvq_quantize_f8", "rvq_matmul_f8", "rvq_token_logprobs_workspace_size", "rvq_token_logprobs",
+           "rvq_token_logprobs_backward", "rvq_distill_loss", "rvq_distill_loss_backward"):
     getattr(_lib, _f).restype = ctypes.c_int
 for _f in ("rvq_mfma_rate", "rvq_prepared_size", "rvq_prepare_codebooks", "rvq_encode_workspace_size",
            "rvq_encode", "rvq_encode_noalloc", "rvq_encode_profiled", "rvq_decode",
@@ -747,6 +780,368 @@ def rvq_adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: int, 
                _dtype_code(state.param_dtype), gcode, state.state_bits, ctypes.byref(opt),
                _address(norm), _address(ws), nbytes, _raw_stream(dev))
     return norm
+
+
+class LayerNormResult(NamedTuple):
+    y: torch.Tensor                  # [n, d]
+    scale: Optional[torch.Tensor]    # [n] fp32: 8-bit outputs only
+    sum: Optional[torch.Tensor]      # [n, d]: x + residual
+    mean: Optional[torch.Tensor]     # [n] fp32
+    rstd: Optional[torch.Tensor]     # [n] fp32
+
+
+def rvq_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                   bias: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                   need_stats: bool = False, out: Optional[torch.Tensor] = None,
+                   sum_out: Optional[torch.Tensor] = None) -> LayerNormResult:
+    """Layer norm of rows x [n, d] (fp32 or bf16) after adding the residual:
+    h = x + residual, y = (h - mean) / sqrt(variance + eps) * weight + bias.
+    out_dtype is float32, bfloat16 (default: x's) or float8_e4m3fn, which comes
+    with one scale per row (y = out * scale).  weight and bias are both fp32 or
+    both bf16.  ``sum`` is h in x's type where there is a residual (sum_out may
+    be x or residual: in place); ``mean`` and ``rstd`` are what
+    rvq_layer_norm_backward needs."""
+    _need_cuda("x", x)
+    if x.dim() != 2:
+        raise ValueError("x must be [n, d]")
+    dev, (n, d) = x.device, x.shape
+    if d >= 2 ** 31:
+        _need_sizes(d=d)
+    code = _dtype_code(x.dtype)
+    if residual is not None:
+        _need_like("residual", residual, x)
+    if sum_out is not None:
+        _need_like("sum_out", sum_out, x)
+    elif residual is not None:
+        sum_out = torch.empty_like(x)
+    wcode = _need_weight(weight, d, dev)
+    if bias is not None:
+        if weight is not None:
+            _need_shape("bias", bias, (d,), weight.dtype, dev)
+        else:
+            _need_cuda("bias", bias, dev)
+            wcode = _need_weight(bias, d, dev)
+    if (x.requires_grad or weight is not None and weight.requires_grad or bias is not None and bias.requires_grad or
+            residual is not None and residual.requires_grad):
+        _refuse_grad()
+    odt = x.dtype if out_dtype is None else out_dtype
+    f8 = odt is torch.float8_e4m3fn
+    ocode = RVQ_F8E4M3 if f8 else _dtype_code(odt)
+    if out is None:
+        out = torch.empty_like(x, dtype=odt)
+    else:
+        _need_shape("out", out, (n, d), odt, dev)
+    scale = torch.empty(n, dtype=torch.float32, device=dev) if f8 else None
+    mean = rstd = None
+    if need_stats:
+        mean, rstd = (torch.empty(n, dtype=torch.float32, device=dev) for _ in range(2))
+    _on_device(dev, _lib.rvq_layer_norm, x.data_ptr(), _address(residual), code, n, d,
+               _address(weight), _address(bias), wcode, eps, _address(sum_out), out.data_ptr(), ocode,
+               _address(scale), _address(mean), _address(rstd), _raw_stream(dev))
+    return LayerNormResult(out, scale, sum_out, mean, rstd)
+
+
+@functools.lru_cache(maxsize=256)
+def rvq_layer_norm_backward_workspace_size(n: int, d: int) -> int:
+    _need_sizes(d=d)
+    out = ctypes.c_size_t()
+    _check(_lib.rvq_layer_norm_backward_workspace_size(n, d, ctypes.byref(out)))
+    return out.value
+
+
+def rvq_layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                            weight: Optional[torch.Tensor] = None,
+                            dsum: Optional[torch.Tensor] = None, need_dweight: bool = True,
+                            need_dbias: bool = True, out: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None
+                            ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradient of rvq_layer_norm: (dx [n, d] in dy's type, dweight [d] fp32,
+    dbias [d] fp32).  h is the forward call's ``sum`` (x without a residual),
+    dsum the gradient that arrives at it; dx is the gradient of x and of the
+    residual.  out may be dy or dsum (in place)."""
+    _need_cuda("dy", dy)
+    dev = dy.device
+    if dy.dim() != 2:
+        raise ValueError("dy must be [n, d]")
+    n, d = dy.shape
+    if d >= 2 ** 31:
+        _need_sizes(d=d)
+    code = _dtype_code(dy.dtype)
+    _need_like("h", h, dy)
+    _need_shape("mean", mean, (n,), torch.float32, dev)
+    _need_shape("rstd", rstd, (n,), torch.float32, dev)
+    if dsum is not None:
+        _need_like("dsum", dsum, dy)
+    wcode = _need_weight(weight, d, dev)
+    if out is None:
+        out = torch.empty_like(dy)
+    else:
+        _need_like("out", out, dy)
+    if (dy.requires_grad or h.requires_grad or weight is not None and weight.requires_grad or
+            dsum is not None and dsum.requires_grad):
+        _refuse_grad()
+    dweight = torch.empty(d, dtype=torch.float32, device=dev) if need_dweight else None
+    dbias = torch.empty(d, dtype=torch.float32, device=dev) if need_dbias else None
+    ws, nbytes = None, 0
+    if need_dweight or need_dbias:
+        ws = _need_workspace(workspace, rvq_layer_norm_backward_workspace_size(n, d), dev)
+        nbytes = ws.numel()
+    _on_device(dev, _lib.rvq_layer_norm_backward, dy.data_ptr(), h.data_ptr(), code, n, d,
+               mean.data_ptr(), rstd.data_ptr(), _address(weight), wcode, _address(dsum), out.data_ptr(),
+               _address(dweight), _address(dbias), _address(ws), nbytes, _raw_stream(dev))
+    return out, dweight, dbias
+
+
+RVQ_SCALE_ROW, RVQ_SCALE_ROW_128, RVQ_SCALE_128_128 = 0, 1, 2
+
+
+def rvq_quantize_f8(x: torch.Tensor, block_rows: int = 1, transpose: bool = False
+                    ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """x [rows, cols] (fp32 or bf16) as (q float8_e4m3fn, scale fp32), operands of
+    rvq_matmul_f8: one scale for every 128 elements of a row (block_rows 1: scale
+    [rows, ceil(cols / 128)]) or for 128 x 128 (block_rows 128:
+    [ceil(rows / 128), ceil(cols / 128)]).  transpose gives x's transpose, with its
+    blocks along the transposed rows.  Rows of q whose length is no multiple of 16
+    are spaced apart so that each begins at a multiple of 128 bytes (q is a view)."""
+    _need_cuda("x", x)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    if x.requires_grad:
+        _refuse_grad()
+    dev, (rows, cols) = x.device, x.shape
+    code = _dtype_code(x.dtype)
+    r, c = (cols, rows) if transpose else (rows, cols)
+    stride = c if c % 16 == 0 else -(-c // 128) * 128
+    q = torch.empty((r, stride), dtype=torch.float8_e4m3fn, device=dev)
+    if stride != c:
+        q = q[:, :c]
+    scale = torch.empty((r if block_rows == 1 else -(-r // 128), -(-c // 128)), dtype=torch.float32, device=dev)
+    layout = RVQ_SCALE_ROW_128 if block_rows == 1 else RVQ_SCALE_128_128
+    _on_device(dev, _lib.rvq_quantize_f8, x.data_ptr(), code, rows, cols, layout, 1 if transpose else 0,
+               q.data_ptr(), stride, scale.data_ptr(), _raw_stream(dev))
+    return q, scale
+
+
+def _f8_operand(name: str, t: torch.Tensor, scale: torch.Tensor, dev: torch.device) -> Tuple[int, int]:
+    """(row stride, scale layout) of an 8-bit operand [rows, k]."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float8_e4m3fn and t.dim() == 2 and t.device == dev):
+        raise ValueError(f"{name} must be a float8_e4m3fn [rows, k] tensor on {dev}")
+    rows, k = t.shape
+    stride = t.stride(0) if rows > 1 else k
+    if k > 1 and t.stride(1) != 1 or stride < k:
+        raise ValueError(f"{name} must have its rows' elements side by side and rows that do not overlap")
+    if not (isinstance(scale, torch.Tensor) and scale.dtype is torch.float32 and scale.device == dev and
+            scale.is_contiguous()):
+        raise ValueError(f"{name}_scale must be a contiguous float32 tensor on {dev}")
+    blocks, shape = -(-k // 128), tuple(scale.shape)
+    if shape == (rows,):
+        layout = RVQ_SCALE_ROW
+    elif shape == (rows, blocks):
+        layout = RVQ_SCALE_ROW_128
+    elif shape == (-(-rows // 128), blocks):
+        layout = RVQ_SCALE_128_128
+    else:
+        raise ValueError(f"{name}_scale must be [{rows}], [{rows}, {blocks}] or [{-(-rows // 128)}, {blocks}] "
+                         f"(got {list(shape)})")
+    if k % 16 and stride >= k + -k % 16 and stride % 16 == 0 and t.data_ptr() % 16 == 0:
+        # rows that the library reads in pieces of 16 bytes: the last one's end, too
+        end = t.storage_offset() + (rows - 1) * stride + k + -k % 16
+        if end > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}: the last row's memory must reach to a multiple of 16 elements, as the others' "
+                             "(use .contiguous())")
+    return stride, layout
+
+
+def rvq_matmul_f8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+                  out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """a b^T [m, n] of 8-bit operands a [m, k] and b [n, k] (float8_e4m3fn) with
+    their scales: one for a row ([rows], as the norms' 8-bit outputs have), for
+    every 128 elements of a row ([rows, ceil(k / 128)]) or for 128 x 128 elements
+    ([ceil(rows / 128), ceil(k / 128)]).  Sums in fp32; out_dtype float32 or
+    bfloat16.  Rows may be spaced apart."""
+    dev = a.device
+    if not a.is_cuda:
+        raise ValueError("a must be a device tensor")
+    a_stride, a_layout = _f8_operand("a", a, a_scale, dev)
+    b_stride, b_layout = _f8_operand("b", b, b_scale, dev)
+    (m, k), n = a.shape, b.shape[0]
+    if b.shape[1] != k:
+        raise ValueError(f"a [{m}, {k}] and b {list(b.shape)} must have rows of the same length")
+    if a_scale.requires_grad or b_scale.requires_grad:
+        _refuse_grad()
+    ocode = _dtype_code(out_dtype)
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    else:
+        _need_shape("out", out, (m, n), out_dtype, dev)
+    _on_device(dev, _lib.rvq_matmul_f8, a.data_ptr(), a_stride, a_scale.data_ptr(), a_layout, b.data_ptr(), b_stride,
+               b_scale.data_ptr(), b_layout, m, n, k, out.data_ptr(), ocode, _raw_stream(dev))
+    return out
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: Optional[torch.Tensor]      # [n] fp32: of the given tokens
+    entropy: Optional[torch.Tensor]      # [n] fp32, nats
+    stats: torch.Tensor                  # [n, 2] fp32: largest logit, log sum exp((logit - largest) / temperature)
+    top_logprob: Optional[torch.Tensor]  # [n, top] fp32
+    top_ids: Optional[torch.Tensor]      # [n, top] int32
+
+
+@functools.lru_cache(maxsize=256)
+def rvq_token_logprobs_workspace_size(n: int, V: int, top: int = 0) -> int:
+    _need_sizes(V=V, top=top)
+    out = ctypes.c_size_t()
+    _check(_lib.rvq_token_logprobs_workspace_size(n, V, top, ctypes.byref(out)))
+    return out.value
+
+
+def _need_logits(logits: torch.Tensor) -> Tuple[torch.device, int, int, int]:
+    """(device, dtype code, n, V) of logits [n, V]."""
+    _need_cuda("logits", logits)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [n, V]")
+    n, V = logits.shape
+    if V >= 2 ** 31:
+        _need_sizes(V=V)
+    if logits.requires_grad:
+        _refuse_grad()
+    return logits.device, _dtype_code(logits.dtype), n, V
+
+
+def rvq_token_logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                       top: int = 0, need_entropy: bool = True, bad_ids: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> TokenLogprobs:
+    """Log probabilities of the tokens ids [n] (int32; -1: none) under
+    softmax(logits / temperature) for logits [n, V] (fp32 or bf16; -inf masks a
+    token), each row's entropy, and its ``top`` best tokens (up to 64, larger
+    first, lower IDs first among equals, then -inf and -1).  ``stats`` is what
+    rvq_token_logprobs_backward needs; stats[:, 0] / temperature + stats[:, 1] is
+    the row's log-sum-exp.  A row with NaN or +inf gives NaN."""
+    dev, code, n, V = _need_logits(logits)
+    nbytes = rvq_token_logprobs_workspace_size(n, V, top)
+    logprob = entropy = top_logprob = top_ids = ws = None
+    if ids is not None:
+        _need_shape("ids", ids, (n,), torch.int32, dev)
+        logprob = torch.empty(n, dtype=torch.float32, device=dev)
+    if bad_ids is not None:
+        _need_shape("bad_ids", bad_ids, (1,), torch.int32, dev)
+    if need_entropy:
+        entropy = torch.empty(n, dtype=torch.float32, device=dev)
+    stats = torch.empty((n, 2), dtype=torch.float32, device=dev)
+    if top:
+        top_logprob = torch.empty((n, top), dtype=torch.float32, device=dev)
+        top_ids = torch.empty((n, top), dtype=torch.int32, device=dev)
+    if nbytes:
+        ws = _need_workspace(workspace, nbytes, dev)
+        nbytes = ws.numel()
+    _on_device(dev, _lib.rvq_token_logprobs, logits.data_ptr(), code, n, V, _address(ids), temperature,
+               _address(logprob), _address(entropy), stats.data_ptr(), top, _address(top_logprob),
+               _address(top_ids), _address(bad_ids), _address(ws), nbytes, _raw_stream(dev))
+    return TokenLogprobs(logprob, entropy, stats, top_logprob, top_ids)
+
+
+def rvq_token_logprobs_backward(logits: torch.Tensor, ids: Optional[torch.Tensor], stats: torch.Tensor,
+                                dlogprob: Optional[torch.Tensor] = None,
+                                entropy: Optional[torch.Tensor] = None,
+                                dentropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of rvq_token_logprobs with respect to the logits, in their type:
+    dlogprob and dentropy [n] fp32 are what arrives at the log probabilities and
+    at the entropies (dentropy needs the forward call's entropy).  The cross
+    entropy's gradient is that of dlogprob = -1 / n.  out may be logits itself."""
+    dev, code, n, V = _need_logits(logits)
+    _need_shape("stats", stats, (n, 2), torch.float32, dev)
+    if ids is not None:
+        _need_shape("ids", ids, (n,), torch.int32, dev)
+    if dlogprob is None and dentropy is None:
+        raise ValueError("dlogprob and dentropy must not both be None")
+    if dlogprob is not None:
+        _need_shape("dlogprob", dlogprob, (n,), torch.float32, dev)
+        if ids is None:
+            raise ValueError("dlogprob needs ids")
+    if dentropy is not None:
+        _need_shape("dentropy", dentropy, (n,), torch.float32, dev)
+        if entropy is None:
+            raise ValueError("dentropy needs entropy")
+        _need_shape("entropy", entropy, (n,), torch.float32, dev)
+    if dlogprob is not None and dlogprob.requires_grad or dentropy is not None and dentropy.requires_grad:
+        _refuse_grad()
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _need_like("out", out, logits)
+    _on_device(dev, _lib.rvq_token_logprobs_backward, logits.data_ptr(), code, n, V, _address(ids), temperature,
+               stats.data_ptr(), _address(dlogprob), _address(entropy), _address(dentropy), out.data_ptr(),
+               _raw_stream(dev))
+    return out
+
+
+class DistillLoss(NamedTuple):
+    loss: torch.Tensor   # [n] fp32
+    stats: torch.Tensor  # [n, 4] fp32, for rvq_distill_loss_backward
+
+
+def _need_teacher(teacher_ids: torch.Tensor, teacher: torch.Tensor, n: int, dev: torch.device) -> int:
+    """k of teacher_ids [n, k] and teacher [n, k]."""
+    _need_cuda("teacher_ids", teacher_ids, dev)
+    if teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids must be int32 [n, k]")
+    k = teacher_ids.shape[1]
+    if k >= 2 ** 31:
+        _need_sizes(k=k)
+    _need_shape("teacher_ids", teacher_ids, (n, k), torch.int32, dev)
+    _need_shape("teacher", teacher, (n, k), torch.float32, dev)
+    if teacher.requires_grad:
+        _refuse_grad()
+    return k
+
+
+def rvq_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher: torch.Tensor,
+                     temperature: float = 1.0, tail: bool = False,
+                     bad_ids: Optional[torch.Tensor] = None) -> DistillLoss:
+    """Kullback-Leibler distance of softmax(logits / temperature), logits [n, V]
+    (fp32 or bf16), from a teacher's k <= 256 top tokens: teacher_ids [n, k]
+    int32 (-1: no entry; a repeated ID counts where it comes first) and teacher
+    [n, k] fp32.  tail false: the teacher's distribution is softmax(teacher /
+    temperature) over its entries (logits, or log probabilities at temperature
+    1).  tail true: teacher holds log probabilities at this temperature, as
+    rvq_token_logprobs gives them, and all other tokens are one outcome more.
+    No factor temperature^2 is applied."""
+    dev, code, n, V = _need_logits(logits)
+    k = _need_teacher(teacher_ids, teacher, n, dev)
+    if bad_ids is not None:
+        _need_shape("bad_ids", bad_ids, (1,), torch.int32, dev)
+    loss = torch.empty(n, dtype=torch.float32, device=dev)
+    stats = torch.empty((n, 4), dtype=torch.float32, device=dev)
+    _on_device(dev, _lib.rvq_distill_loss, logits.data_ptr(), code, n, V, teacher_ids.data_ptr(), teacher.data_ptr(),
+               k, 1 if tail else 0, temperature, loss.data_ptr(), stats.data_ptr(), _address(bad_ids),
+               _raw_stream(dev))
+    return DistillLoss(loss, stats)
+
+
+def rvq_distill_loss_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher: torch.Tensor,
+                              stats: torch.Tensor, dloss: torch.Tensor, temperature: float = 1.0,
+                              tail: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of rvq_distill_loss with respect to the logits, in their type;
+    dloss [n] fp32 is what arrives at the losses (0: a row of zeros).  The other
+    arguments are those of the forward call.  out may be logits itself."""
+    dev, code, n, V = _need_logits(logits)
+    k = _need_teacher(teacher_ids, teacher, n, dev)
+    _need_shape("stats", stats, (n, 4), torch.float32, dev)
+    _need_shape("dloss", dloss, (n,), torch.float32, dev)
+    if dloss.requires_grad:
+        _refuse_grad()
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _need_like("out", out, logits)
+    _on_device(dev, _lib.rvq_distill_loss_backward, logits.data_ptr(), code, n, V, teacher_ids.data_ptr(),
+               teacher.data_ptr(), k, 1 if tail else 0, temperature, stats.data_ptr(), dloss.data_ptr(),
+               out.data_ptr(), _raw_stream(dev))
+    return out
 
 
 def rvq_idcache_resume(path: str, n: int, L: int, K: int, chunk_rows: int) -> int:

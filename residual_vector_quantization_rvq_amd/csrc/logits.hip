@@ -1,0 +1,817 @@
+// logits.hip -- rows of logits x over V tokens at temperature T: log probabilities
+// of given tokens, entropies and top alternatives, the distillation loss of a
+// teacher's top logits, and the gradients of both.
+//
+//   M = max x,  d_j = (M - x_j) / T >= 0,  S = sum exp(-d_j)
+//   log p_j = -d_j - log S,   H = log S + sum d_j exp(-d_j) / S
+//
+// H is a sum of two terms that are not negative, and log S is log1p of the sum
+// without one of its largest terms, so that a row that is all but certain keeps the
+// precision of its small numbers.  Sums are fp32: a thread adds its elements in
+// four chains, lanes and waves join them in a tree; exponentials are the
+// hardware's of base 2 (the factor log2(e) / T is one multiplication).
+//
+// Bound by memory, and for bf16 nearly by the arithmetic too (about eleven
+// instructions an element, four of them the exponential): each row is read once,
+// with a running maximum and sum.  What a row needs after that (top alternatives, the
+// sum of an all but certain row) is read again by the few threads whose largest
+// value says that they hold it.
+#include "head.h"
+
+namespace rvq {
+
+namespace {
+
+constexpr int kMaxGroups = 1 << 20;  // workgroups of a launch; rows beyond are looped over
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kFar = 300.f;        // powers of two: beyond it nothing is left of an fp32 number
+constexpr int kPieces = 4;           // 16-byte pieces that a thread loads at once
+
+__device__ __forceinline__ float exp2_neg(float d) { return __builtin_amdgcn_exp2f(-d); }
+
+// A row (or a part of one) as it is summed: the largest value m, t = sum exp2((x - m) c)
+// and q = sum (m - x) c exp2((x - m) c).  Nothing yet (or -inf alone): m = -inf, t = 0.
+struct Sums {
+  float m, t, q;
+};
+
+template <typename T>
+__device__ __forceinline__ void load_values(const T *row, int at, int left, float (&v)[kPiece<T>]) {
+  unpack(load_piece(row + (left > 0 ? at : 0), left), v);
+#pragma unroll
+  for (int e = 0; e < kPiece<T>; ++e)
+    if (e >= left) v[e] = -INFINITY;
+}
+
+template <int N, bool ENT>
+__device__ __forceinline__ void add_values(const float (&v)[N], float c, Sums &s) {
+  float mc = v[0];
+#pragma unroll
+  for (int e = 1; e < N; ++e) mc = fmaxf(mc, v[e]);
+  if (mc > s.m) {
+    if (s.m > -INFINITY) {
+      const float d = fminf((mc - s.m) * c, kFar), f = exp2_neg(d);
+      if (ENT) s.q = (s.q + d * s.t) * f;
+      s.t *= f;
+    }
+    s.m = mc;
+  }
+  const float m = s.m == -INFINITY ? 0.f : s.m;
+  float t[4] = {0.f, 0.f, 0.f, 0.f}, q[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float d = (m - v[e]) * c, x = exp2_neg(d);
+    t[e & 3] += x;
+    if (ENT) q[e & 3] += fminf(d, kFar) * x;  // a masked value: 0
+  }
+  s.t += (t[0] + t[1]) + (t[2] + t[3]);
+  if (ENT) s.q += (q[0] + q[1]) + (q[2] + q[3]);
+}
+
+// The values of columns [0, cols) of a row that are this thread's: pieces lane,
+// lane + W, ...  With BITS, columns whose bit is set in `bits` are left out.
+template <typename T, int W, bool ENT, bool BITS>
+__device__ __forceinline__ void stream_row(const T *row, int cols, int lane, float c, const uint8_t *bits, Sums &s) {
+  constexpr int N = kPiece<T>, P = kPieces;
+  for (int base = 0; base < cols; base += W * P * N) {
+    float v[P * N];
+    const int at = base + lane * N;
+    if (base + W * P * N <= cols) {
+      u32x4 raw[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) raw[p] = load16(row + at + p * W * N);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float u[N];
+        unpack(raw[p], u);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[p * N + e] = u[e];
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float u[N];
+        load_values(row, at + p * W * N, cols - (at + p * W * N), u);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[p * N + e] = u[e];
+      }
+    }
+    if constexpr (BITS) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int i = at + p * W * N;
+        uint32_t b = i < cols ? bits[i >> 3] : 0;
+        if (N == 4) b >>= i & 4;
+        if (b & ((1u << N) - 1)) {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (b >> e & 1) v[p * N + e] = -INFINITY;
+        }
+      }
+    }
+    add_values<P * N, ENT>(v, c, s);
+  }
+}
+
+// ---- over the W threads of a row; W == 64: a wave, else the whole workgroup ----
+template <int W>
+__device__ __forceinline__ float all_max(float v, float *red) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  if constexpr (W > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < W / 64; ++w) v = fmaxf(v, red[w]);
+  }
+  return v;
+}
+template <int W, typename F>
+__device__ __forceinline__ F all_sum(F v, F *red) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  if constexpr (W > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < W / 64; ++w) v += red[w];
+  }
+  return v;
+}
+// the smallest
+template <int W>
+__device__ __forceinline__ int all_min(int v, int *red) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v = min(v, __shfl_xor(v, off, 64));
+  if constexpr (W > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < W / 64; ++w) v = min(v, red[w]);
+  }
+  return v;
+}
+
+// The threads' sums as one: m, t and q of all (a thread's own stay as they are).
+template <int W, bool ENT>
+__device__ __forceinline__ Sums join_threads(const Sums &s, float c, float *red) {
+  Sums r;
+  r.m = all_max<W>(s.m, red);
+  float t = s.t, q = s.q;
+  if (!(t == 0.f)) {  // NaN goes on
+    const float d = fminf((r.m - s.m) * c, kFar), f = exp2_neg(d);
+    if (ENT) q = (q + d * t) * f;
+    t *= f;
+    if (r.m != r.m || r.m - s.m != r.m - s.m) t = NAN;  // infinite maxima
+  }
+  r.t = all_sum<W>(t, red);
+  r.q = ENT ? all_sum<W>(q, red) : 0.f;
+  return r;
+}
+
+// The sum without one of its largest terms.  Where the rest is small beside that
+// term, it is added up anew without it: the thread that holds the term (the first of
+// them) gives its values to all.
+template <typename T, int W>
+__device__ __forceinline__ float rest_of(const T *row, int cols, int lane, float c, const Sums &own, const Sums &all,
+                                         float *red) {
+  if (!(all.t < 1.5f) || all.t == 0.f) return all.t - 1.f;
+  constexpr int N = kPiece<T>;
+  const int owner = all_min<W>(own.m == all.m ? lane : W, (int *)red);
+  float rest = 0.f;
+  if (lane != owner && own.t != 0.f) rest = own.t * exp2_neg(fminf((all.m - own.m) * c, kFar));
+  for (int64_t i = ((int64_t)lane * W + owner) * N; i < cols; i += (int64_t)W * W * N) {
+    float v[N];
+    load_values(row, (int)i, cols - (int)i, v);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (v[e] != all.m) rest += exp2_neg((all.m - v[e]) * c);
+  }
+  return all_sum<W>(rest, red);
+}
+
+// ---- values and places as one number: larger values first, then lower places ----
+// -0 and +0 are one value.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float from_order_bits(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ uint64_t order_key(float v, int at) {
+  return ((uint64_t)order_bits(v) << 32) | (uint32_t)~at;
+}
+constexpr uint32_t kNoneBits = 0x007fffffu;  // order_bits(-inf): masked values are no alternatives
+constexpr int kMaxCand = 1024;
+static_assert(kMaxTop <= kMaxCand, "the join ranks at least one slice's keys");
+
+// The `top` largest of a row's columns [0, cols), larger first, to out[0 .. top - 1]
+// (0: none left).  tmax holds each thread's largest value as order_bits.
+//
+// At least `top` threads have a largest value of the top-th largest of these or
+// more, so it bounds the answer from below: only threads that reach it look at their
+// values again, and the few that reach it are ranked by counting.  (Of that bound
+// the upper 16 bits are found, by one wave: for bf16 all there is.)  Should more
+// than kMaxCand values reach it (a row of mostly equal values), the largest is
+// taken `top` times over the whole row.
+template <typename T, int W>
+__device__ void top_of_row(const T *row, int cols, int lane, float own_max, int top, uint32_t *tmax, uint64_t *cand,
+                           int *count, uint64_t *out) {
+  constexpr int N = kPiece<T>;
+  const uint32_t own = order_bits(own_max);
+  __syncthreads();
+  tmax[lane] = own;
+  if (lane == 0) count[0] = 0;
+  __syncthreads();
+  if (lane < 64) {
+    uint32_t mine[W / 64], bound = 0;
+#pragma unroll
+    for (int i = 0; i < W / 64; ++i) mine[i] = tmax[i * 64 + lane];
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t trial = bound | (1u << bit);
+      int reached = 0;
+#pragma unroll
+      for (int i = 0; i < W / 64; ++i) reached += __popcll(__ballot(mine[i] >= trial));
+      if (reached >= top) bound = trial;
+    }
+    if (lane == 0) count[1] = (int)bound;
+  }
+  __syncthreads();
+  const uint32_t bound = max((uint32_t)count[1], kNoneBits + 1);
+  if (own >= bound) {
+    for (int i = lane * N; i < cols; i += W * N) {
+      float v[N];
+      load_values(row, i, cols - i, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (order_bits(v[e]) >= bound) {
+          const int at = atomicAdd(count, 1);  // the order does not matter: ranked below
+          if (at < kMaxCand) cand[at] = order_key(v[e], i + e);
+        }
+    }
+  }
+  __syncthreads();
+  const int found = count[0];
+  if (found <= kMaxCand) {
+    for (int i = lane; i < found; i += W) {
+      const uint64_t key = cand[i];
+      int rank = 0;
+      for (int j = 0; j < found; ++j) rank += cand[j] > key;
+      if (rank < top) out[rank] = key;
+    }
+    for (int i = found + lane; i < top; i += W) out[i] = 0;
+    __syncthreads();
+    return;
+  }
+  uint64_t last = ~(uint64_t)0;
+  for (int r = 0; r < top; ++r) {
+    uint64_t best = 0;
+    if (own > kNoneBits)
+      for (int i = lane * N; i < cols; i += W * N) {
+        float v[N];
+        load_values(row, i, cols - i, v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const uint64_t key = order_key(v[e], i + e);
+          if (key < last && key > best && order_bits(v[e]) > kNoneBits) best = key;
+        }
+      }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      const uint64_t o = __shfl_xor((unsigned long long)best, off, 64);
+      best = o > best ? o : best;
+    }
+    __syncthreads();
+    if ((lane & 63) == 0) cand[lane >> 6] = best;
+    __syncthreads();
+    best = cand[0];
+#pragma unroll
+    for (int w = 1; w < W / 64; ++w) best = cand[w] > best ? cand[w] : best;
+    if (lane == 0) out[r] = best;
+    last = best == 0 ? 0 : best;
+  }
+  __syncthreads();
+}
+
+// ---- what a row's sums give ----
+// log S; NaN of a row that holds NaN or +inf; 0 of a row without a value above -inf
+__device__ __forceinline__ float log_sum(float m, float rest) {
+  return m == -INFINITY && !(rest != rest) ? 0.f : log1pf(rest);
+}
+__device__ __forceinline__ float log_prob(float x, float m, float log_s, float inv_t) {
+  if (m == -INFINITY && !(log_s != log_s)) return -INFINITY;  // a row without a token
+  return -((m - x) * inv_t) - log_s;
+}
+
+template <typename T>
+__device__ void finish_row(const LogprobArgs &a, int64_t row, float m, float rest, float q) {
+  const float log_s = log_sum(m, rest);
+  a.stats[2 * row] = m;
+  a.stats[2 * row + 1] = log_s;
+  if (a.entropy) a.entropy[row] = m == -INFINITY && !(log_s != log_s) ? 0.f : log_s + q * kLn2 / (1.f + rest);
+  if (a.ids) {
+    const int id = a.ids[row];
+    float lp = 0.f;
+    if (id >= 0 && id < a.V)
+      lp = log_prob(load_f32((const T *)a.x, row * a.V + id), m, log_s, a.inv_t);
+    else if (id != -1 && a.bad)
+      atomicAdd(a.bad, 1u);
+    a.logprob[row] = lp;
+  }
+}
+__device__ __forceinline__ void finish_top(const LogprobArgs &a, int64_t row, int i, uint64_t key, float m,
+                                           float log_s) {
+  const bool none = key == 0 || log_s != log_s;
+  a.top_ids[row * a.top + i] = none ? -1 : (int)~(uint32_t)key;
+  a.top_logprob[row * a.top + i] =
+      log_s != log_s ? NAN : key == 0 ? -INFINITY : log_prob(from_order_bits((uint32_t)(key >> 32)), m, log_s, a.inv_t);
+}
+
+// a slice's sums and top keys in the workspace, in floats
+__host__ __device__ constexpr int part_floats(int top) { return 4 + 2 * top; }
+
+}  // namespace
+
+template <typename T, int W, bool ENT, bool TOP>
+__global__ __launch_bounds__(W < 256 ? 256 : W) void logprob_kernel(LogprobArgs a, LogprobPlan plan) {
+  constexpr int R = W < 256 ? 256 / W : 1;
+  __shared__ float red[W / 64 > 4 ? W / 64 : 4];
+  __shared__ uint32_t tmax[TOP ? W : 1];
+  __shared__ uint64_t cand[TOP ? kMaxCand : 1];
+  __shared__ uint64_t best[TOP ? kMaxTop : 1];
+  __shared__ int count[2];
+  const int lane = threadIdx.x % W;
+  const float c = a.inv_t * kLog2e;
+  const int64_t jobs = a.n * plan.slices;
+  // W > 64: the job is the same for the whole workgroup, as the barriers need
+  for (int64_t job = (int64_t)blockIdx.x * R + threadIdx.x / W; job < jobs; job += (int64_t)gridDim.x * R) {
+    const int64_t row = plan.slices == 1 ? job : job / plan.slices;
+    const int64_t c0 = (job - row * plan.slices) * plan.slice;
+    const int cols = (int)(a.V - c0 < plan.slice ? a.V - c0 : plan.slice);
+    const T *x = (const T *)a.x + row * a.V + c0;
+    Sums s = {-INFINITY, 0.f, 0.f};
+    stream_row<T, W, ENT, false>(x, cols, lane, c, nullptr, s);
+    const Sums all = join_threads<W, ENT>(s, c, red);
+    const float rest = rest_of<T, W>(x, cols, lane, c, s, all, red);
+    if constexpr (TOP) top_of_row<T, W>(x, cols, lane, s.m, a.top, tmax, cand, count, best);
+    if (plan.slices == 1) {
+      if (lane == 0) finish_row<T>(a, row, all.m, rest, all.q);
+      if constexpr (TOP) {
+        const float log_s = log_sum(all.m, rest);
+        for (int i = lane; i < a.top; i += W) finish_top(a, row, i, best[i], all.m, log_s);
+      }
+    } else {
+      float *part = a.part + job * part_floats(TOP ? a.top : 0);
+      if (lane == 0) {
+        part[0] = all.m;
+        part[1] = rest;
+        part[2] = all.q;
+      }
+      if constexpr (TOP)
+        for (int i = lane; i < a.top; i += W) ((uint64_t *)(part + 4))[i] = best[i] ? best[i] - (uint32_t)c0 : 0;
+    }
+  }
+}
+
+// A row out of its slices: one wave joins their sums, the workgroup ranks their keys.
+template <typename T>
+__global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a, LogprobPlan plan) {
+  __shared__ uint64_t cand[kMaxCand];
+  __shared__ float got[2];
+  const int64_t row = blockIdx.x;
+  const float *part = a.part + row * plan.slices * part_floats(a.top);
+  const float c = a.inv_t * kLog2e;
+  if (threadIdx.x < 64) {
+    const int i = threadIdx.x;
+    const bool in = i < plan.slices;
+    const float *p = part + (in ? i : 0) * part_floats(a.top);
+    const float m = in ? p[0] : -INFINITY, rest = in ? p[1] : -1.f, q = in ? p[2] : 0.f;
+    const float top = all_max<64>(m, nullptr);
+    // a slice's whole sum, but for the first that holds the largest value
+    const uint64_t holds = __ballot(m == top);
+    const bool owner = (holds & (((uint64_t)1 << i) - 1)) == 0 && m == top;
+    float t = rest + 1.f, r = rest, qq = q;
+    if (t != 0.f) {
+      const float d = fminf((top - m) * c, kFar), f = exp2_neg(d);
+      qq = (q + d * t) * f;
+      r = owner ? rest : t * f;
+      if (top - m != top - m) r = NAN;
+    } else {
+      r = 0.f;
+      qq = 0.f;
+    }
+    r = all_sum<64>(r, (float *)nullptr);
+    qq = all_sum<64>(qq, (float *)nullptr);
+    if (top == -INFINITY && !(r != r)) r = -1.f;
+    if (i == 0) {
+      finish_row<T>(a, row, top, r, qq);
+      got[0] = top;
+      got[1] = log_sum(top, r);
+    }
+  }
+  if (a.top == 0) return;
+  const int total = plan.slices * a.top;
+  for (int i = threadIdx.x; i < total; i += 256)
+    cand[i] = ((const uint64_t *)(part + (i / a.top) * part_floats(a.top) + 4))[i % a.top];
+  __syncthreads();
+  int some = 0;
+  for (int i = threadIdx.x; i < total; i += 256) {
+    const uint64_t key = cand[i];
+    if (key == 0) continue;
+    int rank = 0;
+    for (int j = 0; j < total; ++j) rank += cand[j] > key;
+    if (rank < a.top) finish_top(a, row, rank, key, got[0], got[1]);
+  }
+  for (int i = 0; i < total; ++i) some += cand[i] != 0;
+  for (int i = some + threadIdx.x; i < a.top; i += 256) finish_top(a, row, i, 0, got[0], got[1]);
+}
+
+LogprobPlan logprob_plan(int64_t n, int V, int top) {
+  // fewer rows than would fill the device, and long ones: several workgroups each
+  int64_t slices = 1;
+  if (n < 256 && V >= 8192) {
+    slices = ceil_div(512, n);
+    if (slices > V / 2048) slices = V / 2048;
+    if (slices > 64) slices = 64;  // a lane each in the join
+    if (top > 0 && slices * top > kMaxCand) slices = kMaxCand / top;
+  }
+  const int64_t slice = round_up(ceil_div(V, slices), 8);
+  return {(int)ceil_div(V, slice), slice};
+}
+size_t logprob_part_floats(int64_t n, const LogprobPlan &p, int top) {
+  return p.slices == 1 ? 0 : (size_t)n * p.slices * part_floats(top);
+}
+
+template <typename T, int W, bool TOP>
+static void start_logprobs(const LogprobArgs &a, const LogprobPlan &plan, hipStream_t s) {
+  constexpr int R = W < 256 ? 256 / W : 1;
+  const int64_t groups = ceil_div(a.n * plan.slices, R);
+  const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
+  const int threads = W < 256 ? 256 : W;
+  if (a.entropy)
+    logprob_kernel<T, W, true, TOP><<<grid, threads, 0, s>>>(a, plan);
+  else
+    logprob_kernel<T, W, false, TOP><<<grid, threads, 0, s>>>(a, plan);
+}
+
+template <typename T>
+static hipError_t logprobs(const LogprobArgs &a, hipStream_t s) {
+  const LogprobPlan plan = logprob_plan(a.n, a.V, a.top);
+  const int64_t cols = plan.slice;
+  if (a.top > 0) {
+    if (cols <= 16384)
+      start_logprobs<T, 256, true>(a, plan, s);
+    else
+      start_logprobs<T, 1024, true>(a, plan, s);
+  } else if (cols <= 2048 && plan.slices == 1) {
+    start_logprobs<T, 64, false>(a, plan, s);
+  } else if (cols <= 16384) {
+    start_logprobs<T, 256, false>(a, plan, s);
+  } else {
+    start_logprobs<T, 1024, false>(a, plan, s);
+  }
+  if (plan.slices > 1) logprob_join_kernel<T><<<dim3((unsigned)a.n), 256, 0, s>>>(a, plan);
+  return hipGetLastError();
+}
+
+hipError_t launch_logprobs(const LogprobArgs &a, bool x_bf16, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  return x_bf16 ? logprobs<uint16_t>(a, s) : logprobs<float>(a, s);
+}
+
+// ---- the gradient of log probabilities and entropies ----
+//   dx_j = (g ([j = id] - p_j) - gH p_j (log p_j + H)) / T
+// With e_j = exp(-d_j) = S p_j this is e_j (A + B d_j), A = -(g + gH (H - log S)) / (S T),
+// B = gH / (S T); the given token's own element uses 1 - p = -expm1(log p).
+template <typename T, int W>
+__global__ __launch_bounds__(W < 256 ? 256 : W) void logprob_grad_kernel(LogprobGradArgs a, int slices, int64_t slice) {
+  constexpr int R = W < 256 ? 256 / W : 1, N = kPiece<T>, P = kPieces;
+  const int lane = threadIdx.x % W;
+  const float c = a.inv_t * kLog2e;
+  const int64_t jobs = a.n * slices;
+  for (int64_t job = (int64_t)blockIdx.x * R + threadIdx.x / W; job < jobs; job += (int64_t)gridDim.x * R) {
+    const int64_t row = slices == 1 ? job : job / slices;
+    const int64_t c0 = (job - row * slices) * slice;
+    const int cols = (int)(a.V - c0 < slice ? a.V - c0 : slice);
+    const T *x = (const T *)a.x + row * a.V + c0;
+    T *dx = (T *)a.dx + row * a.V + c0;
+    const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
+    int64_t id = a.ids ? a.ids[row] : -1;
+    if (id < 0 || id >= a.V) id = -1;
+    const float g = a.dlogprob && id >= 0 ? a.dlogprob[row] : 0.f;
+    const float gh = a.dentropy ? a.dentropy[row] : 0.f;
+    // no weight, or no token to put it on: zeros, whatever the logits are
+    const bool zero = (g == 0.f && gh == 0.f) || (m == -INFINITY && !(log_s != log_s));
+    const float h = gh != 0.f ? a.entropy[row] : 0.f;
+    const float k = expf(-log_s) * a.inv_t;
+    const float A = -(g + gh * (h - log_s)) * k, B = gh * kLn2 * k;
+    const int64_t at_id = id >= 0 ? id - c0 : -1;
+    for (int64_t base = 0; base < cols; base += W * P * N) {
+      u32x4 raw[P];
+      if (!zero) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int64_t i = base + (p * W + lane) * N;
+          raw[p] = load_piece(x + (i < cols ? i : 0), (int)(cols - i < N ? cols - i : N));
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int64_t i = base + (p * W + lane) * N;
+        if (i >= cols) continue;
+        float v[N];
+        if (zero) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[e] = 0.f;
+        } else {
+          unpack(raw[p], v);
+          const bool has = at_id >= i && at_id < i + N;
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const float x_e = v[e];
+            const float d = fminf((m - x_e) * c, kFar);
+            v[e] = exp2_neg(d) * (A + B * d);
+            if (has && i + e == at_id) {
+              const float lp = log_prob(x_e, m, log_s, a.inv_t);
+              const float p_id = expf(lp);
+              v[e] = (-g * expm1f(lp) - (p_id > 0.f ? gh * p_id * (lp + h) : 0.f)) * a.inv_t;
+            }
+          }
+        }
+        store_n<N>(dx + i, (int)(cols - i < N ? cols - i : N), v);  // may be x: this lane's own piece
+      }
+    }
+  }
+}
+
+template <typename T>
+static hipError_t logprobs_grad(const LogprobGradArgs &a, hipStream_t s) {
+  constexpr int N = kPiece<T>;
+  // a workgroup a row; of few rows, several
+  int64_t slices = 1;
+  if (a.n < 1024) {
+    slices = ceil_div(2048, a.n);
+    const int64_t most = ceil_div(a.V, 256 * kPieces * N);
+    if (slices > most) slices = most;
+  }
+  const int64_t slice = round_up(ceil_div(a.V, slices), 8);
+  slices = ceil_div(a.V, slice);
+  if (slices == 1 && a.V <= 2048) {
+    const int64_t groups = ceil_div(a.n, 4);
+    logprob_grad_kernel<T, 64>
+        <<<dim3((unsigned)(groups < kMaxGroups ? groups : kMaxGroups)), 256, 0, s>>>(a, 1, slice);
+  } else {
+    const int64_t groups = a.n * slices;
+    logprob_grad_kernel<T, 256>
+        <<<dim3((unsigned)(groups < kMaxGroups ? groups : kMaxGroups)), 256, 0, s>>>(a, (int)slices, slice);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_logprobs_grad(const LogprobGradArgs &a, bool x_bf16, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  return x_bf16 ? logprobs_grad<uint16_t>(a, s) : logprobs_grad<float>(a, s);
+}
+
+// ---- distillation ----
+// The teacher gives k tokens of each row and values t.  Without tail, q is the
+// softmax of t / T over them; with tail, q = exp(t), and all other tokens are one
+// outcome more: q_T = 1 - sum q beside p_T, the sum of their p.
+//   loss = sum q_e (log q_e - log p_e) (+ q_T (log q_T - log p_T))
+//   dx_j = (p_j - q_j) / T;   with tail, of the others: p_j (1 - q_T / p_T) / T
+// (without tail, q_j = 0 for the others.)  A repeated ID counts where it comes
+// first; a row without a valid ID has no loss and no gradient.
+//
+// One thread an entry; q and the loss are computed in 64 bits (a few numbers a
+// row).  p_T is added up over the others themselves, whose places a map of bits in
+// LDS tells apart, not as 1 - sum p, which would lose a small p_T.
+
+namespace {
+
+constexpr int kSegment = 1 << 18;  // columns that the map holds at once: 32 KB
+
+struct Entry {
+  int id;       // -1: does not count
+  double q, logq;
+};
+// The row's entry of this thread; the row's W threads call it together.
+template <int W>
+__device__ Entry entry_of(const DistillArgs &a, int64_t row, int lane, int *ids, double *red, bool count_bad) {
+  int id = -1;
+  double t = 0.0;
+  if (lane < a.k) {
+    id = a.ids[row * a.k + lane];
+    if (id < 0 || id >= a.V) {
+      if (id != -1 && a.bad && count_bad) atomicAdd(a.bad, 1u);
+      id = -1;
+    }
+    t = (double)a.teacher[row * a.k + lane];
+  }
+  if (W > 64) __syncthreads();
+  if (lane < a.k) ids[lane] = id;
+  if (W > 64)
+    __syncthreads();
+  else
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (id >= 0) {
+    bool again = false;
+    for (int j = 0; j < lane; ++j) again |= ids[j] == id;
+    if (again) id = -1;
+  }
+  Entry e = {id, 0.0, 0.0};
+  if (a.tail) {
+    e.logq = t;
+  } else {
+    t *= (double)a.inv_t;
+    // NaN is not lost: it returns in the sum
+    float top = all_max<W>(id >= 0 ? (float)t : -INFINITY, (float *)red);
+    if (top == -INFINITY) top = 0.f;
+    const double z = all_sum<W>(id >= 0 ? exp(t - (double)top) : 0.0, red);
+    if (z == 0.0) e.id = -1;  // all of them masked: the teacher says nothing
+    e.logq = t - (double)top - log(z);
+  }
+  if (e.id >= 0) e.q = exp(e.logq);
+  return e;
+}
+
+template <int W>
+__device__ __forceinline__ void row_barrier() {
+  if (W > 64)
+    __syncthreads();
+  else
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+}  // namespace
+
+template <typename T, int W, bool TAIL>
+__global__ __launch_bounds__(W < 256 ? 256 : W) void distill_kernel(DistillArgs a, int words) {
+  constexpr int R = W < 256 ? 256 / W : 1;
+  extern __shared__ uint32_t maps[];  // [R][words]
+  __shared__ double red64[R][16];
+  __shared__ int ids[R][W < kMaxTeacher ? W : kMaxTeacher];
+  const int lane = threadIdx.x % W, sub = threadIdx.x / W;
+  uint32_t *map = maps + sub * words;
+  double *red = red64[sub];
+  const float c = a.inv_t * kLog2e;
+  for (int64_t row = (int64_t)blockIdx.x * R + sub; row < a.n; row += (int64_t)gridDim.x * R) {
+    const T *x = (const T *)a.x + row * a.V;
+    const Entry en = entry_of<W>(a, row, lane, ids[sub], red, true);
+    const float xe = en.id >= 0 ? load_f32(x, en.id) : -INFINITY;
+    Sums s = {-INFINITY, 0.f, 0.f};
+    if constexpr (TAIL) {
+      for (int64_t c0 = 0; c0 < a.V; c0 += kSegment) {
+        const int cols = (int)(a.V - c0 < kSegment ? a.V - c0 : kSegment);
+        row_barrier<W>();
+        for (int i = lane; i < words; i += W) map[i] = 0;
+        row_barrier<W>();
+        if (en.id >= c0 && en.id < c0 + cols) atomicOr(map + ((en.id - (int)c0) >> 5), 1u << (en.id & 31));
+        row_barrier<W>();
+        stream_row<T, W, false, true>(x + c0, cols, lane, c, (const uint8_t *)map, s);
+      }
+    } else {
+      stream_row<T, W, false, false>(x, a.V, lane, c, nullptr, s);
+    }
+    const Sums others = join_threads<W, false>(s, c, (float *)red);  // without tail: all tokens
+    float m = others.m, S = others.t;
+    if (TAIL) {
+      m = fmaxf(m, all_max<W>(xe, (float *)red));
+      float t = xe > -INFINITY || xe != xe ? exp2_neg((m - xe) * c) : 0.f;
+      t = all_sum<W>(t, (float *)red);
+      S = t + (others.t == 0.f ? 0.f : others.t * exp2_neg(fminf((m - others.m) * c, kFar)));
+      if (m == INFINITY) S = NAN;
+    }
+    const double log_s = log((double)S);
+    double term = 0.0;
+    if (en.id >= 0 && en.q != 0.0) {  // NaN goes on
+      const double log_p = ((double)xe - (double)m) * (double)a.inv_t - log_s;
+      term = en.q * (en.logq - log_p);
+    }
+    const double any = all_sum<W>(en.id >= 0 ? 1.0 : 0.0, red);
+    double loss = all_sum<W>(term, red);
+    const double sum_q = TAIL ? all_sum<W>(en.q, red) : 1.0;
+    if (lane == 0) {
+      // of the others: dx_j T = exp((x_j - from) / T) factor
+      float from = m;
+      double factor = exp(-log_s);
+      if (TAIL) {
+        double rest = 1.0 - sum_q;
+        if (rest < 0.0) rest = 0.0;
+        if (others.t == 0.f) {
+          if (rest != 0.0) loss = INFINITY;
+          factor = 0.0;
+        } else {
+          // by the others' own largest value: p_T may be too small for fp32
+          const double down = ((double)others.m - (double)m) * (double)a.inv_t - log_s;
+          if (rest != 0.0) loss += rest * (log(rest) - (down + log((double)others.t)));
+          from = others.m;
+          factor = exp(down) - rest / (double)others.t;
+        }
+      }
+      const bool masked = m == -INFINITY && S == 0.f;  // no token to put weight on
+      const bool none = any == 0.0;
+      a.loss[row] = none ? 0.f : masked ? INFINITY : (float)loss;
+      float *st = a.stats + 4 * row;
+      st[0] = none ? -INFINITY : m;  // -inf, 0: the gradient is zero
+      st[1] = none || masked ? 0.f : (float)log_s;
+      st[2] = from;
+      st[3] = (float)factor;
+    }
+  }
+}
+
+template <typename T, int W>
+__global__ __launch_bounds__(W < 256 ? 256 : W) void distill_grad_kernel(DistillArgs a) {
+  constexpr int R = W < 256 ? 256 / W : 1, N = kPiece<T>, P = kPieces;
+  __shared__ double red64[R][16];
+  __shared__ int ids[R][W < kMaxTeacher ? W : kMaxTeacher];
+  const int lane = threadIdx.x % W, sub = threadIdx.x / W;
+  const float c = a.inv_t * kLog2e;
+  for (int64_t row = (int64_t)blockIdx.x * R + sub; row < a.n; row += (int64_t)gridDim.x * R) {
+    const T *x = (const T *)a.x + row * a.V;
+    T *dx = (T *)a.dx + row * a.V;
+    const float *st = a.stats + 4 * row;
+    const float m = st[0], log_s = st[1], g = a.dloss[row] * a.inv_t;
+    const bool zero = g == 0.f || (m == -INFINITY && log_s == 0.f);
+    const Entry en = entry_of<W>(a, row, lane, ids[sub], red64[sub], false);
+    // read before anything is written: dx may be x
+    const float xe = en.id >= 0 ? load_f32(x, en.id) : 0.f;
+    row_barrier<W>();
+    const float from = st[2], A = g * st[3];
+    for (int64_t base = 0; base < a.V; base += W * P * N) {
+      u32x4 raw[P];
+      if (!zero) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int64_t i = base + (p * W + lane) * N;
+          raw[p] = load_piece(x + (i < a.V ? i : 0), (int)(a.V - i < N ? a.V - i : N));
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int64_t i = base + (p * W + lane) * N;
+        if (i >= a.V) continue;
+        float v[N];
+        if (zero) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[e] = 0.f;
+        } else {
+          unpack(raw[p], v);
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[e] = A * exp2_neg((from - v[e]) * c);
+        }
+        store_n<N>(dx + i, (int)(a.V - i < N ? a.V - i : N), v);
+      }
+    }
+    row_barrier<W>();
+    if (!zero && en.id >= 0) {
+      const double p = exp(((double)xe - (double)m) * (double)a.inv_t - (double)log_s);
+      store_f32(dx, en.id, g * (float)(p - en.q));
+    }
+  }
+}
+
+template <typename T, int W>
+static void start_distill(const DistillArgs &a, bool grad, hipStream_t s) {
+  constexpr int R = W < 256 ? 256 / W : 1, threads = W < 256 ? 256 : W;
+  const int64_t groups = ceil_div(a.n, R);
+  const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
+  if (grad) {
+    distill_grad_kernel<T, W><<<grid, threads, 0, s>>>(a);
+  } else if (a.tail) {
+    const int words = (int)ceil_div(a.V < kSegment ? a.V : kSegment, 32);
+    distill_kernel<T, W, true><<<grid, threads, (size_t)R * words * 4, s>>>(a, words);
+  } else {
+    distill_kernel<T, W, false><<<grid, threads, 0, s>>>(a, 0);
+  }
+}
+
+template <typename T>
+static hipError_t distill(const DistillArgs &a, bool grad, hipStream_t s) {
+  // at least as many threads as the teacher has entries
+  if (a.V <= 2048 && a.k <= 64)
+    start_distill<T, 64>(a, grad, s);
+  else if (a.V <= 16384)
+    start_distill<T, 256>(a, grad, s);
+  else
+    start_distill<T, 1024>(a, grad, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_distill(const DistillArgs &a, bool x_bf16, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  return x_bf16 ? distill<uint16_t>(a, false, s) : distill<float>(a, false, s);
+}
+hipError_t launch_distill_grad(const DistillArgs &a, bool x_bf16, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  return x_bf16 ? distill<uint16_t>(a, true, s) : distill<float>(a, true, s);
+}
+
+}  // namespace rvq

@@ -1,0 +1,139 @@
+"""Host-side checks of the calls for a model's head: sizes and bad arguments,
+which return a status before any HIP call (no GPU needed).  Addresses are
+fakes that nothing reads."""
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "residual_vector_quantization_rvq_amd", "librvq.so")
+
+
+@pytest.fixture(scope="module")
+def rvq():
+    if not os.path.exists(LIB):
+        import __graft_entry__
+        __graft_entry__._builder().build()
+    import residual_vector_quantization_rvq_amd as m
+    return m
+
+
+def _caller(fn, names, ok):
+    def call(**kw):
+        a = {**ok, **kw}
+        assert set(kw) <= set(names.split())
+        return fn(*[a[n] for n in names.split()])
+    return call
+
+
+def test_exports_the_head_calls(rvq):
+    names = set(rvq.exported_symbols())
+    for n in ("rvq_layer_norm", "rvq_layer_norm_backward", "rvq_quantize_f8", "rvq_matmul_f8", "rvq_token_logprobs",
+              "rvq_token_logprobs_backward", "rvq_distill_loss", "rvq_distill_loss_backward"):
+        assert n in names and n in rvq.__all__
+
+
+def test_layer_norm_arguments(rvq):
+    names = "x res xdt n d w b wdt eps sum y ydt scale mean rstd stream"
+    ok = dict(x=256, res=256, xdt=0, n=4, d=8, w=256, b=256, wdt=0, eps=1e-6, sum=512, y=256, ydt=0, scale=None,
+              mean=256, rstd=256, stream=None)
+    call = _caller(rvq.raw_library().rvq_layer_norm, names, ok)
+    for bad in (dict(n=-1), dict(d=0), dict(xdt=2), dict(xdt=7), dict(ydt=3), dict(wdt=2), dict(eps=0.0),
+                dict(eps=float("nan")), dict(eps=float("inf")), dict(x=None), dict(x=258), dict(res=257), dict(y=None),
+                dict(y=2), dict(w=2), dict(b=2), dict(sum=2), dict(sum=256), dict(mean=2), dict(rstd=2), dict(ydt=2),
+                dict(ydt=2, scale=2), dict(w=None, wdt=5)):
+        assert call(**bad) == 1, bad
+    assert call(n=(1 << 25) + 1) == 2 and call(d=(1 << 20) + 1) == 2
+    assert call(n=0, x=None, y=None) == 0
+    assert call(n=0, w=None, b=None, wdt=9) == 0
+
+
+def test_layer_norm_gradient_arguments(rvq):
+    names = "dy h dt n d mean rstd w wdt dsum dx dw db ws bytes stream"
+    ok = dict(dy=256, h=256, dt=1, n=4, d=8, mean=256, rstd=256, w=256, wdt=1, dsum=None, dx=256, dw=256, db=256, ws=256,
+              bytes=1 << 30, stream=None)
+    call = _caller(rvq.raw_library().rvq_layer_norm_backward, names, ok)
+    for bad in (dict(n=-1), dict(d=0), dict(dt=2), dict(wdt=5), dict(dy=None), dict(h=None), dict(mean=None),
+                dict(rstd=None), dict(dx=None), dict(dy=257), dict(dsum=257), dict(dw=2), dict(db=2), dict(ws=None),
+                dict(ws=128), dict(dw=None, ws=None)):
+        assert call(**bad) == 1, bad
+    assert call(bytes=16) == 3 and call(n=(1 << 25) + 1) == 2
+    assert call(n=0, dw=None, db=None, dy=None, h=None, mean=None, rstd=None, dx=None, ws=None) == 0
+    size = rvq.rvq_layer_norm_backward_workspace_size
+    assert size(0, 8) >= 64 and size(100000, 4096) % 256 == 0 and size(1, 1) > 0
+
+
+def test_quantiser_arguments(rvq):
+    names = "x dt rows cols layout tr q stride scale stream"
+    ok = dict(x=256, dt=0, rows=5, cols=7, layout=1, tr=0, q=256, stride=7, scale=256, stream=None)
+    call = _caller(rvq.raw_library().rvq_quantize_f8, names, ok)
+    for bad in (dict(rows=-1), dict(cols=-1), dict(dt=2), dict(layout=0), dict(layout=3), dict(x=None), dict(x=2),
+                dict(q=None), dict(scale=None), dict(scale=2), dict(stride=6), dict(stride=-7),
+                dict(tr=1, stride=4)):
+        assert call(**bad) == 1, bad
+    assert call(rows=(1 << 30) + 1) == 2 and call(rows=1 << 21, cols=1 << 20, stride=1 << 20) == 2
+    assert call(rows=0, x=None, q=None, scale=None) == 0 and call(cols=0, x=None, q=None, scale=None) == 0
+
+
+def test_product_arguments(rvq):
+    names = "a lda sa la b ldb sb lb m n k out odt stream"
+    ok = dict(a=256, lda=7, sa=256, la=1, b=256, ldb=7, sb=256, lb=2, m=3, n=4, k=7, out=256, odt=0, stream=None)
+    call = _caller(rvq.raw_library().rvq_matmul_f8, names, ok)
+    for bad in (dict(m=-1), dict(n=-1), dict(k=-1), dict(la=3), dict(lb=-1), dict(odt=2), dict(a=None), dict(b=None),
+                dict(sa=None), dict(sb=2), dict(out=None), dict(out=2), dict(odt=1, out=257), dict(lda=6), dict(ldb=6)):
+        assert call(**bad) == 1, bad
+    assert call(k=(1 << 30) + 1, lda=1 << 31, ldb=1 << 31) == 2 and call(m=1 << 21, n=1 << 20) == 2
+    assert call(m=0, a=None, out=None) == 0 and call(n=0, b=None, out=None) == 0
+
+
+def test_logprob_arguments(rvq):
+    names = "x dt n V ids T lp ent stats top tlp tid bad ws bytes stream"
+    ok = dict(x=256, dt=0, n=300, V=8, ids=256, T=1.0, lp=256, ent=None, stats=256, top=2, tlp=256, tid=256, bad=None,
+              ws=None, bytes=0, stream=None)
+    call = _caller(rvq.raw_library().rvq_token_logprobs, names, ok)
+    for bad in (dict(n=-1), dict(V=0), dict(dt=2), dict(T=0.0), dict(T=float("nan")), dict(T=1e5), dict(T=-1.0),
+                dict(x=None), dict(x=2), dict(ids=2), dict(lp=None), dict(ent=2), dict(stats=None), dict(top=-1),
+                dict(top=65), dict(tlp=None), dict(tid=None), dict(bad=2), dict(n=1, V=65536), dict(n=1, V=65536, ws=8, bytes=1 << 20)):
+        assert call(**bad) == 1, bad
+    assert call(n=1, V=65536, ws=256, bytes=8) == 3
+    assert call(n=(1 << 25) + 1) == 2 and call(V=(1 << 24) + 1) == 2
+    assert call(n=0, x=None, ids=None, lp=None, stats=None) == 0
+    size = rvq.rvq_token_logprobs_workspace_size
+    assert size(100000, 65536, 64) == 0 and size(0, 65536, 64) == 0
+    for n, V in ((1, 8192), (1, 65536), (3, 200000), (255, 1 << 24)):
+        for top in (0, 1, 20, 64):
+            assert size(n, V, top) % 256 == 0 and size(n, V, top) > 0
+    for kw in (dict(top=65), dict(top=-1)):
+        with pytest.raises(rvq.RVQError):
+            size(1, 8, **kw)
+
+
+def test_logprob_gradient_arguments(rvq):
+    names = "x dt n V ids T stats dlp ent dent dx stream"
+    ok = dict(x=4096, dt=0, n=3, V=8, ids=256, T=1.0, stats=256, dlp=256, ent=256, dent=256, dx=8192, stream=None)
+    call = _caller(rvq.raw_library().rvq_token_logprobs_backward, names, ok)
+    for bad in (dict(n=-1), dict(V=0), dict(dt=2), dict(T=0.0), dict(x=None), dict(stats=None), dict(dx=None), dict(dx=2),
+                dict(dlp=None, dent=None), dict(ids=None), dict(ent=None), dict(dlp=2), dict(dent=2),
+                dict(dx=4096 + 4), dict(dx=4096 - 4)):
+        assert call(**bad) == 1, bad
+    assert call(n=(1 << 25) + 1) == 2
+    assert call(n=0, x=None, stats=None, dx=None) == 0
+
+
+def test_distill_arguments(rvq):
+    names = "x dt n V ids t k tail T loss stats bad stream"
+    ok = dict(x=256, dt=0, n=3, V=8, ids=256, t=256, k=4, tail=0, T=1.0, loss=256, stats=256, bad=None, stream=None)
+    call = _caller(rvq.raw_library().rvq_distill_loss, names, ok)
+    for bad in (dict(n=-1), dict(V=0), dict(dt=2), dict(T=0.0), dict(x=None), dict(ids=None), dict(t=None), dict(t=2),
+                dict(k=0), dict(loss=None), dict(stats=None), dict(bad=2)):
+        assert call(**bad) == 1, bad
+    assert call(k=257) == 2 and call(V=(1 << 24) + 1) == 2
+    assert call(n=0, x=None, ids=None, t=None, loss=None, stats=None) == 0
+    names = "x dt n V ids t k tail T stats dloss dx stream"
+    ok = dict(x=4096, dt=1, n=3, V=8, ids=256, t=256, k=4, tail=1, T=1.0, stats=256, dloss=256, dx=4096, stream=None)
+    call = _caller(rvq.raw_library().rvq_distill_loss_backward, names, ok)
+    for bad in (dict(n=-1), dict(x=None), dict(stats=None), dict(dloss=None), dict(dloss=2), dict(dx=None), dict(dx=3),
+                dict(dx=4096 + 2), dict(k=0)):
+        assert call(**bad) == 1, bad
+    assert call(k=257) == 2
+    assert call(n=0, x=None, ids=None, t=None, stats=None, dloss=None, dx=None) == 0
