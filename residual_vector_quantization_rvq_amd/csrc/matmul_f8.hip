@@ -7,6 +7,8 @@
 // products; a group's error is up to 7 2^-13 of its largest product, and of random
 // values 3e-4 of the result's size).  e4m3 values are bf16 values, though, whose
 // products are exact and added in fp32: operands are widened to bf16 on the way.
+#include <type_traits>
+
 #include "head.h"
 
 namespace rvq {
@@ -40,6 +42,52 @@ __device__ __forceinline__ float scale_at(const ScaleView &s, int64_t row, int64
   return s.p[(row >> s.shift) * s.row_stride + kb * s.block_stride];
 }
 
+// 16 bytes a lane from base + off to lds + 16 * lane.  Written out because the compiler
+// would wait for every load of this kind before the next read of LDS; the waits are
+// the callers'.
+__device__ __forceinline__ void load_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
+  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ u32x4 read_lds(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>((size_t)at);
+}
+struct Frag {  // 32 e4m3 values of a row
+  u32x4 lo, hi;
+};
+// A fragment as the matrix instructions take it: as it is, or widened to bf16.
+template <bool EXACT>
+struct Operand;
+template <>
+struct Operand<false> {
+  i32x8 v;
+  Operand() = default;
+  __device__ __forceinline__ explicit Operand(const Frag &f)
+      : v{(int)f.lo[0], (int)f.lo[1], (int)f.lo[2], (int)f.lo[3], (int)f.hi[0], (int)f.hi[1], (int)f.hi[2], (int)f.hi[3]} {}
+};
+template <>
+struct Operand<true> {
+  bf16x8 v[4];
+  Operand() = default;
+  __device__ __forceinline__ explicit Operand(const Frag &f)
+      : v{widen(f.lo[0], f.lo[1]), widen(f.lo[2], f.lo[3]), widen(f.hi[0], f.hi[1]), widen(f.hi[2], f.hi[3])} {}
+};
+// NT products of one block: 16 rows of b each with 16 rows of a
+template <bool EXACT, int NT>
+__device__ __forceinline__ void product(const Operand<EXACT> (&b)[NT], const Operand<EXACT> &a, f32x4 (&p)[NT]) {
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].v[q], a.v[q], q ? p[j] : zero, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      p[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j].v, a.v, zero, 0, 0, 0, 0, 0, 0);
+  }
+}
+
 }  // namespace
 
 // One 16 x 16 tile a wave, straight from memory.
@@ -52,10 +100,10 @@ __global__ __launch_bounds__(kThreads) void matmul_f8_simple_kernel(MatmulArgs a
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   const int64_t blocks = ceil_div(a.k, kScaleBlock);
   for (int64_t kb = 0; kb < blocks; ++kb) {
-    const int64_t k = kb * kScaleBlock + part * 32;
+    const int64_t k = kb * kScaleBlock + part * 16;  // and 64 further, the order of the tiles
     const uint8_t *pa = a.a + am * a.a_stride + k, *pb = a.b + bn * a.b_stride + k;
-    const u32x4 a0 = load_bytes(pa, a.k - k), a1 = load_bytes(pa + 16, a.k - k - 16);
-    const u32x4 b0 = load_bytes(pb, a.k - k), b1 = load_bytes(pb + 16, a.k - k - 16);
+    const u32x4 a0 = load_bytes(pa, a.k - k), a1 = load_bytes(pa + 64, a.k - k - 64);
+    const u32x4 b0 = load_bytes(pb, a.k - k), b1 = load_bytes(pb + 64, a.k - k - 64);
     // rows of the result: b's (4 a lane), columns: a's (one a lane)
     f32x4 t = {0.f, 0.f, 0.f, 0.f};
     t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b0[0], b0[1]), widen(a0[0], a0[1]), t, 0, 0, 0);
@@ -82,8 +130,220 @@ __global__ __launch_bounds__(kThreads) void matmul_f8_simple_kernel(MatmulArgs a
   }
 }
 
+// ---- tiles ----
+// A workgroup of WM x WN waves makes a tile of BM x BN results, a wave MT x NT
+// products of 16 x 16.  Both operands' rows of one block (128 bytes each) are in LDS,
+// twice: while one stage is multiplied, the next is on its way from memory straight
+// into the other (16 bytes a lane, no registers).  A row's eight pieces are turned by
+// its place (piece p of row r at p ^ (r % 8)), so that the sixteen rows that a fragment
+// takes come from all banks.  A lane's fragment is pieces g and g + 4 of a row, g its
+// quarter of the wave: any order of k serves, the same for both operands.
+//
+// The first operand of a matrix instruction is b: then a lane's results are four
+// columns of one row of out, it needs one scale of a, and stores them side by side.
+template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS>
+__global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulArgs a, int tiles_m, int tiles_n) {
+  constexpr int kWaves = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16, kRows = BM + BN;
+  constexpr int GA = BM / 8 / kWaves, GB = BN / 8 / kWaves;  // a wave's loads: 8 rows each
+  constexpr int kStage = kRows * kScaleBlock;
+  static_assert(GA * 8 * kWaves == BM && GB * 8 * kWaves == BN, "whole loads");
+  __shared__ uint4 ring[2 * kStage / 16];
+  __shared__ float scales[2][kRows];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+
+  // each XCD a run of tiles, in groups of eight rows of tiles: those at work at one time share their operands in its L2
+  const int tiles = tiles_m * tiles_n, per = (tiles + 7) / 8;
+  const int t = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  if (t >= tiles || (int)(blockIdx.x / 8) >= per) return;
+  const int group = t / (8 * tiles_n), in_group = t - group * 8 * tiles_n;
+  const int rows_here = min(8, tiles_m - group * 8);
+  const int64_t m0 = (int64_t)(group * 8 + in_group % rows_here) * BM, n0 = (int64_t)(in_group / rows_here) * BN;
+
+  const uint32_t lds = (uint32_t)(size_t)((__attribute__((address_space(3))) uint4 *)ring);
+  const uint8_t *pa = a.a + m0 * a.a_stride, *pb = a.b + n0 * a.b_stride;
+  const int piece = (lane & 7) ^ (lane >> 3);  // of its row, that this lane loads
+  uint32_t off[GA + GB];                       // from pa or pb: below 2^31 (the launch sees to it)
+#pragma unroll
+  for (int i = 0; i < GA; ++i) {
+    const int64_t row = (i * kWaves + wave) * 8 + (lane >> 3), last = a.m - 1 - m0;
+    off[i] = (uint32_t)((row < last ? row : last) * a.a_stride) + piece * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < GB; ++i) {
+    const int64_t row = (i * kWaves + wave) * 8 + (lane >> 3), last = a.n - 1 - n0;
+    off[GA + i] = (uint32_t)((row < last ? row : last) * a.b_stride) + piece * 16;
+  }
+  const int k = (int)a.k, blocks = (k + kScaleBlock - 1) / kScaleBlock;
+  const auto load_stage = [&](int kb, int slot) {
+    // a piece behind the row's end is not read (any other is, and its place masked below)
+    const uint32_t ko = kb * kScaleBlock + piece * 16 < k ? (uint32_t)kb * kScaleBlock : (uint32_t)(-piece * 16);
+    const uint32_t to = lds + slot * kStage + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < GA; ++i) load_lds(pa, off[i] + ko, to + i * kWaves * 1024);
+#pragma unroll
+    for (int i = 0; i < GB; ++i) load_lds(pb, off[GA + i] + ko, to + BM * kScaleBlock + i * kWaves * 1024);
+  };
+  // the scales of the tile's rows: one a thread and block
+  constexpr int kPer = (kRows + kWaves * 64 - 1) / (kWaves * 64);
+  const float *ps[kPer];
+  int step[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int r = tid + i * kWaves * 64;
+    const bool of_a = r < BM;
+    const ScaleView &v = of_a ? a.sa : a.sb;
+    const int64_t row = of_a ? (m0 + r < a.m ? m0 + r : a.m - 1) : (n0 + r - BM < a.n ? n0 + r - BM : a.n - 1);
+    ps[i] = v.p + (row >> v.shift) * v.row_stride;
+    step[i] = v.block_stride;
+  }
+  float next[kPer];
+  const auto load_scales = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (tid + i * kWaves * 64 < kRows) next[i] = ps[i][(int64_t)kb * step[i]];
+  };
+  const auto store_scales = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (tid + i * kWaves * 64 < kRows) scales[slot][tid + i * kWaves * 64] = next[i];
+  };
+
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int r16 = lane & 15, g = lane >> 4;
+  const uint32_t frag = r16 * 128 + ((g ^ (lane & 7)) << 4);  // and ^ 64
+  const auto block = [&](auto tail, int kb, int slot) {
+    u32x4 mask[2];
+    if constexpr (tail) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int have = k - kb * kScaleBlock - (g + 4 * h) * 16 - 4 * j;
+          mask[h][j] = have >= 4 ? 0xffffffffu : have <= 0 ? 0u : (1u << (8 * have)) - 1;
+        }
+    }
+    // places of the lane's two pieces in the wave's first tiles; other tiles are at constant distances
+    const uint32_t a_lo = lds + slot * kStage + wm * MT * 16 * 128 + frag, a_hi = a_lo - frag + (frag ^ 64);
+    const uint32_t b_lo = lds + slot * kStage + (BM + wn * NT * 16) * 128 + frag, b_hi = b_lo - frag + (frag ^ 64);
+    const auto read = [&](uint32_t lo_at, uint32_t hi_at, int tile) {
+      u32x4 lo = read_lds(lo_at + tile * 2048), hi = read_lds(hi_at + tile * 2048);
+      if constexpr (tail) {
+        lo &= mask[0];
+        hi &= mask[1];
+      }
+      return Frag{lo, hi};
+    };
+    const float *sc = scales[slot];
+    f32x4 sb[NT];
+    if constexpr (B_BLOCKS) {
+      sb[0][0] = sc[BM + wn * NT * 16];  // the wave's columns lie in one block of 128
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sb[j][e] = sc[BM + (wn * NT + j) * 16 + g * 4 + e];
+    }
+    Operand<EXACT> fb[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fb[j] = Operand<EXACT>(read(b_lo, b_hi, j));
+    // Products of one row of tiles run while those of the row before are scaled and
+    // added, and the next row's fragment is on its way; no further ahead, for registers.
+    const auto read_a = [&](int i, Frag &f, float &sa) {
+      f = read(a_lo, a_hi, i);
+      sa = sc[(wm * MT + i) * 16 + r16];
+    };
+    Frag f[2];
+    float sa[2], s_of[2];
+    f32x4 p[2][NT];
+    read_a(0, f[0], sa[0]);
+#pragma unroll
+    for (int i = 0; i <= MT; ++i) {
+      if (i + 1 < MT) read_a(i + 1, f[(i + 1) & 1], sa[(i + 1) & 1]);
+      if (i < MT) {
+        const Operand<EXACT> fa(f[i & 1]);
+        s_of[i & 1] = B_BLOCKS ? sa[i & 1] * sb[0][0] : sa[i & 1];
+        product<EXACT, NT>(fb, fa, p[i & 1]);
+      }
+      if (i > 0) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i - 1][j][e] = __builtin_fmaf(p[(i - 1) & 1][j][e],
+                                              B_BLOCKS ? s_of[(i - 1) & 1] : s_of[(i - 1) & 1] * sb[j][e], acc[i - 1][j][e]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  load_scales(0);
+  load_stage(0, 0);
+  store_scales(0);
+  if (blocks > 1) load_scales(1);
+  const auto advance = [&](int kb) {
+    // this stage and the next scales are here, for all waves; the other stage has been read
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kb + 1 < blocks) {
+      store_scales((kb + 1) & 1);
+      if (kb + 2 < blocks) load_scales(kb + 2);
+      load_stage(kb + 1, (kb + 1) & 1);
+    }
+  };
+  const int whole = k / kScaleBlock;
+  for (int kb = 0; kb < whole; ++kb) {
+    advance(kb);
+    block(std::false_type{}, kb, kb & 1);
+  }
+  if (whole < blocks) {
+    advance(whole);
+    block(std::true_type{}, whole, whole & 1);
+  }
+
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = m0 + (wm * MT + i) * 16 + r16;
+    if (m >= a.m) continue;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int64_t n = n0 + (wn * NT + j) * 16 + g * 4;
+      const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      const int left = a.n - n < 4 ? (int)(a.n - n) : 4;
+      if (left <= 0) continue;
+      if (a.out_bf16)
+        store_n<4>((uint16_t *)a.out + m * a.n + n, left, v);
+      else
+        store_n<4>((float *)a.out + m * a.n + n, left, v);
+    }
+  }
+}
+
+template <int WM, int WN, int MT, int NT, bool EXACT>
+static hipError_t tiles(const MatmulArgs &a, hipStream_t s) {
+  const int tm = (int)ceil_div(a.m, WM * MT * 16), tn = (int)ceil_div(a.n, WN * NT * 16);
+  const dim3 grid((unsigned)(ceil_div((int64_t)tm * tn, 8) * 8));
+  if (a.sb.shift)
+    matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, true><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
+  else
+    matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, false><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
+  return hipGetLastError();
+}
+
 hipError_t launch_matmul_f8(const MatmulArgs &a, hipStream_t s) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
+  const auto even = [](const uint8_t *p, int64_t stride, int64_t k) {
+    return (uintptr_t)p % 16 == 0 && stride % 16 == 0 && stride >= round_up(k, 16) && stride < (1 << 22);
+  };
+  if (a.m > 32 && a.n > 32 && a.k > 0 && even(a.a, a.a_stride, a.k) && even(a.b, a.b_stride, a.k)) {
+    const bool large = ceil_div(a.m, 256) * ceil_div(a.n, 256) >= 128;
+    if (a.out_bf16) return large ? tiles<2, 4, 8, 4, false>(a, s) : tiles<2, 2, 4, 4, false>(a, s);
+    return large ? tiles<4, 2, 4, 4, true>(a, s) : tiles<2, 2, 4, 4, true>(a, s);
+  }
   const dim3 grid((unsigned)ceil_div(a.n, 64), (unsigned)ceil_div(a.m, 16));
   matmul_f8_simple_kernel<<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();

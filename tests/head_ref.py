@@ -80,11 +80,13 @@ def matmul(a, sa, b, sb):
     return torch.mm(x, y), torch.mm(x.abs(), y.abs())
 
 
-def matmul_bound(size, k):
+def matmul_bound(size, k, eight=False):
     """Products of e4m3 values are exact; 128 of them are added (each addition within
     two units, should the hardware cut off), a block's sum is multiplied by the product of two
-    scales (two roundings) and added to the others'."""
-    return (256 + -(-k // 128) + 8) * U * size
+    scales (two roundings) and added to the others'.  eight: the matrix cores' 8-bit products,
+    as bf16 results may use: eight at a time are added with what lies below 2^-13 of the
+    largest cut off, so each of the seven others loses less than that."""
+    return (256 + -(-k // 128) + 8) * U * size + (7 * 2.0 ** -13 * size if eight else 0.0)
 
 
 class Logits:

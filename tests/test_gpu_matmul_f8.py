@@ -109,7 +109,8 @@ def _check_product(rvq, a, sa, b, sb, odt, **kw):
     got = rvq.rvq_matmul_f8(a, sa, b, sb, out_dtype=odt, **kw)
     assert got.shape == (a.shape[0], b.shape[0]) and got.dtype == odt
     want, size = ref.matmul(a, sa, b, sb)
-    bound = ref.matmul_bound(size, a.shape[1]) + (ref.BF16_ROUND if odt == BF16 else ref.U) * want.abs()
+    bound = ref.matmul_bound(size, a.shape[1], odt == BF16)
+    bound = bound * (1 + (2 ** -8 if odt == BF16 else 0)) + (ref.BF16_ROUND if odt == BF16 else ref.U) * want.abs()
     learn_ref.close(got, want, bound, f"product {tuple(a.shape)} x {tuple(b.shape)}")
     return got
 
