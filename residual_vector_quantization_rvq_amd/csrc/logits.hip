@@ -142,6 +142,30 @@ __device__ __forceinline__ F all_sum(F v, F *red) {
   }
   return v;
 }
+// two at once; `red` holds 2 W / 64
+template <int W>
+__device__ __forceinline__ void all_sum2(float &a, float &b, float *red) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    a += __shfl_xor(a, off, 64);
+    b += __shfl_xor(b, off, 64);
+  }
+  if constexpr (W > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+      red[2 * (threadIdx.x >> 6)] = a;
+      red[2 * (threadIdx.x >> 6) + 1] = b;
+    }
+    __syncthreads();
+    a = red[0];
+    b = red[1];
+#pragma unroll
+    for (int w = 1; w < W / 64; ++w) {
+      a += red[2 * w];
+      b += red[2 * w + 1];
+    }
+  }
+}
 // the smallest
 template <int W>
 __device__ __forceinline__ int all_min(int v, int *red) {
@@ -170,8 +194,14 @@ __device__ __forceinline__ Sums join_threads(const Sums &s, float c, float *red)
     t *= f;
     if (r.m != r.m || r.m - s.m != r.m - s.m) t = NAN;  // infinite maxima
   }
-  r.t = all_sum<W>(t, red);
-  r.q = ENT ? all_sum<W>(q, red) : 0.f;
+  if (ENT) {
+    all_sum2<W>(t, q, red);
+  } else {
+    t = all_sum<W>(t, red);
+    q = 0.f;
+  }
+  r.t = t;
+  r.q = q;
   return r;
 }
 
@@ -209,64 +239,80 @@ __device__ __forceinline__ uint64_t order_key(float v, int at) {
   return ((uint64_t)order_bits(v) << 32) | (uint32_t)~at;
 }
 constexpr uint32_t kNoneBits = 0x007fffffu;  // order_bits(-inf): masked values are no alternatives
-constexpr int kMaxCand = 1024;
+constexpr int kMaxCand = 1024, kTopThreads = 256;
 static_assert(kMaxTop <= kMaxCand, "the join ranks at least one slice's keys");
 
+// A bound that at least `top` of the `total` numbers in v reach (0 if there are fewer):
+// the upper 16 bits of the top-th largest.  By one wave, a bit at a time.
+template <int PER>
+__device__ __forceinline__ uint32_t bound_of(const uint32_t (&v)[PER], int top) {
+  uint32_t bound = 0;
+  for (int bit = 31; bit >= 16; --bit) {
+    const uint32_t trial = bound | (1u << bit);
+    int reached = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) reached += __popcll(__ballot(v[i] >= trial));
+    if (reached >= top) bound = trial;
+  }
+  return bound;
+}
+// Ranks `found` different keys: the largest `top` of them to out in order, zeros behind them.
+__device__ __forceinline__ void rank_keys(const uint64_t *cand, int found, int top, uint64_t *out) {
+  for (int i = threadIdx.x; i < found; i += kTopThreads) {
+    const uint64_t key = cand[i];
+    int rank = 0;
+    for (int j = 0; j < found; ++j) rank += cand[j] > key;
+    if (rank < top) out[rank] = key;
+  }
+  for (int i = found + threadIdx.x; i < top; i += kTopThreads) out[i] = 0;
+}
+
 // The `top` largest of a row's columns [0, cols), larger first, to out[0 .. top - 1]
-// (0: none left).  tmax holds each thread's largest value as order_bits.
+// (0: none left).
 //
 // At least `top` threads have a largest value of the top-th largest of these or
-// more, so it bounds the answer from below: only threads that reach it look at their
-// values again, and the few that reach it are ranked by counting.  (Of that bound
-// the upper 16 bits are found, by one wave: for bf16 all there is.)  Should more
-// than kMaxCand values reach it (a row of mostly equal values), the largest is
+// more, so it bounds the answer from below: only the values of threads that reach it
+// are looked at again, all threads together, and the few that reach it are ranked by
+// counting.  (Of that bound the upper 16 bits are found: for bf16 all there is.)  Should
+// more than kMaxCand values reach it (a row of mostly equal values), the largest is
 // taken `top` times over the whole row.
-template <typename T, int W>
-__device__ void top_of_row(const T *row, int cols, int lane, float own_max, int top, uint32_t *tmax, uint64_t *cand,
-                           int *count, uint64_t *out) {
-  constexpr int N = kPiece<T>;
+template <typename T>
+__device__ void top_of_row(const T *row, int cols, float own_max, int top, uint32_t *tmax, uint64_t *cand, int *count,
+                           uint64_t *out) {
+  constexpr int N = kPiece<T>, W = kTopThreads;
+  const int lane = threadIdx.x;
   const uint32_t own = order_bits(own_max);
   __syncthreads();
   tmax[lane] = own;
-  if (lane == 0) count[0] = 0;
+  if (lane == 0) count[0] = count[2] = 0;
   __syncthreads();
   if (lane < 64) {
-    uint32_t mine[W / 64], bound = 0;
+    uint32_t mine[W / 64];
 #pragma unroll
     for (int i = 0; i < W / 64; ++i) mine[i] = tmax[i * 64 + lane];
-    for (int bit = 31; bit >= 16; --bit) {
-      const uint32_t trial = bound | (1u << bit);
-      int reached = 0;
-#pragma unroll
-      for (int i = 0; i < W / 64; ++i) reached += __popcll(__ballot(mine[i] >= trial));
-      if (reached >= top) bound = trial;
-    }
-    if (lane == 0) count[1] = (int)bound;
+    const uint32_t bound = bound_of(mine, top);
+    if (lane == 0) count[1] = (int)max(bound, kNoneBits + 1);
   }
   __syncthreads();
-  const uint32_t bound = max((uint32_t)count[1], kNoneBits + 1);
-  if (own >= bound) {
-    for (int i = lane * N; i < cols; i += W * N) {
-      float v[N];
-      load_values(row, i, cols - i, v);
+  const uint32_t bound = (uint32_t)count[1];
+  if (own >= bound) tmax[atomicAdd(count + 2, 1)] = lane;  // nobody's tmax is read from here on
+  __syncthreads();
+  const int holders = count[2], each = (cols + W * N - 1) / (W * N);
+  for (int i = lane; i < holders * each; i += W) {
+    const int j = i / holders, at = (j * W + (int)tmax[i - j * holders]) * N;
+    float v[N];
+    load_values(row, at, cols - at, v);
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (order_bits(v[e]) >= bound) {
-          const int at = atomicAdd(count, 1);  // the order does not matter: ranked below
-          if (at < kMaxCand) cand[at] = order_key(v[e], i + e);
-        }
-    }
+    for (int e = 0; e < N; ++e)
+      if (order_bits(v[e]) >= bound) {
+        const int place = atomicAdd(count, 1);  // the order does not matter: ranked below
+        if (place < kMaxCand) cand[place] = order_key(v[e], at + e);
+      }
   }
   __syncthreads();
   const int found = count[0];
   if (found <= kMaxCand) {
-    for (int i = lane; i < found; i += W) {
-      const uint64_t key = cand[i];
-      int rank = 0;
-      for (int j = 0; j < found; ++j) rank += cand[j] > key;
-      if (rank < top) out[rank] = key;
-    }
-    for (int i = found + lane; i < top; i += W) out[i] = 0;
+    rank_keys(cand, found, top, out);
     __syncthreads();
     return;
   }
@@ -295,7 +341,7 @@ __device__ void top_of_row(const T *row, int cols, int lane, float own_max, int 
 #pragma unroll
     for (int w = 1; w < W / 64; ++w) best = cand[w] > best ? cand[w] : best;
     if (lane == 0) out[r] = best;
-    last = best == 0 ? 0 : best;
+    last = best;
   }
   __syncthreads();
 }
@@ -340,13 +386,13 @@ __host__ __device__ constexpr int part_floats(int top) { return 4 + 2 * top; }
 }  // namespace
 
 template <typename T, int W, bool ENT, bool TOP>
-__global__ __launch_bounds__(W < 256 ? 256 : W) void logprob_kernel(LogprobArgs a, LogprobPlan plan) {
-  constexpr int R = W < 256 ? 256 / W : 1;
-  __shared__ float red[W / 64 > 4 ? W / 64 : 4];
-  __shared__ uint32_t tmax[TOP ? W : 1];
+__global__ __launch_bounds__(256, 6) void logprob_kernel(LogprobArgs a, LogprobPlan plan) {
+  constexpr int R = 256 / W;
+  __shared__ float red[2 * 256 / 64];
+  __shared__ uint32_t tmax[TOP ? kTopThreads : 1];
   __shared__ uint64_t cand[TOP ? kMaxCand : 1];
   __shared__ uint64_t best[TOP ? kMaxTop : 1];
-  __shared__ int count[2];
+  __shared__ int count[3];
   const int lane = threadIdx.x % W;
   const float c = a.inv_t * kLog2e;
   const int64_t jobs = a.n * plan.slices;
@@ -360,7 +406,7 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void logprob_kernel(LogprobArgs 
     stream_row<T, W, ENT, false>(x, cols, lane, c, nullptr, s);
     const Sums all = join_threads<W, ENT>(s, c, red);
     const float rest = rest_of<T, W>(x, cols, lane, c, s, all, red);
-    if constexpr (TOP) top_of_row<T, W>(x, cols, lane, s.m, a.top, tmax, cand, count, best);
+    if constexpr (TOP) top_of_row<T>(x, cols, s.m, a.top, tmax, cand, count, best);
     if (plan.slices == 1) {
       if (lane == 0) finish_row<T>(a, row, all.m, rest, all.q);
       if constexpr (TOP) {
@@ -380,14 +426,22 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void logprob_kernel(LogprobArgs 
   }
 }
 
-// A row out of its slices: one wave joins their sums, the workgroup ranks their keys.
+// A row out of its slices: one wave joins their sums, another bounds their keys, and
+// the workgroup ranks those that reach the bound.
 template <typename T>
-__global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a, LogprobPlan plan) {
-  __shared__ uint64_t cand[kMaxCand];
+__global__ __launch_bounds__(kTopThreads) void logprob_join_kernel(LogprobArgs a, LogprobPlan plan) {
+  __shared__ uint64_t cand[kMaxCand], kept[kMaxCand], best[kMaxTop];
   __shared__ float got[2];
+  __shared__ int count[2];
   const int64_t row = blockIdx.x;
   const float *part = a.part + row * plan.slices * part_floats(a.top);
   const float c = a.inv_t * kLog2e;
+  const int total = plan.slices * a.top;
+  for (int i = threadIdx.x; i < kMaxCand; i += kTopThreads) {
+    const int slice = i < total ? i / a.top : 0;
+    cand[i] = i < total ? ((const uint64_t *)(part + slice * part_floats(a.top) + 4))[i - slice * a.top] : 0;
+  }
+  if (threadIdx.x == 0) count[0] = 0;
   if (threadIdx.x < 64) {
     const int i = threadIdx.x;
     const bool in = i < plan.slices;
@@ -407,8 +461,7 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a, Logpro
       r = 0.f;
       qq = 0.f;
     }
-    r = all_sum<64>(r, (float *)nullptr);
-    qq = all_sum<64>(qq, (float *)nullptr);
+    all_sum2<64>(r, qq, nullptr);
     if (top == -INFINITY && !(r != r)) r = -1.f;
     if (i == 0) {
       finish_row<T>(a, row, top, r, qq);
@@ -417,20 +470,22 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a, Logpro
     }
   }
   if (a.top == 0) return;
-  const int total = plan.slices * a.top;
-  for (int i = threadIdx.x; i < total; i += 256)
-    cand[i] = ((const uint64_t *)(part + (i / a.top) * part_floats(a.top) + 4))[i % a.top];
   __syncthreads();
-  int some = 0;
-  for (int i = threadIdx.x; i < total; i += 256) {
-    const uint64_t key = cand[i];
-    if (key == 0) continue;
-    int rank = 0;
-    for (int j = 0; j < total; ++j) rank += cand[j] > key;
-    if (rank < a.top) finish_top(a, row, rank, key, got[0], got[1]);
+  if (threadIdx.x >= 64 && threadIdx.x < 128) {
+    uint32_t mine[kMaxCand / 64];
+#pragma unroll
+    for (int i = 0; i < kMaxCand / 64; ++i) mine[i] = (uint32_t)(cand[i * 64 + threadIdx.x - 64] >> 32);
+    const uint32_t bound = bound_of(mine, a.top);
+    if (threadIdx.x == 64) count[1] = (int)max(bound, kNoneBits + 1);
   }
-  for (int i = 0; i < total; ++i) some += cand[i] != 0;
-  for (int i = some + threadIdx.x; i < a.top; i += 256) finish_top(a, row, i, 0, got[0], got[1]);
+  __syncthreads();
+  const uint32_t bound = (uint32_t)count[1];
+  for (int i = threadIdx.x; i < total; i += kTopThreads)
+    if ((uint32_t)(cand[i] >> 32) >= bound) kept[atomicAdd(count, 1)] = cand[i];
+  __syncthreads();
+  rank_keys(kept, count[0], a.top, best);
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.top; i += kTopThreads) finish_top(a, row, i, best[i], got[0], got[1]);
 }
 
 LogprobPlan logprob_plan(int64_t n, int V, int top) {
@@ -451,33 +506,24 @@ size_t logprob_part_floats(int64_t n, const LogprobPlan &p, int top) {
 
 template <typename T, int W, bool TOP>
 static void start_logprobs(const LogprobArgs &a, const LogprobPlan &plan, hipStream_t s) {
-  constexpr int R = W < 256 ? 256 / W : 1;
-  const int64_t groups = ceil_div(a.n * plan.slices, R);
+  const int64_t groups = ceil_div(a.n * plan.slices, 256 / W);
   const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
-  const int threads = W < 256 ? 256 : W;
   if (a.entropy)
-    logprob_kernel<T, W, true, TOP><<<grid, threads, 0, s>>>(a, plan);
+    logprob_kernel<T, W, true, TOP><<<grid, 256, 0, s>>>(a, plan);
   else
-    logprob_kernel<T, W, false, TOP><<<grid, threads, 0, s>>>(a, plan);
+    logprob_kernel<T, W, false, TOP><<<grid, 256, 0, s>>>(a, plan);
 }
 
 template <typename T>
 static hipError_t logprobs(const LogprobArgs &a, hipStream_t s) {
   const LogprobPlan plan = logprob_plan(a.n, a.V, a.top);
-  const int64_t cols = plan.slice;
-  if (a.top > 0) {
-    if (cols <= 16384)
-      start_logprobs<T, 256, true>(a, plan, s);
-    else
-      start_logprobs<T, 1024, true>(a, plan, s);
-  } else if (cols <= 2048 && plan.slices == 1) {
+  if (a.top > 0)
+    start_logprobs<T, 256, true>(a, plan, s);
+  else if (a.V <= 2048)
     start_logprobs<T, 64, false>(a, plan, s);
-  } else if (cols <= 16384) {
+  else
     start_logprobs<T, 256, false>(a, plan, s);
-  } else {
-    start_logprobs<T, 1024, false>(a, plan, s);
-  }
-  if (plan.slices > 1) logprob_join_kernel<T><<<dim3((unsigned)a.n), 256, 0, s>>>(a, plan);
+  if (plan.slices > 1) logprob_join_kernel<T><<<dim3((unsigned)a.n), kTopThreads, 0, s>>>(a, plan);
   return hipGetLastError();
 }
 
@@ -486,13 +532,47 @@ hipError_t launch_logprobs(const LogprobArgs &a, bool x_bf16, hipStream_t s) {
   return x_bf16 ? logprobs<uint16_t>(a, s) : logprobs<float>(a, s);
 }
 
+namespace {
+
+template <typename T, int W>
+__device__ __forceinline__ void zero_row(T *dx, int cols, int lane) {
+  constexpr int N = kPiece<T>;
+  const float v[N] = {};
+  for (int i = lane * N; i < cols; i += W * N) store_n<N>(dx + i, cols - i, v);
+}
+// dx = f(x) for a lane's pieces of a row; dx may be x
+template <typename T, int W, typename F>
+__device__ __forceinline__ void map_row(const T *x, T *dx, int cols, int lane, F f) {
+  constexpr int N = kPiece<T>, P = kPieces;
+  for (int base = lane * N; base < cols; base += W * P * N) {
+    u32x4 raw[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int i = base + p * W * N;
+      raw[p] = load_piece(x + (i < cols ? i : 0), cols - i);
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int i = base + p * W * N;
+      if (i >= cols) break;
+      float v[N];
+      unpack(raw[p], v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = f(v[e]);
+      store_n<N>(dx + i, cols - i, v);
+    }
+  }
+}
+
+}  // namespace
+
 // ---- the gradient of log probabilities and entropies ----
 //   dx_j = (g ([j = id] - p_j) - gH p_j (log p_j + H)) / T
 // With e_j = exp(-d_j) = S p_j this is e_j (A + B d_j), A = -(g + gH (H - log S)) / (S T),
 // B = gH / (S T); the given token's own element uses 1 - p = -expm1(log p).
 template <typename T, int W>
-__global__ __launch_bounds__(W < 256 ? 256 : W) void logprob_grad_kernel(LogprobGradArgs a, int slices, int64_t slice) {
-  constexpr int R = W < 256 ? 256 / W : 1, N = kPiece<T>, P = kPieces;
+__global__ __launch_bounds__(256, 6) void logprob_grad_kernel(LogprobGradArgs a, int slices, int64_t slice) {
+  constexpr int R = 256 / W, N = kPiece<T>;
   const int lane = threadIdx.x % W;
   const float c = a.inv_t * kLog2e;
   const int64_t jobs = a.n * slices;
@@ -508,45 +588,24 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void logprob_grad_kernel(Logprob
     const float g = a.dlogprob && id >= 0 ? a.dlogprob[row] : 0.f;
     const float gh = a.dentropy ? a.dentropy[row] : 0.f;
     // no weight, or no token to put it on: zeros, whatever the logits are
-    const bool zero = (g == 0.f && gh == 0.f) || (m == -INFINITY && !(log_s != log_s));
+    if ((g == 0.f && gh == 0.f) || (m == -INFINITY && !(log_s != log_s))) {
+      zero_row<T, W>(dx, cols, lane);
+      continue;
+    }
     const float h = gh != 0.f ? a.entropy[row] : 0.f;
     const float k = expf(-log_s) * a.inv_t;
     const float A = -(g + gh * (h - log_s)) * k, B = gh * kLn2 * k;
-    const int64_t at_id = id >= 0 ? id - c0 : -1;
-    for (int64_t base = 0; base < cols; base += W * P * N) {
-      u32x4 raw[P];
-      if (!zero) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const int64_t i = base + (p * W + lane) * N;
-          raw[p] = load_piece(x + (i < cols ? i : 0), (int)(cols - i < N ? cols - i : N));
-        }
-      }
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int64_t i = base + (p * W + lane) * N;
-        if (i >= cols) continue;
-        float v[N];
-        if (zero) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) v[e] = 0.f;
-        } else {
-          unpack(raw[p], v);
-          const bool has = at_id >= i && at_id < i + N;
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const float x_e = v[e];
-            const float d = fminf((m - x_e) * c, kFar);
-            v[e] = exp2_neg(d) * (A + B * d);
-            if (has && i + e == at_id) {
-              const float lp = log_prob(x_e, m, log_s, a.inv_t);
-              const float p_id = expf(lp);
-              v[e] = (-g * expm1f(lp) - (p_id > 0.f ? gh * p_id * (lp + h) : 0.f)) * a.inv_t;
-            }
-          }
-        }
-        store_n<N>(dx + i, (int)(cols - i < N ? cols - i : N), v);  // may be x: this lane's own piece
-      }
+    // the given token's own element is this lane's to write again; it is read before (dx may be x)
+    const int64_t at_id = id - c0;
+    const bool mine = id >= 0 && at_id >= 0 && at_id < cols && (int)(at_id / N) % W == lane;
+    const float x_id = mine ? load_f32(x, at_id) : 0.f;
+    map_row<T, W>(x, dx, cols, lane, [&](float v) {
+      const float d = fminf((m - v) * c, kFar);
+      return exp2_neg(d) * (A + B * d);
+    });
+    if (mine) {
+      const float lp = log_prob(x_id, m, log_s, a.inv_t), p = expf(lp);
+      store_f32(dx, at_id, (-g * expm1f(lp) - (p > 0.f ? gh * p * (lp + h) : 0.f)) * a.inv_t);
     }
   }
 }
@@ -652,11 +711,11 @@ __device__ __forceinline__ void row_barrier() {
 }  // namespace
 
 template <typename T, int W, bool TAIL>
-__global__ __launch_bounds__(W < 256 ? 256 : W) void distill_kernel(DistillArgs a, int words) {
-  constexpr int R = W < 256 ? 256 / W : 1;
+__global__ __launch_bounds__(256, 6) void distill_kernel(DistillArgs a, int words) {
+  constexpr int R = 256 / W;
   extern __shared__ uint32_t maps[];  // [R][words]
   __shared__ double red64[R][16];
-  __shared__ int ids[R][W < kMaxTeacher ? W : kMaxTeacher];
+  __shared__ int ids[R][W];
   const int lane = threadIdx.x % W, sub = threadIdx.x / W;
   uint32_t *map = maps + sub * words;
   double *red = red64[sub];
@@ -728,10 +787,10 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void distill_kernel(DistillArgs 
 }
 
 template <typename T, int W>
-__global__ __launch_bounds__(W < 256 ? 256 : W) void distill_grad_kernel(DistillArgs a) {
-  constexpr int R = W < 256 ? 256 / W : 1, N = kPiece<T>, P = kPieces;
+__global__ __launch_bounds__(256, 6) void distill_grad_kernel(DistillArgs a) {
+  constexpr int R = 256 / W;
   __shared__ double red64[R][16];
-  __shared__ int ids[R][W < kMaxTeacher ? W : kMaxTeacher];
+  __shared__ int ids[R][W];
   const int lane = threadIdx.x % W, sub = threadIdx.x / W;
   const float c = a.inv_t * kLog2e;
   for (int64_t row = (int64_t)blockIdx.x * R + sub; row < a.n; row += (int64_t)gridDim.x * R) {
@@ -739,39 +798,18 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void distill_grad_kernel(Distill
     T *dx = (T *)a.dx + row * a.V;
     const float *st = a.stats + 4 * row;
     const float m = st[0], log_s = st[1], g = a.dloss[row] * a.inv_t;
-    const bool zero = g == 0.f || (m == -INFINITY && log_s == 0.f);
+    if (g == 0.f || (m == -INFINITY && log_s == 0.f)) {  // the same for the row's threads
+      zero_row<T, W>(dx, a.V, lane);
+      continue;
+    }
     const Entry en = entry_of<W>(a, row, lane, ids[sub], red64[sub], false);
     // read before anything is written: dx may be x
     const float xe = en.id >= 0 ? load_f32(x, en.id) : 0.f;
     row_barrier<W>();
     const float from = st[2], A = g * st[3];
-    for (int64_t base = 0; base < a.V; base += W * P * N) {
-      u32x4 raw[P];
-      if (!zero) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const int64_t i = base + (p * W + lane) * N;
-          raw[p] = load_piece(x + (i < a.V ? i : 0), (int)(a.V - i < N ? a.V - i : N));
-        }
-      }
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int64_t i = base + (p * W + lane) * N;
-        if (i >= a.V) continue;
-        float v[N];
-        if (zero) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) v[e] = 0.f;
-        } else {
-          unpack(raw[p], v);
-#pragma unroll
-          for (int e = 0; e < N; ++e) v[e] = A * exp2_neg((from - v[e]) * c);
-        }
-        store_n<N>(dx + i, (int)(a.V - i < N ? a.V - i : N), v);
-      }
-    }
+    map_row<T, W>(x, dx, a.V, lane, [&](float v) { return A * exp2_neg((from - v) * c); });
     row_barrier<W>();
-    if (!zero && en.id >= 0) {
+    if (en.id >= 0) {
       const double p = exp(((double)xe - (double)m) * (double)a.inv_t - (double)log_s);
       store_f32(dx, en.id, g * (float)(p - en.q));
     }
@@ -780,28 +818,27 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void distill_grad_kernel(Distill
 
 template <typename T, int W>
 static void start_distill(const DistillArgs &a, bool grad, hipStream_t s) {
-  constexpr int R = W < 256 ? 256 / W : 1, threads = W < 256 ? 256 : W;
+  constexpr int R = 256 / W;
   const int64_t groups = ceil_div(a.n, R);
   const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
   if (grad) {
-    distill_grad_kernel<T, W><<<grid, threads, 0, s>>>(a);
+    distill_grad_kernel<T, W><<<grid, 256, 0, s>>>(a);
   } else if (a.tail) {
     const int words = (int)ceil_div(a.V < kSegment ? a.V : kSegment, 32);
-    distill_kernel<T, W, true><<<grid, threads, (size_t)R * words * 4, s>>>(a, words);
+    distill_kernel<T, W, true><<<grid, 256, (size_t)R * words * 4, s>>>(a, words);
   } else {
-    distill_kernel<T, W, false><<<grid, threads, 0, s>>>(a, 0);
+    distill_kernel<T, W, false><<<grid, 256, 0, s>>>(a, 0);
   }
 }
 
 template <typename T>
 static hipError_t distill(const DistillArgs &a, bool grad, hipStream_t s) {
   // at least as many threads as the teacher has entries
+  static_assert(kMaxTeacher <= 256, "a thread each");
   if (a.V <= 2048 && a.k <= 64)
     start_distill<T, 64>(a, grad, s);
-  else if (a.V <= 16384)
-    start_distill<T, 256>(a, grad, s);
   else
-    start_distill<T, 1024>(a, grad, s);
+    start_distill<T, 256>(a, grad, s);
   return hipGetLastError();
 }
 
