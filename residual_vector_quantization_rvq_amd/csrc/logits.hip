@@ -711,7 +711,7 @@ __device__ __forceinline__ void row_barrier() {
 }  // namespace
 
 template <typename T, int W, bool TAIL>
-__global__ __launch_bounds__(256, 6) void distill_kernel(DistillArgs a, int words) {
+__global__ __launch_bounds__(256, 4) void distill_kernel(DistillArgs a, int words) {
   constexpr int R = 256 / W;
   extern __shared__ uint32_t maps[];  // [R][words]
   __shared__ double red64[R][16];
@@ -787,7 +787,7 @@ __global__ __launch_bounds__(256, 6) void distill_kernel(DistillArgs a, int word
 }
 
 template <typename T, int W>
-__global__ __launch_bounds__(256, 6) void distill_grad_kernel(DistillArgs a) {
+__global__ __launch_bounds__(256, 4) void distill_grad_kernel(DistillArgs a) {
   constexpr int R = 256 / W;
   __shared__ double red64[R][16];
   __shared__ int ids[R][W];
