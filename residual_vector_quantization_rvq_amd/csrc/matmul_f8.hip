@@ -90,44 +90,119 @@ __device__ __forceinline__ void product(const Operand<EXACT> (&b)[NT], const Ope
 
 }  // namespace
 
-// One 16 x 16 tile a wave, straight from memory.
-__global__ __launch_bounds__(kThreads) void matmul_f8_simple_kernel(MatmulArgs a) {
+// ---- few rows on one side ----
+// `w` is the operand with many rows, `s` the one with few: a workgroup takes 16 rows
+// of w and 16 MT of s, its KW waves the blocks of k in turn, straight from memory to
+// registers (each byte of w is read once).  The waves' sums are added in order.
+// Bound by the bytes of w: four blocks of a wave are on their way at once.
+template <int MT, int KW, bool SWAP>
+__global__ __launch_bounds__(KW * 64) void matmul_f8_few_kernel(MatmulArgs a) {
+  constexpr int U = 4;
+  __shared__ f32x4 sums[KW][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m0 = (int64_t)blockIdx.y * 16, n0 = ((int64_t)blockIdx.x * 4 + wave) * 16;
-  if (n0 >= a.n) return;
-  const int r = lane & 15, part = lane >> 4;
-  const int64_t am = m0 + r < a.m ? m0 + r : a.m - 1, bn = n0 + r < a.n ? n0 + r : a.n - 1;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  const int64_t blocks = ceil_div(a.k, kScaleBlock);
-  for (int64_t kb = 0; kb < blocks; ++kb) {
-    const int64_t k = kb * kScaleBlock + part * 16;  // and 64 further, the order of the tiles
-    const uint8_t *pa = a.a + am * a.a_stride + k, *pb = a.b + bn * a.b_stride + k;
-    const u32x4 a0 = load_bytes(pa, a.k - k), a1 = load_bytes(pa + 64, a.k - k - 64);
-    const u32x4 b0 = load_bytes(pb, a.k - k), b1 = load_bytes(pb + 64, a.k - k - 64);
-    // rows of the result: b's (4 a lane), columns: a's (one a lane)
-    f32x4 t = {0.f, 0.f, 0.f, 0.f};
-    t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b0[0], b0[1]), widen(a0[0], a0[1]), t, 0, 0, 0);
-    t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b0[2], b0[3]), widen(a0[2], a0[3]), t, 0, 0, 0);
-    t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b1[0], b1[1]), widen(a1[0], a1[1]), t, 0, 0, 0);
-    t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b1[2], b1[3]), widen(a1[2], a1[3]), t, 0, 0, 0);
-    const float sa = scale_at(a.sa, am, kb);
+  const int r16 = lane & 15, g = lane >> 4;
+  const uint8_t *w = SWAP ? a.a : a.b, *s = SWAP ? a.b : a.a;
+  const int64_t w_stride = SWAP ? a.a_stride : a.b_stride, s_stride = SWAP ? a.b_stride : a.a_stride;
+  const ScaleView vw = SWAP ? a.sa : a.sb, vs = SWAP ? a.sb : a.sa;
+  const int64_t w_rows = SWAP ? a.m : a.n, s_rows = SWAP ? a.n : a.m;
+  const int64_t w0 = (int64_t)blockIdx.x * 16, s0 = (int64_t)blockIdx.y * 16 * MT;
+  const int64_t wr = w0 + r16 < w_rows ? w0 + r16 : w_rows - 1;
+  const uint8_t *pw = w + wr * w_stride + g * 16, *ps[MT];
+  const float *qs[MT], *qw[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t n = n0 + part * 4 + i;
-      acc[i] += t[i] * (sa * scale_at(a.sb, n < a.n ? n : a.n - 1, kb));
+  for (int i = 0; i < MT; ++i) {
+    const int64_t row = s0 + i * 16 + r16 < s_rows ? s0 + i * 16 + r16 : s_rows - 1;
+    ps[i] = s + row * s_stride + g * 16;
+    qs[i] = vs.p + (row >> vs.shift) * vs.row_stride;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t row = w0 + g * 4 + e < w_rows ? w0 + g * 4 + e : w_rows - 1;
+    qw[e] = vw.p + (row >> vw.shift) * vw.row_stride;
+  }
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t whole = a.k / kScaleBlock, blocks = ceil_div(a.k, kScaleBlock);
+  const auto add = [&](const Frag &fw, const Frag (&fs)[MT], const float (&sw)[4], const float (&ss)[MT]) {
+    const Operand<true> ow[1] = {Operand<true>(fw)};
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      f32x4 p[1];
+      product<true, 1>(ow, Operand<true>(fs[i]), p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(p[0][e], ss[i] * sw[e], acc[i][e]);
+    }
+  };
+  const auto scales = [&](int64_t kb, float (&sw)[4], float (&ss)[MT]) {
+    sw[0] = qw[0][kb * vw.block_stride];
+#pragma unroll
+    for (int e = 1; e < 4; ++e) sw[e] = vw.shift ? sw[0] : qw[e][kb * vw.block_stride];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ss[i] = qs[i][kb * vs.block_stride];
+  };
+  int64_t kb = wave;
+  for (; kb + (U - 1) * KW < whole; kb += U * KW) {
+    Frag fw[U], fs[U][MT];
+    float sw[U][4], ss[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = (kb + u * KW) * kScaleBlock;
+      fw[u] = {load_bytes(pw + k, 16), load_bytes(pw + k + 64, 16)};
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = (kb + u * KW) * kScaleBlock;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fs[u][i] = {load_bytes(ps[i] + k, 16), load_bytes(ps[i] + k + 64, 16)};
+      scales(kb + u * KW, sw[u], ss[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) add(fw[u], fs[u], sw[u], ss[u]);
+  }
+  for (; kb < blocks; kb += KW) {
+    const int64_t k = kb * kScaleBlock, left = a.k - k - g * 16;
+    Frag fs[MT];
+    float sw[4], ss[MT];
+    const Frag fw = {load_bytes(pw + k, left), load_bytes(pw + k + 64, left - 64)};
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fs[i] = {load_bytes(ps[i] + k, left), load_bytes(ps[i] + k + 64, left - 64)};
+    scales(kb, sw, ss);
+    add(fw, fs, sw, ss);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) sums[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (int j = threadIdx.x; j < MT * 64; j += KW * 64) {
+    const int i = j >> 6, l = j & 63;
+    f32x4 sum = sums[0][i][l];
+#pragma unroll
+    for (int v = 1; v < KW; ++v) sum += sums[v][i][l];
+    const int64_t sr = s0 + i * 16 + (l & 15), wc = w0 + (l >> 4) * 4;
+    if (sr >= s_rows) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (wc + e >= w_rows) break;
+      const int64_t at = SWAP ? (wc + e) * a.n + sr : sr * a.n + wc + e;
+      if (a.out_bf16)
+        ((uint16_t *)a.out)[at] = f32_to_bf16_bits(sum[e]);
+      else
+        ((float *)a.out)[at] = sum[e];
     }
   }
-  if (m0 + r >= a.m) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t n = n0 + part * 4 + i;
-    if (n >= a.n) continue;
-    const int64_t at = (m0 + r) * a.n + n;
-    if (a.out_bf16)
-      ((uint16_t *)a.out)[at] = f32_to_bf16_bits(acc[i]);
-    else
-      ((float *)a.out)[at] = acc[i];
-  }
+}
+
+template <int MT, int KW, bool SWAP>
+static hipError_t few(const MatmulArgs &a, hipStream_t s) {
+  const int64_t w_rows = SWAP ? a.m : a.n, s_rows = SWAP ? a.n : a.m;
+  const dim3 grid((unsigned)ceil_div(w_rows, 16), (unsigned)ceil_div(s_rows, 16 * MT));
+  matmul_f8_few_kernel<MT, KW, SWAP><<<grid, KW * 64, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <int MT, bool SWAP>
+static hipError_t few(const MatmulArgs &a, hipStream_t s) {
+  // few workgroups: more waves each
+  return ceil_div(SWAP ? a.m : a.n, 16) >= 1024 ? few<MT, 4, SWAP>(a, s) : few<MT, 16, SWAP>(a, s);
 }
 
 // ---- tiles ----
@@ -139,9 +214,11 @@ __global__ __launch_bounds__(kThreads) void matmul_f8_simple_kernel(MatmulArgs a
 // takes come from all banks.  A lane's fragment is pieces g and g + 4 of a row, g its
 // quarter of the wave: any order of k serves, the same for both operands.
 //
+// Rows at any address or distance (not DIRECT) go through registers into LDS.
+//
 // The first operand of a matrix instruction is b: then a lane's results are four
 // columns of one row of out, it needs one scale of a, and stores them side by side.
-template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS>
+template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS, bool DIRECT>
 __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulArgs a, int tiles_m, int tiles_n) {
   constexpr int kWaves = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16, kRows = BM + BN;
   constexpr int GA = BM / 8 / kWaves, GB = BN / 8 / kWaves;  // a wave's loads: 8 rows each
@@ -163,26 +240,44 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
   const uint32_t lds = (uint32_t)(size_t)((__attribute__((address_space(3))) uint4 *)ring);
   const uint8_t *pa = a.a + m0 * a.a_stride, *pb = a.b + n0 * a.b_stride;
   const int piece = (lane & 7) ^ (lane >> 3);  // of its row, that this lane loads
-  uint32_t off[GA + GB];                       // from pa or pb: below 2^31 (the launch sees to it)
+  // from pa or pb; DIRECT: below 2^31 (the launch sees to it)
+  std::conditional_t<DIRECT, uint32_t, int64_t> off[GA + GB];
 #pragma unroll
   for (int i = 0; i < GA; ++i) {
     const int64_t row = (i * kWaves + wave) * 8 + (lane >> 3), last = a.m - 1 - m0;
-    off[i] = (uint32_t)((row < last ? row : last) * a.a_stride) + piece * 16;
+    off[i] = (row < last ? row : last) * a.a_stride + piece * 16;
   }
 #pragma unroll
   for (int i = 0; i < GB; ++i) {
     const int64_t row = (i * kWaves + wave) * 8 + (lane >> 3), last = a.n - 1 - n0;
-    off[GA + i] = (uint32_t)((row < last ? row : last) * a.b_stride) + piece * 16;
+    off[GA + i] = (row < last ? row : last) * a.b_stride + piece * 16;
   }
   const int k = (int)a.k, blocks = (k + kScaleBlock - 1) / kScaleBlock;
+  u32x4 held[DIRECT ? 1 : GA + GB];
   const auto load_stage = [&](int kb, int slot) {
-    // a piece behind the row's end is not read (any other is, and its place masked below)
-    const uint32_t ko = kb * kScaleBlock + piece * 16 < k ? (uint32_t)kb * kScaleBlock : (uint32_t)(-piece * 16);
-    const uint32_t to = lds + slot * kStage + wave * 1024;
+    if constexpr (DIRECT) {
+      // a piece behind the row's end is not read (any other is, and its place masked below)
+      const uint32_t ko = kb * kScaleBlock + piece * 16 < k ? (uint32_t)kb * kScaleBlock : (uint32_t)(-piece * 16);
+      const uint32_t to = lds + slot * kStage + wave * 1024;
 #pragma unroll
-    for (int i = 0; i < GA; ++i) load_lds(pa, off[i] + ko, to + i * kWaves * 1024);
+      for (int i = 0; i < GA; ++i) load_lds(pa, off[i] + ko, to + i * kWaves * 1024);
 #pragma unroll
-    for (int i = 0; i < GB; ++i) load_lds(pb, off[GA + i] + ko, to + BM * kScaleBlock + i * kWaves * 1024);
+      for (int i = 0; i < GB; ++i) load_lds(pb, off[GA + i] + ko, to + BM * kScaleBlock + i * kWaves * 1024);
+    } else {
+      const int64_t ko = (int64_t)kb * kScaleBlock, left = a.k - ko - piece * 16;
+#pragma unroll
+      for (int i = 0; i < GA + GB; ++i) held[i] = load_bytes((i < GA ? pa : pb) + off[i] + ko, left);
+    }
+  };
+  const auto store_stage = [&](int slot) {
+    if constexpr (!DIRECT) {
+      uint4 *to = ring + (slot * kStage + wave * 1024) / 16 + lane;
+#pragma unroll
+      for (int i = 0; i < GA; ++i) to[i * kWaves * 64] = {held[i][0], held[i][1], held[i][2], held[i][3]};
+#pragma unroll
+      for (int i = GA; i < GA + GB; ++i)
+        to[BM * kScaleBlock / 16 + (i - GA) * kWaves * 64] = {held[i][0], held[i][1], held[i][2], held[i][3]};
+    }
   };
   // the scales of the tile's rows: one a thread and block
   constexpr int kPer = (kRows + kWaves * 64 - 1) / (kWaves * 64);
@@ -284,6 +379,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
 
   load_scales(0);
   load_stage(0, 0);
+  store_stage(0);
   store_scales(0);
   if (blocks > 1) load_scales(1);
   const auto advance = [&](int kb) {
@@ -299,6 +395,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
   for (int kb = 0; kb < whole; ++kb) {
     advance(kb);
     block(std::false_type{}, kb, kb & 1);
+    if (kb + 1 < blocks) store_stage((kb + 1) & 1);
   }
   if (whole < blocks) {
     advance(whole);
@@ -323,14 +420,14 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
   }
 }
 
-template <int WM, int WN, int MT, int NT, bool EXACT>
+template <int WM, int WN, int MT, int NT, bool EXACT, bool DIRECT>
 static hipError_t tiles(const MatmulArgs &a, hipStream_t s) {
   const int tm = (int)ceil_div(a.m, WM * MT * 16), tn = (int)ceil_div(a.n, WN * NT * 16);
   const dim3 grid((unsigned)(ceil_div((int64_t)tm * tn, 8) * 8));
   if (a.sb.shift)
-    matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, true><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
+    matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, true, DIRECT><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
   else
-    matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, false><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
+    matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, false, DIRECT><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
   return hipGetLastError();
 }
 
@@ -339,14 +436,16 @@ hipError_t launch_matmul_f8(const MatmulArgs &a, hipStream_t s) {
   const auto even = [](const uint8_t *p, int64_t stride, int64_t k) {
     return (uintptr_t)p % 16 == 0 && stride % 16 == 0 && stride >= round_up(k, 16) && stride < (1 << 22);
   };
-  if (a.m > 32 && a.n > 32 && a.k > 0 && even(a.a, a.a_stride, a.k) && even(a.b, a.b_stride, a.k)) {
+  if (a.m > 32 && a.n > 32 && a.k > 0) {
+    if (!even(a.a, a.a_stride, a.k) || !even(a.b, a.b_stride, a.k))
+      return a.out_bf16 ? tiles<2, 2, 4, 4, false, false>(a, s) : tiles<2, 2, 4, 4, true, false>(a, s);
     const bool large = ceil_div(a.m, 256) * ceil_div(a.n, 256) >= 128;
-    if (a.out_bf16) return large ? tiles<2, 4, 8, 4, false>(a, s) : tiles<2, 2, 4, 4, false>(a, s);
-    return large ? tiles<4, 2, 4, 4, true>(a, s) : tiles<2, 2, 4, 4, true>(a, s);
+    if (a.out_bf16) return large ? tiles<2, 4, 8, 4, false, true>(a, s) : tiles<2, 2, 4, 4, false, true>(a, s);
+    return large ? tiles<4, 2, 4, 4, true, true>(a, s) : tiles<2, 2, 4, 4, true, true>(a, s);
   }
-  const dim3 grid((unsigned)ceil_div(a.n, 64), (unsigned)ceil_div(a.m, 16));
-  matmul_f8_simple_kernel<<<grid, kThreads, 0, s>>>(a);
-  return hipGetLastError();
+  // the operand with more rows is read once
+  if (a.m <= a.n) return a.m <= 16 ? few<1, false>(a, s) : few<2, false>(a, s);
+  return a.n <= 16 ? few<1, true>(a, s) : few<2, true>(a, s);
 }
 
 }  // namespace rvq
