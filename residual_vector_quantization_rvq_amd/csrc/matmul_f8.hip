@@ -19,15 +19,20 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 
-// 16 bytes of a row from byte k on; zeros beyond its end
-__device__ __forceinline__ u32x4 load_bytes(const uint8_t *p, int64_t left) {
+// 16 bytes of a row; zeros beyond its end, which is `left` bytes away
+__device__ __forceinline__ u32x4 load_whole(const uint8_t *p) {
   typedef u32x4 u32x4_at1 __attribute__((aligned(1)));
-  if (left >= 16) return *(const u32x4_at1 *)p;
-  u32x4 q = {0, 0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < 15; ++e)
-    if (e < left) q[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
-  return q;
+  return *(const u32x4_at1 *)p;
+}
+__device__ __forceinline__ u32x4 load_bytes(const uint8_t *p, int64_t left) {
+  if (left >= 16) return load_whole(p);
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int e = (int)left - 1; e >= 0; --e) {
+    hi = hi << 8 | lo >> 56;
+    lo = lo << 8 | p[e];
+  }
+  return {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 // eight e4m3 values as bf16, exactly
 __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
@@ -95,11 +100,11 @@ __device__ __forceinline__ void product(const Operand<EXACT> (&b)[NT], const Ope
 // of w and 16 MT of s, its KW waves the blocks of k in turn, straight from memory to
 // registers (each byte of w is read once).  The waves' sums are added in order.
 // Bound by the bytes of w: four blocks of a wave are on their way at once.
-template <int MT, int KW, bool SWAP>
-__global__ __launch_bounds__(KW * 64) void matmul_f8_few_kernel(MatmulArgs a) {
-  constexpr int U = 4;
+template <int MT, int KW, bool SWAP, bool W_BLOCKS>
+__global__ __launch_bounds__(KW * 64, 4) void matmul_f8_few_kernel(MatmulArgs a) {
+  constexpr int U = 4, E = W_BLOCKS ? 1 : 4;
   __shared__ f32x4 sums[KW][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const uint8_t *w = SWAP ? a.a : a.b, *s = SWAP ? a.b : a.a;
   const int64_t w_stride = SWAP ? a.a_stride : a.b_stride, s_stride = SWAP ? a.b_stride : a.a_stride;
@@ -108,7 +113,7 @@ __global__ __launch_bounds__(KW * 64) void matmul_f8_few_kernel(MatmulArgs a) {
   const int64_t w0 = (int64_t)blockIdx.x * 16, s0 = (int64_t)blockIdx.y * 16 * MT;
   const int64_t wr = w0 + r16 < w_rows ? w0 + r16 : w_rows - 1;
   const uint8_t *pw = w + wr * w_stride + g * 16, *ps[MT];
-  const float *qs[MT], *qw[4];
+  const float *qs[MT], *qw[E];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t row = s0 + i * 16 + r16 < s_rows ? s0 + i * 16 + r16 : s_rows - 1;
@@ -116,59 +121,72 @@ __global__ __launch_bounds__(KW * 64) void matmul_f8_few_kernel(MatmulArgs a) {
     qs[i] = vs.p + (row >> vs.shift) * vs.row_stride;
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < E; ++e) {
     const int64_t row = w0 + g * 4 + e < w_rows ? w0 + g * 4 + e : w_rows - 1;
-    qw[e] = vw.p + (row >> vw.shift) * vw.row_stride;
+    qw[e] = vw.p + (W_BLOCKS ? w0 >> vw.shift : row) * vw.row_stride;
   }
   f32x4 acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int64_t whole = a.k / kScaleBlock, blocks = ceil_div(a.k, kScaleBlock);
-  const auto add = [&](const Frag &fw, const Frag (&fs)[MT], const float (&sw)[4], const float (&ss)[MT]) {
-    const Operand<true> ow[1] = {Operand<true>(fw)};
+  const int whole = (int)(a.k / kScaleBlock), blocks = (int)ceil_div(a.k, kScaleBlock);
+  // what is on its way: w's bytes of the next U blocks, s's and the scales (from a cache) of the next
+  Frag fw[U], fs[MT];
+  float sw[E], ss[MT];
+  const auto load_w = [&](int kb, int u) {
+    const uint8_t *p = pw + (int64_t)kb * kScaleBlock;
+    fw[u] = {load_whole(p), load_whole(p + 64)};
+  };
+  const auto load_scales = [&](int kb) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sw[e] = qw[e][(int64_t)kb * vw.block_stride];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ss[i] = qs[i][(int64_t)kb * vs.block_stride];
+  };
+  const auto load_s = [&](int kb) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      f32x4 p[1];
-      product<true, 1>(ow, Operand<true>(fs[i]), p);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(p[0][e], ss[i] * sw[e], acc[i][e]);
+      const uint8_t *p = ps[i] + (int64_t)kb * kScaleBlock;
+      fs[i] = {load_whole(p), load_whole(p + 64)};
     }
+    load_scales(kb);
   };
-  const auto scales = [&](int64_t kb, float (&sw)[4], float (&ss)[MT]) {
-    sw[0] = qw[0][kb * vw.block_stride];
+  // adds a block; what comes next is sent for as soon as a fragment is free
+  const auto add = [&](const Frag &f, int next) {
+    const Operand<true> ow[1] = {Operand<true>(f)};
+    f32x4 p[MT][1];
+    float factor[MT][E];
 #pragma unroll
-    for (int e = 1; e < 4; ++e) sw[e] = vw.shift ? sw[0] : qw[e][kb * vw.block_stride];
+    for (int i = 0; i < MT; ++i) {
+      product<true, 1>(ow, Operand<true>(fs[i]), p[i]);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) ss[i] = qs[i][kb * vs.block_stride];
+      for (int e = 0; e < E; ++e) factor[i][e] = ss[i] * sw[e];
+    }
+    if (next < whole) load_s(next);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(p[i][0][e], factor[i][e % E], acc[i][e]);
   };
-  int64_t kb = wave;
-  for (; kb + (U - 1) * KW < whole; kb += U * KW) {
-    Frag fw[U], fs[U][MT];
-    float sw[U][4], ss[U][MT];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (wave + u * KW < whole) load_w(wave + u * KW, u);
+  if (wave < whole) load_s(wave);
+  for (int base = wave; base < whole; base += U * KW) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t k = (kb + u * KW) * kScaleBlock;
-      fw[u] = {load_bytes(pw + k, 16), load_bytes(pw + k + 64, 16)};
+      const int kb = base + u * KW;
+      if (kb >= whole) break;
+      add(fw[u], kb + KW);
+      if (kb + U * KW < whole) load_w(kb + U * KW, u);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t k = (kb + u * KW) * kScaleBlock;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fs[u][i] = {load_bytes(ps[i] + k, 16), load_bytes(ps[i] + k + 64, 16)};
-      scales(kb + u * KW, sw[u], ss[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) add(fw[u], fs[u], sw[u], ss[u]);
   }
-  for (; kb < blocks; kb += KW) {
-    const int64_t k = kb * kScaleBlock, left = a.k - k - g * 16;
-    Frag fs[MT];
-    float sw[4], ss[MT];
-    const Frag fw = {load_bytes(pw + k, left), load_bytes(pw + k + 64, left - 64)};
+  if (whole < blocks && whole % KW == wave) {  // the block that the row ends in
+    const int64_t k = (int64_t)whole * kScaleBlock, left = a.k - k - g * 16;
+    fw[0] = {load_bytes(pw + k, left), load_bytes(pw + k + 64, left - 64)};
 #pragma unroll
     for (int i = 0; i < MT; ++i) fs[i] = {load_bytes(ps[i] + k, left), load_bytes(ps[i] + k + 64, left - 64)};
-    scales(kb, sw, ss);
-    add(fw, fs, sw, ss);
+    load_scales(whole);
+    add(fw[0], whole);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) sums[wave][i][lane] = acc[i];
@@ -196,7 +214,10 @@ template <int MT, int KW, bool SWAP>
 static hipError_t few(const MatmulArgs &a, hipStream_t s) {
   const int64_t w_rows = SWAP ? a.m : a.n, s_rows = SWAP ? a.n : a.m;
   const dim3 grid((unsigned)ceil_div(w_rows, 16), (unsigned)ceil_div(s_rows, 16 * MT));
-  matmul_f8_few_kernel<MT, KW, SWAP><<<grid, KW * 64, 0, s>>>(a);
+  if ((SWAP ? a.sa : a.sb).shift)
+    matmul_f8_few_kernel<MT, KW, SWAP, true><<<grid, KW * 64, 0, s>>>(a);
+  else
+    matmul_f8_few_kernel<MT, KW, SWAP, false><<<grid, KW * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 template <int MT, bool SWAP>
