@@ -101,8 +101,8 @@ __device__ __forceinline__ void product(const Operand<EXACT> (&b)[NT], const Ope
 // registers (each byte of w is read once).  The waves' sums are added in order.
 // Bound by the bytes of w: four blocks of a wave are on their way at once.
 template <int MT, int KW, bool SWAP, bool W_BLOCKS>
-__global__ __launch_bounds__(KW * 64, 4) void matmul_f8_few_kernel(MatmulArgs a) {
-  constexpr int U = 4, E = W_BLOCKS ? 1 : 4;
+__global__ __launch_bounds__(KW * 64, KW == 4 && !W_BLOCKS ? 3 : 4) void matmul_f8_few_kernel(MatmulArgs a) {
+  constexpr int U = MT == 1 && W_BLOCKS ? 8 : 4, E = W_BLOCKS ? 1 : 4;
   __shared__ f32x4 sums[KW][MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
