@@ -226,6 +226,24 @@ static hipError_t few(const MatmulArgs &a, hipStream_t s) {
   return ceil_div(SWAP ? a.m : a.n, 16) >= 1024 ? few<MT, 4, SWAP>(a, s) : few<MT, 16, SWAP>(a, s);
 }
 
+// The order of a block's instructions: behind each matrix instruction the sums of
+// the row of tiles before, which run while it does.  Left to itself the compiler puts all
+// of a row's products first and its sums behind them, and two waves that begin together
+// then wait for the matrix core together and leave it idle together.
+template <bool B_BLOCKS, int MT, int NT>
+__device__ __forceinline__ void order_block() {
+  constexpr int kMfma = 0x8, kValu = 0x2, kRead = 0x100;
+  __builtin_amdgcn_sched_group_barrier(kRead, 2 * NT + (B_BLOCKS ? 1 : NT) + MT / 2 + 2, 0);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+      if (j == 0 && i + 1 < MT) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+      if (i > 0) __builtin_amdgcn_sched_group_barrier(kValu, B_BLOCKS ? 4 : 8, 0);
+    }
+}
+
 // ---- tiles ----
 // A workgroup of WM x WN waves makes a tile of BM x BN results, a wave MT x NT
 // products of 16 x 16.  Both operands' rows of one block (128 bytes each) are in LDS,
@@ -242,9 +260,7 @@ static hipError_t few(const MatmulArgs &a, hipStream_t s) {
 template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS, bool DIRECT>
 __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulArgs a, int tiles_m, int tiles_n) {
   constexpr int kWaves = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16, kRows = BM + BN;
-  constexpr int GA = BM / 8 / kWaves, GB = BN / 8 / kWaves;  // a wave's loads: 8 rows each
   constexpr int kStage = kRows * kScaleBlock;
-  static_assert(GA * 8 * kWaves == BM && GB * 8 * kWaves == BN, "whole loads");
   __shared__ uint4 ring[2 * kStage / 16];
   __shared__ float scales[2][kRows];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -260,56 +276,65 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
 
   const uint32_t lds = (uint32_t)(size_t)((__attribute__((address_space(3))) uint4 *)ring);
   const uint8_t *pa = a.a + m0 * a.a_stride, *pb = a.b + n0 * a.b_stride;
+  // The second half of the waves bring the data in (on each SIMD one of its two waves):
+  // while they send for the next stage, the others multiply, and then wait for them.
+  // (Through registers all waves do: half of them would not have enough.)
+  constexpr int kLoaders = DIRECT ? kWaves / 2 : kWaves;
+  constexpr int GA = BM / 8 / kLoaders, GB = BN / 8 / kLoaders;  // a wave's loads: 8 rows each
+  static_assert(GA * 8 * kLoaders == BM && GB * 8 * kLoaders == BN, "whole loads");
+  const bool loader = wave >= kWaves - kLoaders;
+  const int wl = wave - (kWaves - kLoaders);
   const int piece = (lane & 7) ^ (lane >> 3);  // of its row, that this lane loads
-  // from pa or pb; DIRECT: below 2^31 (the launch sees to it)
-  std::conditional_t<DIRECT, uint32_t, int64_t> off[GA + GB];
-#pragma unroll
-  for (int i = 0; i < GA; ++i) {
-    const int64_t row = (i * kWaves + wave) * 8 + (lane >> 3), last = a.m - 1 - m0;
-    off[i] = (row < last ? row : last) * a.a_stride + piece * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < GB; ++i) {
-    const int64_t row = (i * kWaves + wave) * 8 + (lane >> 3), last = a.n - 1 - n0;
-    off[GA + i] = (row < last ? row : last) * a.b_stride + piece * 16;
-  }
+  const int last_a = (int)min((int64_t)BM, a.m - m0) - 1, last_b = (int)min((int64_t)BN, a.n - n0) - 1;
   const int k = (int)a.k, blocks = (k + kScaleBlock - 1) / kScaleBlock;
   u32x4 held[DIRECT ? 1 : GA + GB];
   const auto load_stage = [&](int kb, int slot) {
     if constexpr (DIRECT) {
-      // a piece behind the row's end is not read (any other is, and its place masked below)
-      const uint32_t ko = kb * kScaleBlock + piece * 16 < k ? (uint32_t)kb * kScaleBlock : (uint32_t)(-piece * 16);
-      const uint32_t to = lds + slot * kStage + wave * 1024;
+      // rows beyond the last are read as the last; a piece behind the row's end is not
+      // read (its row's first is, and its place masked below); offsets are below 2^31 (the launch sees to it)
+      const uint32_t ko = kb * kScaleBlock + piece * 16 < k ? (uint32_t)(kb * kScaleBlock + piece * 16) : 0;
+      const uint32_t to = lds + slot * kStage + wl * 1024;
 #pragma unroll
-      for (int i = 0; i < GA; ++i) load_lds(pa, off[i] + ko, to + i * kWaves * 1024);
+      for (int i = 0; i < GA; ++i) {
+        const int row = min((i * kLoaders + wl) * 8 + (lane >> 3), last_a);
+        load_lds(pa, __umul24(row, (uint32_t)a.a_stride) + ko, to + i * kLoaders * 1024);
+      }
 #pragma unroll
-      for (int i = 0; i < GB; ++i) load_lds(pb, off[GA + i] + ko, to + BM * kScaleBlock + i * kWaves * 1024);
+      for (int i = 0; i < GB; ++i) {
+        const int row = min((i * kLoaders + wl) * 8 + (lane >> 3), last_b);
+        load_lds(pb, __umul24(row, (uint32_t)a.b_stride) + ko, to + BM * kScaleBlock + i * kLoaders * 1024);
+      }
     } else {
-      const int64_t ko = (int64_t)kb * kScaleBlock, left = a.k - ko - piece * 16;
+      const int64_t ko = (int64_t)kb * kScaleBlock + piece * 16;
 #pragma unroll
-      for (int i = 0; i < GA + GB; ++i) held[i] = load_bytes((i < GA ? pa : pb) + off[i] + ko, left);
+      for (int i = 0; i < GA + GB; ++i) {
+        const int at = ((i < GA ? i : i - GA) * kLoaders + wl) * 8 + (lane >> 3);
+        const int64_t from = i < GA ? min(at, last_a) * a.a_stride : min(at, last_b) * a.b_stride;
+        held[i] = load_bytes((i < GA ? pa : pb) + from + ko, a.k - ko);
+      }
     }
   };
   const auto store_stage = [&](int slot) {
     if constexpr (!DIRECT) {
-      uint4 *to = ring + (slot * kStage + wave * 1024) / 16 + lane;
+      uint4 *to = ring + (slot * kStage + wl * 1024) / 16 + lane;
 #pragma unroll
-      for (int i = 0; i < GA; ++i) to[i * kWaves * 64] = {held[i][0], held[i][1], held[i][2], held[i][3]};
+      for (int i = 0; i < GA; ++i) to[i * kLoaders * 64] = {held[i][0], held[i][1], held[i][2], held[i][3]};
 #pragma unroll
       for (int i = GA; i < GA + GB; ++i)
-        to[BM * kScaleBlock / 16 + (i - GA) * kWaves * 64] = {held[i][0], held[i][1], held[i][2], held[i][3]};
+        to[BM * kScaleBlock / 16 + (i - GA) * kLoaders * 64] = {held[i][0], held[i][1], held[i][2], held[i][3]};
     }
   };
-  // the scales of the tile's rows: one a thread and block
-  constexpr int kPer = (kRows + kWaves * 64 - 1) / (kWaves * 64);
+  // the scales of the tile's rows: kPer a loading thread and block
+  constexpr int kPer = (kRows + kLoaders * 64 - 1) / (kLoaders * 64);
+  const int tl = tid - (kWaves - kLoaders) * 64;
   const float *ps[kPer];
   int step[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int r = tid + i * kWaves * 64;
+    const int r = tl + i * kLoaders * 64;
     const bool of_a = r < BM;
     const ScaleView &v = of_a ? a.sa : a.sb;
-    const int64_t row = of_a ? (m0 + r < a.m ? m0 + r : a.m - 1) : (n0 + r - BM < a.n ? n0 + r - BM : a.n - 1);
+    const int64_t row = of_a ? m0 + min(max(r, 0), last_a) : n0 + min(r - BM, last_b);
     ps[i] = v.p + (row >> v.shift) * v.row_stride;
     step[i] = v.block_stride;
   }
@@ -317,12 +342,12 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
   const auto load_scales = [&](int kb) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (tid + i * kWaves * 64 < kRows) next[i] = ps[i][(int64_t)kb * step[i]];
+      if (tl + i * kLoaders * 64 < kRows) next[i] = ps[i][(int64_t)kb * step[i]];
   };
   const auto store_scales = [&](int slot) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (tid + i * kWaves * 64 < kRows) scales[slot][tid + i * kWaves * 64] = next[i];
+      if (tl + i * kLoaders * 64 < kRows) scales[slot][tl + i * kLoaders * 64] = next[i];
   };
 
   f32x4 acc[MT][NT];
@@ -370,43 +395,44 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
     for (int j = 0; j < NT; ++j) fb[j] = Operand<EXACT>(read(b_lo, b_hi, j));
     // Products of one row of tiles run while those of the row before are scaled and
     // added, and the next row's fragment is on its way; no further ahead, for registers.
-    const auto read_a = [&](int i, Frag &f, float &sa) {
-      f = read(a_lo, a_hi, i);
-      sa = sc[(wm * MT + i) * 16 + r16];
-    };
+    float sa[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sa[i] = sc[(wm * MT + i) * 16 + r16];
     Frag f[2];
-    float sa[2], s_of[2];
     f32x4 p[2][NT];
-    read_a(0, f[0], sa[0]);
+    f[0] = read(a_lo, a_hi, 0);
 #pragma unroll
     for (int i = 0; i <= MT; ++i) {
-      if (i + 1 < MT) read_a(i + 1, f[(i + 1) & 1], sa[(i + 1) & 1]);
+      if (i + 1 < MT) f[(i + 1) & 1] = read(a_lo, a_hi, i + 1);
       if (i < MT) {
-        const Operand<EXACT> fa(f[i & 1]);
-        s_of[i & 1] = B_BLOCKS ? sa[i & 1] * sb[0][0] : sa[i & 1];
-        product<EXACT, NT>(fb, fa, p[i & 1]);
+        if (B_BLOCKS) sa[i] *= sb[0][0];
+        product<EXACT, NT>(fb, Operand<EXACT>(f[i & 1]), p[i & 1]);
       }
       if (i > 0) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            acc[i - 1][j][e] = __builtin_fmaf(p[(i - 1) & 1][j][e],
-                                              B_BLOCKS ? s_of[(i - 1) & 1] : s_of[(i - 1) & 1] * sb[j][e], acc[i - 1][j][e]);
+            acc[i - 1][j][e] = __builtin_fmaf(p[(i - 1) & 1][j][e], B_BLOCKS ? sa[i - 1] : sa[i - 1] * sb[j][e],
+                                              acc[i - 1][j][e]);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (!EXACT) order_block<B_BLOCKS, MT, NT>();
   };
 
-  load_scales(0);
-  load_stage(0, 0);
-  store_stage(0);
-  store_scales(0);
-  if (blocks > 1) load_scales(1);
+  if (loader) {
+    load_scales(0);
+    load_stage(0, 0);
+    store_stage(0);
+    store_scales(0);
+    if (blocks > 1) load_scales(1);
+  } else if (!EXACT) {
+    __builtin_amdgcn_s_setprio(1);
+  }
   const auto advance = [&](int kb) {
     // this stage and the next scales are here, for all waves; the other stage has been read
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kb + 1 < blocks) {
+    if (loader && kb + 1 < blocks) {
       store_scales((kb + 1) & 1);
       if (kb + 2 < blocks) load_scales(kb + 2);
       load_stage(kb + 1, (kb + 1) & 1);
@@ -416,27 +442,57 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
   for (int kb = 0; kb < whole; ++kb) {
     advance(kb);
     block(std::false_type{}, kb, kb & 1);
-    if (kb + 1 < blocks) store_stage((kb + 1) & 1);
+    if (loader && kb + 1 < blocks) store_stage((kb + 1) & 1);
   }
   if (whole < blocks) {
     advance(whole);
     block(std::true_type{}, whole, whole & 1);
   }
 
+  if constexpr (EXACT) {  // fp32
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = m0 + (wm * MT + i) * 16 + r16;
-    if (m >= a.m) continue;
+    for (int i = 0; i < MT; ++i) {
+      const int64_t m = m0 + (wm * MT + i) * 16 + r16;
+      if (m >= a.m) continue;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int64_t n = n0 + (wn * NT + j) * 16 + g * 4;
-      const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      const int left = a.n - n < 4 ? (int)(a.n - n) : 4;
-      if (left <= 0) continue;
-      if (a.out_bf16)
-        store_n<4>((uint16_t *)a.out + m * a.n + n, left, v);
-      else
-        store_n<4>((float *)a.out + m * a.n + n, left, v);
+      for (int j = 0; j < NT; ++j) {
+        const int64_t n = n0 + (wn * NT + j) * 16 + g * 4;
+        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        const int left = a.n - n < 4 ? (int)(a.n - n) : 4;
+        if (left > 0) store_n<4>((float *)a.out + m * a.n + n, left, v);
+      }
+    }
+  } else {
+    // bf16, turned through the wave's part of LDS so that whole lines leave: a row of 64
+    // columns is eight pieces of 16 bytes, at their place ^ (row % 8)
+    static_assert(NT == 4 && kWaves * MT * 16 * 128 <= 2 * kStage, "the ring holds the tile");
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // all have read their last fragments
+    const uint32_t own = lds + wave * MT * 16 * 128;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const u32x2 q = {pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+        const uint32_t at = own + (i * 16 + r16) * 128 + (((j * 2 + (g >> 1)) ^ (r16 & 7)) << 4) + (g & 1) * 8;
+        *reinterpret_cast<__attribute__((address_space(3))) u32x2 *>((size_t)at) = q;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int64_t n = n0 + wn * NT * 16 + (lane & 7) * 8;
+    const int left = a.n - n < 8 ? (int)(a.n - n) : 8;
+#pragma unroll
+    for (int t = 0; t < MT * 2; ++t) {
+      const int row = t * 8 + (lane >> 3);
+      const int64_t m = m0 + wm * MT * 16 + row;
+      if (m >= a.m || left <= 0) continue;
+      const u32x4 q = read_lds(own + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+      uint16_t *to = (uint16_t *)a.out + m * a.n + n;
+      if (left == 8) {
+        *(u32x4_at2 *)to = q;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < left) to[e] = (uint16_t)(q[e >> 1] >> (16 * (e & 1)));
+      }
     }
   }
 }
@@ -461,7 +517,11 @@ hipError_t launch_matmul_f8(const MatmulArgs &a, hipStream_t s) {
     if (!even(a.a, a.a_stride, a.k) || !even(a.b, a.b_stride, a.k))
       return a.out_bf16 ? tiles<2, 2, 4, 4, false, false>(a, s) : tiles<2, 2, 4, 4, true, false>(a, s);
     const bool large = ceil_div(a.m, 256) * ceil_div(a.n, 256) >= 128;
-    if (a.out_bf16) return large ? tiles<2, 4, 8, 4, false, true>(a, s) : tiles<2, 2, 4, 4, false, true>(a, s);
+    if (a.out_bf16) {
+      if (!large) return tiles<2, 2, 4, 4, false, true>(a, s);
+      // b's scales by rows need more registers
+      return a.sb.shift ? tiles<2, 4, 8, 4, false, true>(a, s) : tiles<4, 2, 4, 4, false, true>(a, s);
+    }
     return large ? tiles<4, 2, 4, 4, true, true>(a, s) : tiles<2, 2, 4, 4, true, true>(a, s);
   }
   // the operand with more rows is read once
