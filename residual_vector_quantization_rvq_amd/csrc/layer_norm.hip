@@ -15,20 +15,32 @@
 // lanes of P 16-byte pieces; rows of more than 2048 pieces are read again for each
 // pass over them.
 #include "head.h"
+#include "lanes.h"
 #include "rows.h"
 
 namespace rvq {
 
 namespace {
 
-// Two sums over the W lanes of a row at once; `red` holds 2 * kThreads / 64.
+// Over the W lanes of a row; for W == kThreads through `red`, which holds
+// 2 * kThreads / 64 and is free again after the next barrier.
 template <int W>
-__device__ __forceinline__ void row_sum2(float &a, float &b, float *red) {
+__device__ __forceinline__ float sum_of_row(float v, float *red) {
+  v = lane_sum<W < 64 ? W : 64>(v);
+  if constexpr (W > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.f;
 #pragma unroll
-  for (int off = (W < 64 ? W : 64) / 2; off >= 1; off >>= 1) {
-    a += __shfl_xor(a, off, 64);
-    b += __shfl_xor(b, off, 64);
+    for (int w = 0; w < W / 64; ++w) v += red[w];
   }
+  return v;
+}
+template <int W>
+__device__ __forceinline__ void sums_of_row(float &a, float &b, float *red) {
+  a = lane_sum<W < 64 ? W : 64>(a);
+  b = lane_sum<W < 64 ? W : 64>(b);
   if constexpr (W > 64) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) {
@@ -43,6 +55,19 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, float *red) {
       b += red[2 * w + 1];
     }
   }
+}
+template <int W>
+__device__ __forceinline__ uint32_t top_of_row(uint32_t v, float *red) {
+  v = lane_max_bits<W < 64 ? W : 64>(v);
+  if constexpr (W > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = __uint_as_float(v);
+    __syncthreads();
+    v = __float_as_uint(red[0]);
+#pragma unroll
+    for (int w = 1; w < W / 64; ++w) v = max(v, __float_as_uint(red[w]));
+  }
+  return v;
 }
 
 // weight or bias; `none` where there is none
@@ -145,7 +170,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
         s += h[p][e];
         s2 += h[p][e] * h[p][e];
       }
-    row_sum2<W>(s, s2, red);
+    sums_of_row<W>(s, s2, red);
     const bool down = too_large(s2 * inv_d);  // the same for the row's lanes, as what follows from it
     if (down) {
       s = 0.f;
@@ -156,7 +181,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
           h[p][e] *= kDown;
           s += h[p][e];
         }
-      s = row_sum<W>(s, red);
+      s = sum_of_row<W>(s, red);
     }
     float m = rounded(s * inv_d);
     float s1 = 0.f;
@@ -177,7 +202,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
         s2 += h[p][e] * h[p][e];
       }
     }
-    row_sum2<W>(s1, s2, red);
+    sums_of_row<W>(s1, s2, red);
     const float off = rounded(s1 * inv_d);  // what m was short of
     m += off;
     float var = not_negative(s2 * inv_d - off * off);
@@ -198,7 +223,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
         }
       }
       shift = 0.f;
-      var = row_sum<W>(s2, red) * inv_d;
+      var = sum_of_row<W>(s2, red) * inv_d;
     }
     const Root root = root_of(var, a.eps, down, small);
     if (lane == 0) {
@@ -228,7 +253,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
       }
     }
     if (f8) {
-      const float scale = row_scale_of(row_max<W>(top, red));
+      const float scale = row_scale_of(top_of_row<W>(top, red));
       const float inv = 1.f / scale;
       if (lane == 0) a.scale[row] = scale;
 #pragma unroll
@@ -263,13 +288,13 @@ __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs
       s += h;
       s2 += h * h;
     }
-    row_sum2<kThreads>(s, s2, red);
+    sums_of_row<kThreads>(s, s2, red);
     const bool down = too_large(s2 * inv_d);
     const float f = down ? kDown : 1.f;
     if (down) {
       s = 0.f;
       for (int i = threadIdx.x; i < a.d; i += kThreads) s += h_of(i) * f;
-      s = row_sum<kThreads>(s, red);
+      s = sum_of_row<kThreads>(s, red);
     }
     float m = rounded(s * inv_d), s1 = 0.f;
     s2 = 0.f;
@@ -278,7 +303,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs
       s1 += c;
       s2 += c * c;
     }
-    row_sum2<kThreads>(s1, s2, red);
+    sums_of_row<kThreads>(s1, s2, red);
     const float off = rounded(s1 * inv_d);
     float var = not_negative(s2 * inv_d - off * off), up = 1.f;
     const bool small = !down && var + a.eps < 0x1p-100f;
@@ -289,7 +314,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs
         const float c = ((h_of(i) * f - m) - off) * up;
         s2 += c * c;
       }
-      var = row_sum<kThreads>(s2, red) * inv_d;
+      var = sum_of_row<kThreads>(s2, red) * inv_d;
     }
     const Root root = root_of(var, a.eps, down, small);
     if (threadIdx.x == 0) {
@@ -305,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs
     if (a.y_type == RVQ_F8E4M3) {
       uint32_t top = 0;
       for (int i = threadIdx.x; i < a.d; i += kThreads) top = max(top, magnitude_bits(y_of(h_of(i), i)));
-      scale = row_scale_of(row_max<kThreads>(top, red));
+      scale = row_scale_of(top_of_row<kThreads>(top, red));
       inv = 1.f / scale;
       if (threadIdx.x == 0) a.scale[row] = scale;
     }
@@ -411,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(LayerNormGrad
         dot += g[p][e] * u[p][e];
       }
     }
-    row_sum2<W>(sum, dot, red);
+    sums_of_row<W>(sum, dot, red);
     const float mg = sum / (float)a.d, mu = dot / (float)a.d;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -480,7 +505,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_wide_kernel(LayerNor
       sum += g;
       dot += g * u_of(i);
     }
-    row_sum2<kThreads>(sum, dot, red);
+    sums_of_row<kThreads>(sum, dot, red);
     const float mg = sum / (float)a.d, mu = dot / (float)a.d;
     for (int i = threadIdx.x; i < a.d; i += kThreads) {
       float v = r * ((g_of(i) - mg) - u_of(i) * mu);

@@ -17,6 +17,7 @@
 // sum of an all but certain row) is read again by the few threads whose largest
 // value says that they hold it.
 #include "head.h"
+#include "lanes.h"
 
 namespace rvq {
 
@@ -116,8 +117,7 @@ __device__ __forceinline__ void stream_row(const T *row, int cols, int lane, flo
 // ---- over the W threads of a row; W == 64: a wave, else the whole workgroup ----
 template <int W>
 __device__ __forceinline__ float all_max(float v, float *red) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  v = lane_max<64>(v);
   if constexpr (W > 64) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -130,8 +130,12 @@ __device__ __forceinline__ float all_max(float v, float *red) {
 }
 template <int W, typename F>
 __device__ __forceinline__ F all_sum(F v, F *red) {
+  if constexpr (sizeof(F) == 4) {
+    v = lane_sum<64>(v);
+  } else {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  }
   if constexpr (W > 64) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -145,11 +149,8 @@ __device__ __forceinline__ F all_sum(F v, F *red) {
 // two at once; `red` holds 2 W / 64
 template <int W>
 __device__ __forceinline__ void all_sum2(float &a, float &b, float *red) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    a += __shfl_xor(a, off, 64);
-    b += __shfl_xor(b, off, 64);
-  }
+  a = lane_sum<64>(a);
+  b = lane_sum<64>(b);
   if constexpr (W > 64) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) {
