@@ -52,5 +52,15 @@ __device__ __forceinline__ uint32_t lane_max_bits(uint32_t v) {
   }));
 }
 
+// the larger of a lane's value and that of the lane 16 (or 32) away
+__device__ __forceinline__ uint32_t lane_max_rows(uint32_t v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return max(r[0], r[1]);
+}
+__device__ __forceinline__ uint32_t lane_max_halves(uint32_t v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(r[0], r[1]);
+}
+
 }  // namespace
 }  // namespace rvq

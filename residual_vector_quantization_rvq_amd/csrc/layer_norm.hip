@@ -22,53 +22,50 @@ namespace rvq {
 
 namespace {
 
-// Over the W lanes of a row; for W == kThreads through `red`, which holds
-// 2 * kThreads / 64 and is free again after the next barrier.
+// Sums and largest values over the W lanes of a row.  For W == kThreads the waves meet
+// in LDS, in two places by turns: whoever writes to one again has passed a barrier
+// behind everyone's reading of it, so that one barrier a sum is enough.
 template <int W>
-__device__ __forceinline__ float sum_of_row(float v, float *red) {
-  v = lane_sum<W < 64 ? W : 64>(v);
-  if constexpr (W > 64) {
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.f;
+struct Row {
+  float (&red)[2][2 * kThreads / 64];
+  int turn = 0;
+
+  __device__ __forceinline__ void sums(float &a, float &b) {
+    a = lane_sum<W < 64 ? W : 64>(a);
+    b = lane_sum<W < 64 ? W : 64>(b);
+    if constexpr (W > 64) {
+      float *r = red[turn ^= 1];
+      if ((threadIdx.x & 63) == 0) {
+        r[2 * (threadIdx.x >> 6)] = a;
+        r[2 * (threadIdx.x >> 6) + 1] = b;
+      }
+      __syncthreads();
+      a = b = 0.f;
 #pragma unroll
-    for (int w = 0; w < W / 64; ++w) v += red[w];
-  }
-  return v;
-}
-template <int W>
-__device__ __forceinline__ void sums_of_row(float &a, float &b, float *red) {
-  a = lane_sum<W < 64 ? W : 64>(a);
-  b = lane_sum<W < 64 ? W : 64>(b);
-  if constexpr (W > 64) {
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) {
-      red[2 * (threadIdx.x >> 6)] = a;
-      red[2 * (threadIdx.x >> 6) + 1] = b;
-    }
-    __syncthreads();
-    a = b = 0.f;
-#pragma unroll
-    for (int w = 0; w < W / 64; ++w) {
-      a += red[2 * w];
-      b += red[2 * w + 1];
+      for (int w = 0; w < W / 64; ++w) {
+        a += r[2 * w];
+        b += r[2 * w + 1];
+      }
     }
   }
-}
-template <int W>
-__device__ __forceinline__ uint32_t top_of_row(uint32_t v, float *red) {
-  v = lane_max_bits<W < 64 ? W : 64>(v);
-  if constexpr (W > 64) {
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = __uint_as_float(v);
-    __syncthreads();
-    v = __float_as_uint(red[0]);
-#pragma unroll
-    for (int w = 1; w < W / 64; ++w) v = max(v, __float_as_uint(red[w]));
+  __device__ __forceinline__ float sum(float v) {
+    float none = 0.f;
+    sums(v, none);
+    return v;
   }
-  return v;
-}
+  __device__ __forceinline__ uint32_t top(uint32_t v) {
+    v = lane_max_bits<W < 64 ? W : 64>(v);
+    if constexpr (W > 64) {
+      float *r = red[turn ^= 1];
+      if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = __uint_as_float(v);
+      __syncthreads();
+      v = __float_as_uint(r[0]);
+#pragma unroll
+      for (int w = 1; w < W / 64; ++w) v = max(v, __float_as_uint(r[w]));
+    }
+    return v;
+  }
+};
 
 // weight or bias; `none` where there is none
 template <int N>
@@ -123,38 +120,62 @@ __device__ __forceinline__ float not_negative(float v) { return v < 0.f ? 0.f : 
 
 }  // namespace
 
-// Two pieces a lane are held to the registers of seven waves, as in the RMS norm.
+// What a lane keeps from row to row: its parts of weight and bias (up to 24 values of
+// each), which would otherwise be read from the L2 again for every row, four times the bytes of
+// a bf16 row, and the next row's bytes, which come while this one is summed.
+template <int P, int N>
+constexpr bool kKeep = P * N <= 24;
+// Workgroups of a launch: as many as are at work at once with these registers (of the
+// narrowest shapes, twice as many).  39,731 x 4096 bf16 129 us with four a CU, 152 with five, of
+// which one begins when the others end.
+template <int P, int N>
+constexpr int kAtOnce = 256 * (P * N <= 8 ? 12 : P * N <= 16 ? 4 : P * N <= 24 ? 3 : 16);
+
 template <typename T, int W, int P>
-__global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(LayerNormArgs a) {
+__global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a) {
   constexpr int N = kPiece<T>, R = kThreads / W;
-  __shared__ float red[2 * kThreads / 64];
+  constexpr bool keep = kKeep<P, N>;
+  __shared__ float red[2][2 * kThreads / 64];
+  Row<W> over{red};
   const int lane = threadIdx.x % W;
   const float inv_d = 1.f / (float)a.d;
-  // W == kThreads: the row is the same for the whole workgroup, as the barriers need
-  for (int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / W; row < a.n; row += (int64_t)gridDim.x * R) {
-    const int64_t at = row * a.d;
-    float h[P][N];
+  float w[P][N], b[P][N];
+  const auto params = [&](int p) {
+    const int c = (p * W + lane) * N;
+    load_param<N>(a.weight, a.w_bf16, c, a.d - c, 1.f, w[p]);
+    load_param<N>(a.bias, a.w_bf16, c, a.d - c, 0.f, b[p]);
+  };
+  u32x4 raw[P], raw_res[P];
+  const auto load = [&](int64_t row) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = (p * W + lane) * N;
-      if (c < a.d) {
-        load_n<N>((const T *)a.x + at + c, a.d - c, h[p]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) h[p][e] = 0.f;
-      }
+      raw[p] = load_piece((const T *)a.x + row * a.d + c, a.d - c);
+      if (a.residual) raw_res[p] = load_piece((const T *)a.residual + row * a.d + c, a.d - c);
     }
-    if (a.residual) {
+  };
+  const int64_t first = (int64_t)blockIdx.x * R + threadIdx.x / W, stride = (int64_t)gridDim.x * R;
+  if (keep && first < a.n) load(first);
+  if constexpr (keep) {
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int c = (p * W + lane) * N;
-        if (c >= a.d) continue;
+    for (int p = 0; p < P; ++p) params(p);
+  }
+  // W == kThreads: the row is the same for the whole workgroup, as the barriers need
+  for (int64_t row = first; row < a.n; row += stride) {
+    const int64_t at = row * a.d;
+    if (!keep) load(row);
+    float h[P][N];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      unpack(raw[p], h[p]);
+      if (a.residual) {
         float v[N];
-        load_n<N>((const T *)a.residual + at + c, a.d - c, v);
+        unpack(raw_res[p], v);
 #pragma unroll
         for (int e = 0; e < N; ++e) h[p][e] += v[e];
       }
     }
+    if (keep && row + stride < a.n) load(row + stride);
     if (a.sum) {  // after this lane's own loads of the piece: sum may be x or residual itself
 #pragma unroll
       for (int p = 0; p < P; ++p) {
@@ -170,7 +191,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
         s += h[p][e];
         s2 += h[p][e] * h[p][e];
       }
-    sums_of_row<W>(s, s2, red);
+    over.sums(s, s2);
     const bool down = too_large(s2 * inv_d);  // the same for the row's lanes, as what follows from it
     if (down) {
       s = 0.f;
@@ -181,7 +202,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
           h[p][e] *= kDown;
           s += h[p][e];
         }
-      s = sum_of_row<W>(s, red);
+      s = over.sum(s);
     }
     float m = rounded(s * inv_d);
     float s1 = 0.f;
@@ -202,7 +223,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
         s2 += h[p][e] * h[p][e];
       }
     }
-    sums_of_row<W>(s1, s2, red);
+    over.sums(s1, s2);
     const float off = rounded(s1 * inv_d);  // what m was short of
     m += off;
     float var = not_negative(s2 * inv_d - off * off);
@@ -223,7 +244,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
         }
       }
       shift = 0.f;
-      var = sum_of_row<W>(s2, red) * inv_d;
+      var = over.sum(s2) * inv_d;
     }
     const Root root = root_of(var, a.eps, down, small);
     if (lane == 0) {
@@ -237,11 +258,9 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
     for (int p = 0; p < P; ++p) {
       const int c = (p * W + lane) * N;
       if (c >= a.d) continue;
-      float w[N], b[N];
-      load_param<N>(a.weight, a.w_bf16, c, a.d - c, 1.f, w);
-      load_param<N>(a.bias, a.w_bf16, c, a.d - c, 0.f, b);
+      if (!keep) params(p);
 #pragma unroll
-      for (int e = 0; e < N; ++e) h[p][e] = (h[p][e] - shift) * r * w[e] + b[e];
+      for (int e = 0; e < N; ++e) h[p][e] = (h[p][e] - shift) * r * w[p][e] + b[p][e];
       if (f8) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
@@ -253,7 +272,7 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
       }
     }
     if (f8) {
-      const float scale = row_scale_of(top_of_row<W>(top, red));
+      const float scale = row_scale_of(over.top(top));
       const float inv = 1.f / scale;
       if (lane == 0) a.scale[row] = scale;
 #pragma unroll
@@ -272,7 +291,8 @@ __global__ __launch_bounds__(kThreads, P == 2 ? 7 : 1) void layer_norm_kernel(La
 // each pass over it, by elements.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs a) {
-  __shared__ float red[2 * kThreads / 64];
+  __shared__ float red[2][2 * kThreads / 64];
+  Row<kThreads> over{red};
   const T *x = (const T *)a.x, *res = (const T *)a.residual;
   const float inv_d = 1.f / (float)a.d;
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
@@ -288,13 +308,13 @@ __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs
       s += h;
       s2 += h * h;
     }
-    sums_of_row<kThreads>(s, s2, red);
+    over.sums(s, s2);
     const bool down = too_large(s2 * inv_d);
     const float f = down ? kDown : 1.f;
     if (down) {
       s = 0.f;
       for (int i = threadIdx.x; i < a.d; i += kThreads) s += h_of(i) * f;
-      s = sum_of_row<kThreads>(s, red);
+      s = over.sum(s);
     }
     float m = rounded(s * inv_d), s1 = 0.f;
     s2 = 0.f;
@@ -303,7 +323,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs
       s1 += c;
       s2 += c * c;
     }
-    sums_of_row<kThreads>(s1, s2, red);
+    over.sums(s1, s2);
     const float off = rounded(s1 * inv_d);
     float var = not_negative(s2 * inv_d - off * off), up = 1.f;
     const bool small = !down && var + a.eps < 0x1p-100f;
@@ -314,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs
         const float c = ((h_of(i) * f - m) - off) * up;
         s2 += c * c;
       }
-      var = sum_of_row<kThreads>(s2, red) * inv_d;
+      var = over.sum(s2) * inv_d;
     }
     const Root root = root_of(var, a.eps, down, small);
     if (threadIdx.x == 0) {
@@ -330,7 +350,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs
     if (a.y_type == RVQ_F8E4M3) {
       uint32_t top = 0;
       for (int i = threadIdx.x; i < a.d; i += kThreads) top = max(top, magnitude_bits(y_of(h_of(i), i)));
-      scale = row_scale_of(top_of_row<kThreads>(top, red));
+      scale = row_scale_of(over.top(top));
       inv = 1.f / scale;
       if (threadIdx.x == 0) a.scale[row] = scale;
     }
@@ -352,15 +372,15 @@ template <typename T>
 static hipError_t layer_norm_rows(const LayerNormArgs &a, hipStream_t s) {
   const Shape sh = shape_of(ceil_div(a.d, kPiece<T>));
   const int64_t groups = sh.w ? ceil_div(a.n, kThreads / sh.w) : a.n;
-  const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
-#define RVQ_NORM(W, P)                                           \
-  if (sh.w == W && sh.p == P) {                                  \
-    layer_norm_kernel<T, W, P><<<grid, kThreads, 0, s>>>(a);     \
-    return hipGetLastError();                                    \
+  const auto grid = [&](int64_t most) { return dim3((unsigned)(groups < most ? groups : most)); };
+#define RVQ_NORM(W, P)                                                                                \
+  if (sh.w == W && sh.p == P) {                                                                       \
+    layer_norm_kernel<T, W, P><<<grid(kAtOnce<P, kPiece<T>>), kThreads, 0, s>>>(a);                   \
+    return hipGetLastError();                                                                         \
   }
   RVQ_NORM_SHAPES(RVQ_NORM)
 #undef RVQ_NORM
-  layer_norm_wide_kernel<T><<<grid, kThreads, 0, s>>>(a);
+  layer_norm_wide_kernel<T><<<grid(kMaxGroups), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -396,7 +416,8 @@ int64_t layer_norm_grad_parts(int64_t n, int d, bool bf16) {
 template <typename T, int W, int P, bool DW>
 __global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(LayerNormGradArgs a) {
   constexpr int N = kPiece<T>, R = kThreads / W;
-  __shared__ float red[2 * kThreads / 64];
+  __shared__ float red[2][2 * kThreads / 64];
+  Row<W> over{red};
   const int lane = threadIdx.x % W;
   float acc[P][N], accb[P][N];
 #pragma unroll
@@ -436,7 +457,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(LayerNormGrad
         dot += g[p][e] * u[p][e];
       }
     }
-    sums_of_row<W>(sum, dot, red);
+    over.sums(sum, dot);
     const float mg = sum / (float)a.d, mu = dot / (float)a.d;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -490,7 +511,8 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(LayerNormGrad
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void layer_norm_grad_wide_kernel(LayerNormGradArgs a) {
-  __shared__ float red[2 * kThreads / 64];
+  __shared__ float red[2][2 * kThreads / 64];
+  Row<kThreads> over{red};
   const T *dy = (const T *)a.dy, *h = (const T *)a.h, *ds = (const T *)a.dsum;
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
     const int64_t at = row * a.d;
@@ -505,7 +527,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_wide_kernel(LayerNor
       sum += g;
       dot += g * u_of(i);
     }
-    sums_of_row<kThreads>(sum, dot, red);
+    over.sums(sum, dot);
     const float mg = sum / (float)a.d, mu = dot / (float)a.d;
     for (int i = threadIdx.x; i < a.d; i += kThreads) {
       float v = r * ((g_of(i) - mg) - u_of(i) * mu);

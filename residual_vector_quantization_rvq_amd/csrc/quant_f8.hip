@@ -9,6 +9,7 @@
 // its largest value and its quotients), and the bytes are written once; a
 // transposed tile turns through LDS, so that its rows leave in whole lines.
 #include "head.h"
+#include "lanes.h"
 
 namespace rvq {
 
@@ -65,9 +66,11 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantArgs a) {
 template <typename T, bool BLOCK, bool TRANS>
 __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs a) {
   constexpr int N = kPiece<T>, L = kB / N, G = kThreads / L, R = kB / G;  // G groups of R rows
-  constexpr int kPitch = kB + 16;  // bytes of a turned row in LDS, whole 16-byte pieces
-  __shared__ uint32_t tops[BLOCK ? kThreads / 64 : G * kB];
-  __shared__ __attribute__((aligned(16))) uint8_t turned[TRANS ? kB * kPitch : 16];
+  constexpr int kWaves = kThreads / 64;
+  __shared__ __attribute__((aligned(16))) uint32_t tops[BLOCK ? kWaves : kWaves * kB];
+  // a turned row is eight pieces of 16 bytes, piece p of row r at p ^ (r / 8 % 8), so that
+  // the lanes of a wave, eight or four rows apart, do not meet in a bank
+  __shared__ __attribute__((aligned(16))) uint8_t turned[TRANS ? kB * kB : 16];
   const int64_t tiles_c = ceil_div(a.cols, kB), tiles_r = ceil_div(a.rows, kB);
   const int lane = threadIdx.x % L, g = threadIdx.x / L;
   for (int64_t t = blockIdx.x; t < tiles_r * tiles_c; t += gridDim.x) {
@@ -104,16 +107,30 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs a) {
       for (int e = 0; e < N; ++e) scale[e] = scale_of(all);
       if (threadIdx.x == 0) a.scale[TRANS ? tc * tiles_r + tr : t] = scale[0];
     } else {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < N; ++e) tops[g * kB + lane * N + e] = top[e];
-      __syncthreads();
+      // over the groups of this wave, then over the waves
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        uint32_t all = 0;
+        if constexpr (L == 16) top[e] = lane_max_rows(top[e]);
+        top[e] = lane_max_halves(top[e]);
+      }
+      __syncthreads();  // the tile before has read tops and turned
+      if ((threadIdx.x & 63) < L) {
 #pragma unroll
-        for (int o = 0; o < G; ++o) all = max(all, tops[o * kB + lane * N + e]);
-        scale[e] = scale_of(all);
+        for (int e = 0; e < N; e += 4)
+          *(u32x4 *)(tops + (threadIdx.x >> 6) * kB + lane * N + e) = u32x4{top[e], top[e + 1], top[e + 2], top[e + 3]};
+      }
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+          const u32x4 q = *(const u32x4 *)(tops + w * kB + lane * N + e);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) top[e + f] = max(top[e + f], q[f]);
+        }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        scale[e] = scale_of(top[e]);
         if (g == 0 && e < left) a.scale[(c + e) * tiles_r + tr] = scale[e];
       }
     }
@@ -131,11 +148,16 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs a) {
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e)
+      for (int e = 0; e < N; ++e) {
+        const int row = lane * N + e, at = row * kB + (((g * R) >> 4 ^ (row >> 3 & 7)) << 4) + (g * R & 15);
+        uint32_t word[R / 4];
 #pragma unroll
-        for (int i = 0; i < R; i += 4)
-          *(uint32_t *)(turned + (lane * N + e) * kPitch + g * R + i) =
-              pack_f8x4(v[i][e], v[i + 1][e], v[i + 2][e], v[i + 3][e]);
+        for (int i = 0; i < R; i += 4) word[i / 4] = pack_f8x4(v[i][e], v[i + 1][e], v[i + 2][e], v[i + 3][e]);
+        if constexpr (R == 8)
+          *(u32x2 *)(turned + at) = u32x2{word[0], word[1]};
+        else
+          *(u32x4 *)(turned + at) = u32x4{word[0], word[1], word[2], word[3]};
+      }
       __syncthreads();
       // 16 bytes a lane, 8 lanes a turned row
       const int64_t r0 = tr * kB + (threadIdx.x % 8) * 16;
@@ -143,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs a) {
       for (int i = threadIdx.x / 8; i < kB; i += kThreads / 8) {
         const int64_t col = tc * kB + i;
         if (col >= a.cols || left_r <= 0) continue;
-        const uint8_t *from = turned + i * kPitch + (threadIdx.x % 8) * 16;
+        const uint8_t *from = turned + i * kB + ((threadIdx.x % 8 ^ (i >> 3 & 7)) << 4);
         uint8_t *to = a.q + col * a.q_stride + r0;
         if (left_r == 16) {
           typedef u32x4 u32x4_at1 __attribute__((aligned(1)));
