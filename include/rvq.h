@@ -543,7 +543,7 @@ rvq_status rvq_quantize_f8(const void *x, rvq_dtype x_dtype, int64_t rows, int64
  * a_scale, b_scale : device, fp32, laid out as a_layout and b_layout say; a product
  *                of two scales has to be within fp32.
  * out          : device, [m][n] in out_dtype (RVQ_F32 or RVQ_BF16).  k == 0 gives zeros.
- * Limits: m, n <= 2^30, m n <= 2^40, k <= 2^30.
+ * Limits: m, n <= 2^27, m n <= 2^36, k <= 2^30.
  */
 rvq_status rvq_matmul_f8(const void *a, int64_t a_stride, const float *a_scale,
                          rvq_scale_layout a_layout, const void *b, int64_t b_stride,

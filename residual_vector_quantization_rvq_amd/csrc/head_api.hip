@@ -14,6 +14,8 @@ constexpr int64_t kMaxRows = (int64_t)1 << 25;
 constexpr int kMaxWidth = 1 << 20;
 constexpr int kMaxVocab = 1 << 24;
 constexpr int64_t kMaxSide = (int64_t)1 << 30, kMaxArea = (int64_t)1 << 40;
+// of a product: its workgroups stay under 2^32 work-items
+constexpr int64_t kMaxMatmulRows = (int64_t)1 << 27, kMaxMatmulArea = (int64_t)1 << 36;
 
 rvq_status need(const void *p, const char *name, size_t align) {
   if (!p) return fail(RVQ_ERR_INVALID_ARGUMENT, "%s must not be NULL", name);
@@ -181,9 +183,9 @@ rvq_status rvq_matmul_f8(const void *a, int64_t a_stride, const float *a_scale,
   if (m < 0 || n < 0 || k < 0)
     return fail(RVQ_ERR_INVALID_ARGUMENT, "m, n and k must be >= 0 (got %lld, %lld, %lld)", (long long)m, (long long)n,
                 (long long)k);
-  if (m > kMaxSide || n > kMaxSide || k > kMaxSide || m * n > kMaxArea)
-    return fail(RVQ_ERR_UNSUPPORTED, "m, n or k above 2^30, or m n above 2^40 (got %lld, %lld, %lld)", (long long)m,
-                (long long)n, (long long)k);
+  if (m > kMaxMatmulRows || n > kMaxMatmulRows || k > kMaxSide || m * n > kMaxMatmulArea)
+    return fail(RVQ_ERR_UNSUPPORTED, "m or n above 2^27, k above 2^30, or m n above 2^36 (got %lld, %lld, %lld)",
+                (long long)m, (long long)n, (long long)k);
   RVQ_TRY(check_dtype(out_dtype, "out_dtype"));
   MatmulArgs r;
   RVQ_TRY(view_of(a_scale, a_layout, k, "a_layout", &r.sa));

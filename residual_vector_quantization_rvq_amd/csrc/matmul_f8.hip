@@ -18,6 +18,7 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
+constexpr int kFewRows = 32;  // of either operand: no tiles
 
 // 16 bytes of a row; zeros beyond its end, which is `left` bytes away
 __device__ __forceinline__ u32x4 load_whole(const uint8_t *p) {
@@ -497,32 +498,46 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
   }
 }
 
-template <int WM, int WN, int MT, int NT, bool EXACT, bool DIRECT>
+// k == 0
+__global__ __launch_bounds__(kThreads) void matmul_f8_empty_kernel(MatmulArgs a) {
+  const int64_t total = a.m * a.n;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads)
+    a.out_bf16 ? store_f32((uint16_t *)a.out, i, 0.f) : store_f32((float *)a.out, i, 0.f);
+}
+
+template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS, bool DIRECT>
 static hipError_t tiles(const MatmulArgs &a, hipStream_t s) {
   const int tm = (int)ceil_div(a.m, WM * MT * 16), tn = (int)ceil_div(a.n, WN * NT * 16);
   const dim3 grid((unsigned)(ceil_div((int64_t)tm * tn, 8) * 8));
-  if (a.sb.shift)
-    matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, true, DIRECT><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
-  else
-    matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, false, DIRECT><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
+  matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, B_BLOCKS, DIRECT><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
   return hipGetLastError();
+}
+template <bool EXACT, bool B_BLOCKS>
+static hipError_t tiles(const MatmulArgs &a, hipStream_t s) {
+  const auto even = [](const uint8_t *p, int64_t stride, int64_t k) {
+    return (uintptr_t)p % 16 == 0 && stride % 16 == 0 && stride >= round_up(k, 16) && stride < (1 << 22);
+  };
+  if (!even(a.a, a.a_stride, a.k) || !even(a.b, a.b_stride, a.k)) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false>(a, s);
+  // large tiles move half the bytes, but only as many workgroups as there are of them
+  if (ceil_div(a.m, 256) * ceil_div(a.n, 256) < 128) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, true>(a, s);
+  // 256 x 256 where the registers hold a wave's 128 x 64, that is 8-bit operands and one scale of b a wave
+  if constexpr (!EXACT && B_BLOCKS)
+    return tiles<2, 4, 8, 4, EXACT, B_BLOCKS, true>(a, s);
+  else
+    return tiles<4, 2, 4, 4, EXACT, B_BLOCKS, true>(a, s);
 }
 
 hipError_t launch_matmul_f8(const MatmulArgs &a, hipStream_t s) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
-  const auto even = [](const uint8_t *p, int64_t stride, int64_t k) {
-    return (uintptr_t)p % 16 == 0 && stride % 16 == 0 && stride >= round_up(k, 16) && stride < (1 << 22);
-  };
-  if (a.m > 32 && a.n > 32 && a.k > 0) {
-    if (!even(a.a, a.a_stride, a.k) || !even(a.b, a.b_stride, a.k))
-      return a.out_bf16 ? tiles<2, 2, 4, 4, false, false>(a, s) : tiles<2, 2, 4, 4, true, false>(a, s);
-    const bool large = ceil_div(a.m, 256) * ceil_div(a.n, 256) >= 128;
-    if (a.out_bf16) {
-      if (!large) return tiles<2, 2, 4, 4, false, true>(a, s);
-      // b's scales by rows need more registers
-      return a.sb.shift ? tiles<2, 4, 8, 4, false, true>(a, s) : tiles<4, 2, 4, 4, false, true>(a, s);
-    }
-    return large ? tiles<4, 2, 4, 4, true, true>(a, s) : tiles<2, 2, 4, 4, true, true>(a, s);
+  if (a.k == 0) {
+    const int64_t groups = ceil_div(a.m * a.n, kThreads);
+    matmul_f8_empty_kernel<<<dim3((unsigned)(groups < 4096 ? groups : 4096)), kThreads, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const bool blocks = a.sb.shift != 0;
+  if (a.m > kFewRows && a.n > kFewRows) {
+    if (a.out_bf16) return blocks ? tiles<false, true>(a, s) : tiles<false, false>(a, s);
+    return blocks ? tiles<true, true>(a, s) : tiles<true, false>(a, s);
   }
   // the operand with more rows is read once
   if (a.m <= a.n) return a.m <= 16 ? few<1, false>(a, s) : few<2, false>(a, s);
