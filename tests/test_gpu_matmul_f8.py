@@ -118,7 +118,10 @@ def _check_product(rvq, a, sa, b, sb, odt, **kw):
 # one row, few rows, tiles and what is left of them, contractions within, at and past a block
 SHAPES = [(1, 1, 1), (1, 16, 128), (1, 1000, 4096), (2, 17, 31), (5, 300, 129), (16, 64, 256), (17, 65, 384), (33, 257, 640),
           (64, 64, 16), (64, 1152, 1152), (65, 100, 1155), (100, 129, 112), (128, 128, 128), (129, 256, 1000), (200, 700, 2048),
-          (256, 256, 1024), (257, 511, 4096), (300, 1000, 1280), (512, 640, 100), (1000, 1024, 256), (700, 513, 5000)]
+          (256, 256, 1024), (257, 511, 4096), (300, 1000, 1280), (512, 640, 100), (1000, 1024, 256), (700, 513, 5000),
+          # few rows beside many, on either side; tiles of each size, whole and broken
+          (1, 50000, 260), (16, 40001, 1000), (17, 33000, 128), (32, 30000, 129), (30000, 16, 200), (40000, 31, 1155),
+          (900, 1300, 300), (1300, 1400, 1155), (2560, 4200, 384), (4100, 5001, 273), (4096, 8192, 128)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
@@ -132,7 +135,8 @@ def test_product(rvq, dev, shape):
 
 def test_product_of_small_whole_numbers_is_exact(rvq, dev):
     g = torch.Generator(device=dev).manual_seed(3)
-    for m, n, k in ((1, 333, 1000), (7, 128, 2048), (100, 300, 999), (256, 512, 1024), (515, 700, 640), (1024, 2048, 4096)):
+    for m, n, k in ((1, 333, 1000), (7, 128, 2048), (100, 300, 999), (256, 512, 1024), (515, 700, 640), (1024, 2048, 4096),
+                    (9, 44000, 500), (31, 34000, 300), (2700, 4300, 999)):
         a = torch.randint(-4, 5, (m, k), generator=g, device=dev).to(F8)
         b = torch.randint(-4, 5, (n, k), generator=g, device=dev).to(F8)
         kb = -(-k // 128)
@@ -147,7 +151,8 @@ def test_product_of_small_whole_numbers_is_exact(rvq, dev):
 
 def test_product_of_rows_that_are_apart(rvq, dev):
     # padding between rows (NaN bytes in it), slices of columns, rows at any byte
-    for m, n, k in ((3, 200, 300), (70, 130, 777), (300, 260, 1000), (260, 513, 130)):
+    # (few rows of one operand, and tiles, for which both ways are the same sums in the same order)
+    for m, n, k in ((3, 200, 300), (70, 130, 777), (300, 260, 1000), (260, 513, 130), (1100, 1000, 300), (1000, 2100, 130)):
         a, sa = _operand(rvq, m, k, "line", 1, dev)
         b, sb = _operand(rvq, n, k, "block", 2, dev)
         want = rvq.rvq_matmul_f8(a.contiguous(), sa, b.contiguous(), sb, out_dtype=F32)
