@@ -18,7 +18,6 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
-constexpr int kFewRows = 32;
 
 // 16 bytes of a row; zeros beyond its end, which is `left` bytes away
 __device__ __forceinline__ u32x4 load_whole(const uint8_t *p) {
@@ -223,10 +222,10 @@ static hipError_t few(const MatmulArgs &a, hipStream_t s) {
 }
 template <int MT, bool SWAP>
 static hipError_t few(const MatmulArgs &a, hipStream_t s) {
-  // fewer workgroups than two a CU: more waves each (one row, k = 4096: of 4096 rows 5.6 us with sixteen
-  // waves and 6.9 with four, of 8192 rows 8.5 and 8.1)
+  // fewer workgroups than four a CU: more waves each (one row, k = 4096: of 4096 rows 6.6 us with sixteen
+  // waves and 9.8 with four, of 8192 rows 11.2 and 13.2; in the Infinity Cache 16,384 rows 18.5 and 17.1)
   const int64_t groups = ceil_div(SWAP ? a.m : a.n, 16) * ceil_div(SWAP ? a.n : a.m, 16 * MT);
-  return groups >= 512 ? few<MT, 4, SWAP>(a, s) : few<MT, 16, SWAP>(a, s);
+  return groups >= 1024 ? few<MT, 4, SWAP>(a, s) : few<MT, 16, SWAP>(a, s);
 }
 
 // The order of a block's instructions: behind each matrix instruction the sums of
@@ -518,10 +517,6 @@ template <bool EXACT, bool B_BLOCKS>
 static hipError_t tiles(const MatmulArgs &a, bool direct, hipStream_t s) {
   // 8192 x 8192 x 8192: 498 us direct and 1223 us through registers, fp32 results 962 and 2470
   if (!direct) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false>(a, s);
-  // few rows of a: as little of them in LDS, and two workgroups a CU (65,536 rows of 4096, one row:
-  // 41 us, 6.6 TB/s, 54 us straight from memory, 43 to 74 us in tiles of 128 rows; 32 rows 44, 118 and 47 to 69 us)
-  if (a.m <= 16) return tiles<1, 4, 1, 4, EXACT, B_BLOCKS, true>(a, s);
-  if (a.m <= kFewRows) return tiles<1, 4, 2, 4, EXACT, B_BLOCKS, true>(a, s);
   // 256 x 256 where the registers hold a wave's 128 x 64, that is 8-bit operands and one scale of b a
   // wave; else 256 x 128.  Large tiles move half the bytes, but only as many workgroups as there are of them
   // (k = 4096: 192 of 256 x 256 66 us, their 768 parts 83; 128 of them 60 us, their 512 parts 45; fp32 results, 192 of
@@ -546,10 +541,12 @@ hipError_t launch_matmul_f8(const MatmulArgs &a, hipStream_t s) {
   };
   const bool direct = even(a.a, a.a_stride, a.k) && even(a.b, a.b_stride, a.k);
   const int64_t few_rows = a.m < a.n ? a.m : a.n, many = a.m < a.n ? a.n : a.m;
-  // Straight from memory where that is less than the latency of a tile's stages, 0.9 us for each of its blocks of k:
-  // it takes about (52 + 2 rows) us for 65,536 rows of 4096 on the other side (1 x 16,384 17 and 27 us; 64 x 8192 both 31;
-  // 128 x 8192 60 and 32).  And where there are no tiles for few rows: of b, or of rows at any address.
-  if (many * (few_rows + 26) <= (1 << 20) || (few_rows <= kFewRows && (!direct || a.m > a.n))) {
+  // Straight from memory where that is less than a tile's time, which is at least that of its stages, about 1.2 us
+  // for each of its blocks of k: it takes about (52 + 2.2 rows) us for 65,536 rows of 4096 on the other side (from HBM: 1 x
+  // 65,536 57 and 82 us, 8 rows 69 and 75, 16 rows 82 and 76; 16 x 32,768 45 and 47, 32 rows 63 and 47; 32 x 16,384 35
+  // and 39, 64 rows 62 and 40; 64 x 8192 34 and 38; 128 x 4096 33 and 38).  And few rows at any address (tiles of them
+  // go through registers, at half the rate).
+  if (many * (few_rows + 2) <= 655360 || (few_rows <= 32 && !direct)) {
     if (a.m <= a.n) return a.m <= 16 ? few<1, false>(a, s) : few<2, false>(a, s);
     return a.n <= 16 ? few<1, true>(a, s) : few<2, true>(a, s);
   }

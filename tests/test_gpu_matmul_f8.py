@@ -120,7 +120,7 @@ SHAPES = [(1, 1, 1), (1, 16, 128), (1, 1000, 4096), (2, 17, 31), (5, 300, 129), 
           (64, 64, 16), (64, 1152, 1152), (65, 100, 1155), (100, 129, 112), (128, 128, 128), (129, 256, 1000), (200, 700, 2048),
           (256, 256, 1024), (257, 511, 4096), (300, 1000, 1280), (512, 640, 100), (1000, 1024, 256), (700, 513, 5000),
           # few rows beside many, on either side; tiles of each size, whole and broken
-          (1, 50000, 260), (16, 40001, 1000), (17, 33000, 128), (32, 30000, 129), (30000, 16, 200), (40000, 31, 1155),
+          (1, 50000, 260), (16, 40001, 1000), (17, 33000, 128), (32, 30000, 129), (30000, 16, 200), (40000, 31, 1155), (40000, 20, 256),
           (900, 1300, 300), (1300, 1400, 1155), (2560, 4200, 384), (4100, 5001, 273), (4096, 8192, 128)]
 
 
