@@ -832,10 +832,13 @@ def rvq_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         out = torch.empty_like(x, dtype=odt)
     else:
         _need_shape("out", out, (n, d), odt, dev)
-    scale = torch.empty(n, dtype=torch.float32, device=dev) if f8 else None
-    mean = rstd = None
-    if need_stats:
-        mean, rstd = (torch.empty(n, dtype=torch.float32, device=dev) for _ in range(2))
+    scale = mean = rstd = None
+    if f8 and need_stats:  # one allocation
+        scale, mean, rstd = torch.empty((3, n), dtype=torch.float32, device=dev).unbind(0)
+    elif need_stats:
+        mean, rstd = torch.empty((2, n), dtype=torch.float32, device=dev).unbind(0)
+    elif f8:
+        scale = torch.empty(n, dtype=torch.float32, device=dev)
     _on_device(dev, _lib.rvq_layer_norm, x.data_ptr(), _address(residual), code, n, d,
                _address(weight), _address(bias), wcode, eps, _address(sum_out), out.data_ptr(), ocode,
                _address(scale), _address(mean), _address(rstd), _raw_stream(dev))

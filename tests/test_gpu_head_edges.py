@@ -1,0 +1,199 @@
+"""Edges of the calls for a model's head: memory past 32-bit offsets, buffers that begin
+at any element, rows left as they were, results that do not depend on what stands beside."""
+import pytest
+import torch
+
+import head_ref as ref
+import learn_ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def rvq():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import residual_vector_quantization_rvq_amd as m
+    return m
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return torch.device("cuda:0")
+
+
+def _randn(shape, seed, dev, dtype=F32, scale=1.0):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    return (scale * torch.randn(shape, generator=g, device=dev)).to(dtype)
+
+
+def _bits(t):
+    return t.contiguous().view(-1).view(torch.uint8)
+
+
+def test_layer_norm_offsets_past_32_bits(rvq, dev):
+    n, d = 66000, 65536
+    x = torch.zeros((n, d), dtype=BF16, device=dev)
+    x[-3:] = _randn((3, d), 7, dev, BF16) + 1.0
+    out = rvq.rvq_layer_norm(x, need_stats=True)
+    few = rvq.rvq_layer_norm(x[-3:].contiguous(), need_stats=True)
+    assert torch.equal(out.y[-3:], few.y) and torch.equal(out.mean[-3:], few.mean) and torch.equal(out.rstd[-3:], few.rstd)
+    dy = torch.zeros_like(x)
+    dy[-3:] = _randn((3, d), 9, dev, BF16)
+    small = rvq.rvq_layer_norm_backward(dy[-3:].contiguous(), x[-3:].contiguous(), few.mean, few.rstd, need_dweight=False,
+                                        need_dbias=False)[0]
+    dx = rvq.rvq_layer_norm_backward(dy, x, out.mean, out.rstd, need_dweight=False, need_dbias=False, out=out.y)[0]
+    assert torch.equal(dx[-3:], small) and float(dx[:-3:997].float().abs().sum()) == 0.0
+
+
+def test_quantiser_and_product_offsets_past_32_bits(rvq, dev):
+    # an operand and a result of more than 2^32 elements
+    n, k = 1100000, 4096
+    x = torch.zeros((n, k), dtype=BF16, device=dev)
+    tail = _randn((200, k), 1, dev, BF16)
+    x[-200:] = tail
+    q, s = rvq.rvq_quantize_f8(x)
+    qt, st = rvq.rvq_quantize_f8(tail)
+    assert torch.equal(_bits(q[-200:]), _bits(qt)) and torch.equal(s[-200:], st)
+    q2, s2 = rvq.rvq_quantize_f8(x, 128, transpose=True)
+    qt2, st2 = rvq.rvq_quantize_f8(x[-(n % 128 or 128):].contiguous(), 128, transpose=True)
+    assert torch.equal(_bits(q2[:, -(n % 128 or 128):]), _bits(qt2)) and torch.equal(s2[:, -1:], st2)
+    del x, q2
+    a, sa = rvq.rvq_quantize_f8(_randn((4000, k), 2, dev, BF16))
+    want = rvq.rvq_matmul_f8(a, sa, qt, st, out_dtype=F32)
+    got = rvq.rvq_matmul_f8(a, sa, q, s)                        # 4.4e9 bf16 results
+    assert torch.equal(got[:, -200:], rvq.rvq_matmul_f8(a, sa, q[-200:], s[-200:])) or \
+        torch.all((got[:, -200:].double() - want.double()).abs() <=
+                  (ref.BF16_ROUND + 7 * 2 ** -13) * ref.matmul(a, sa, qt, st)[1])
+    assert float(got[::500, :-200:997].float().abs().sum()) == 0.0
+    one = rvq.rvq_matmul_f8(a[:1], sa[:1], q, s, out_dtype=F32)  # the last rows lie past 2^32 bytes
+    few = rvq.rvq_matmul_f8(a[:1], sa[:1], qt, st, out_dtype=F32)
+    size = ref.matmul(a[:1], sa[:1], qt, st)[1]
+    learn_ref.close(one[:, -200:], few, 2 * ref.matmul_bound(size, k), "one row")
+
+
+def test_distill_offsets_past_32_bits(rvq, dev):
+    n, V = 66000, 65536
+    x = torch.zeros((n, V), dtype=BF16, device=dev)
+    tail = _randn((3, V), 7, dev, BF16, 2.0)
+    x[-3:] = tail
+    ids = torch.arange(8, device=dev).repeat(n, 1).int() * 8191
+    t = torch.full((n, 8), -3.0, device=dev)
+    for with_tail in (False, True):
+        got = rvq.rvq_distill_loss(x, ids, t, tail=with_tail)
+        few = rvq.rvq_distill_loss(tail, ids[-3:], t[-3:], tail=with_tail)
+        assert torch.equal(got.loss[-3:], few.loss) and torch.equal(got.stats[-3:], few.stats)
+    w = torch.zeros(n, device=dev)
+    w[-2] = 1.0
+    small = rvq.rvq_distill_loss_backward(tail, ids[-3:], t[-3:], few.stats, w[-3:], tail=True)
+    d = rvq.rvq_distill_loss_backward(x, ids, t, got.stats, w, tail=True, out=x)
+    assert torch.equal(d[-3:], small) and float(d[:-3:997].float().abs().sum()) == 0.0
+
+
+@pytest.mark.parametrize("V", [7, 300, 2048, 5001, 65536])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_logits_that_begin_at_any_element(rvq, dev, V, dtype):
+    n = 9
+    k = min(V, 6)
+    buf = _randn(n * V + 1, V, dev, dtype, 2.0)
+    x = buf[1:].view(n, V)
+    y = x.clone()
+    ids = (torch.arange(n, device=dev) * 31 % V).int()
+    tids = torch.stack([torch.arange(k, device=dev)] * n).int()
+    t = _randn((n, k), 3, dev)
+    one = torch.ones(n, device=dev)
+    a, b = rvq.rvq_token_logprobs(x, ids, top=k), rvq.rvq_token_logprobs(y, ids, top=k)
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+    out = torch.empty(n * V + 1, dtype=dtype, device=dev)[1:].view(n, V)
+    d = rvq.rvq_token_logprobs_backward(x, ids, a.stats, one, a.entropy, one, out=out)
+    assert torch.equal(d, rvq.rvq_token_logprobs_backward(y, ids, a.stats, one, a.entropy, one))
+    for tail in (False, True):
+        c, e = rvq.rvq_distill_loss(x, tids, t - 4, 1.0, tail), rvq.rvq_distill_loss(y, tids, t - 4, 1.0, tail)
+        assert torch.equal(c.loss, e.loss)
+        d = rvq.rvq_distill_loss_backward(x, tids, t - 4, c.stats, one, 1.0, tail, out=out)
+        assert torch.equal(d, rvq.rvq_distill_loss_backward(y, tids, t - 4, e.stats, one, 1.0, tail))
+
+
+def test_outputs_end_where_they_end(rvq, dev):
+    # guards of 64 elements on both sides of every output, by the C calls
+    lib = rvq.raw_library()
+    g = lambda n, dt=F32: torch.full((n + 128,), 7.0, device=dev).to(dt)  # noqa: E731
+    at = lambda t: t.data_ptr() + 64 * t.element_size()  # noqa: E731
+
+    def intact(*ts):
+        torch.cuda.synchronize()
+        for t in ts:
+            assert torch.all(t[:64].float() == 7.0) and torch.all(t[-64:].float() == 7.0)
+            assert bool((t[64:-64].float() != 7.0).any())
+    for n, V, top, k in ((5, 37, 3, 4), (3, 3001, 5, 9), (2, 20001, 6, 17), (1, 70001, 20, 3)):
+        x = _randn((n, V), V, dev, BF16)
+        ids = torch.zeros(n, dtype=torch.int32, device=dev)
+        lp, ent, st, tl = g(n), g(n), g(2 * n), g(n * top)
+        ti = torch.full((n * top + 128,), 7, dtype=torch.int32, device=dev)
+        nb = rvq.rvq_token_logprobs_workspace_size(n, V, top)
+        ws = torch.full((nb + 256,), 0x55, dtype=torch.uint8, device=dev)
+        s = lib.rvq_token_logprobs(x.data_ptr(), 1, n, V, ids.data_ptr(), 1.0, at(lp), at(ent), at(st), top, at(tl), at(ti), None,
+                                   ws.data_ptr(), nb, None)
+        assert s == 0
+        intact(lp, ent, st, tl, ti)
+        assert torch.all(ws[nb:] == 0x55)
+        one = torch.ones(n, device=dev)
+        dx = g(n * V, BF16)
+        assert lib.rvq_token_logprobs_backward(x.data_ptr(), 1, n, V, ids.data_ptr(), 1.0, at(st), one.data_ptr(), at(ent), one.data_ptr(),
+                                               at(dx), None) == 0
+        intact(dx)
+        tids = torch.arange(k, device=dev).repeat(n, 1).int()
+        t = _randn((n, k), 3, dev) - 5
+        for tail in (0, 1):
+            loss, st4, dx = g(n), g(4 * n), g(n * V, BF16)
+            assert lib.rvq_distill_loss(x.data_ptr(), 1, n, V, tids.data_ptr(), t.data_ptr(), k, tail, 1.0, at(loss), at(st4), None, None) == 0
+            assert lib.rvq_distill_loss_backward(x.data_ptr(), 1, n, V, tids.data_ptr(), t.data_ptr(), k, tail, 1.0, at(st4), one.data_ptr(),
+                                                 at(dx), None) == 0
+            intact(loss, st4, dx)
+    for m, n, k in ((1, 50, 200), (3, 1000, 130), (300, 270, 640), (1000, 1100, 256), (1001, 1099, 300), (2561, 4199, 129)):
+        for odt, code in ((F32, 0), (BF16, 1)):
+            a, sa = rvq.rvq_quantize_f8(_randn((m, k), 1, dev))
+            b, sb = rvq.rvq_quantize_f8(_randn((n, k), 2, dev), 128)
+            out = g(m * n, odt)
+            assert lib.rvq_matmul_f8(a.data_ptr(), a.stride(0), sa.data_ptr(), 1, b.data_ptr(), b.stride(0), sb.data_ptr(), 2, m, n, k, at(out),
+                                     code, None) == 0
+            intact(out)
+    for n, d in ((3, 5), (7, 100), (9, 1155), (300, 4096), (2, 20001)):
+        x = _randn((n, d), d, dev, BF16)
+        y, mean, rstd, dx, dw, db = g(n * d, BF16), g(n), g(n), g(n * d, BF16), g(d), g(d)
+        assert lib.rvq_layer_norm(x.data_ptr(), None, 1, n, d, None, None, 0, 1e-6, None, at(y), 1, None, at(mean), at(rstd), None) == 0
+        nb = rvq.rvq_layer_norm_backward_workspace_size(n, d)
+        ws = torch.full((nb + 256,), 0x55, dtype=torch.uint8, device=dev)
+        assert lib.rvq_layer_norm_backward(x.data_ptr(), x.data_ptr(), 1, n, d, at(mean), at(rstd), None, 0, None, at(dx), at(dw), at(db),
+                                           ws.data_ptr(), nb, None) == 0
+        intact(y, mean, rstd, dx, dw, db)
+        assert torch.all(ws[nb:] == 0x55)
+        for block, tr in ((1, 0), (128, 0), (1, 1), (128, 1)):
+            r, c = (d, n) if tr else (n, d)
+            q = torch.full((r * c + 128,), 0x55, dtype=torch.uint8, device=dev)
+            sc = g((r if block == 1 else -(-r // 128)) * -(-c // 128))
+            assert lib.rvq_quantize_f8(x.data_ptr(), 1, n, d, 1 if block == 1 else 2, tr, at(q), c, at(sc), None) == 0
+            torch.cuda.synchronize()
+            assert torch.all(q[:64] == 0x55) and torch.all(q[-64:] == 0x55)
+            intact(sc)
+
+
+def test_rows_do_not_depend_on_their_neighbours(rvq, dev):
+    # each row of a batch as if it were in any other batch of the same number of rows
+    V = 3000
+    x = _randn((600, V), 1, dev, BF16, 3.0)
+    ids = torch.arange(600, device=dev).int()
+    perm = torch.randperm(600, generator=torch.Generator(device=dev).manual_seed(2), device=dev)
+    a, b = rvq.rvq_token_logprobs(x, ids, top=9), rvq.rvq_token_logprobs(x[perm], ids[perm], top=9)
+    for u, v in zip(a, b):
+        assert torch.equal(u[perm], v)
+    y, z = rvq.rvq_layer_norm(x, need_stats=True), rvq.rvq_layer_norm(x[perm], need_stats=True)
+    assert torch.equal(y.y[perm], z.y) and torch.equal(y.mean[perm], z.mean) and torch.equal(y.rstd[perm], z.rstd)
+    q, s = rvq.rvq_quantize_f8(x)
+    w, sw = rvq.rvq_quantize_f8(_randn((700, V), 3, dev), 128)
+    for odt in (F32, BF16):
+        c = rvq.rvq_matmul_f8(q, s, w, sw, out_dtype=odt)
+        d = rvq.rvq_matmul_f8(q[perm], s[perm], w, sw, out_dtype=odt)
+        assert torch.equal(c[perm], d)
