@@ -399,7 +399,15 @@ hipError_t launch_layer_norm(const LayerNormArgs &a, bool x_bf16, hipStream_t s)
 
 namespace {
 
-constexpr int kMaxParts = 1024;
+// Workgroups of a launch, and with them the parts: three a CU, which are at work at once
+// with most shapes' registers (277,777 x 1152 bf16 476 us, 621 with four; 78,125 x 4096 459 and
+// 474; 39,062 x 4096 fp32 464 and 541; the other way round 138,888 x 1152 fp32 501 and
+// 488).  Four of the widest, which two or one a CU are at work on (52,083 x 6144 bf16 480, 564
+// with three; without parameters, where it is three, 564 and 458).
+int most_at_once(const Shape &sh, int piece, bool params) {
+  const int values = sh.p * piece;
+  return values < 32 || (values == 32 && piece == 8 && !params) ? 768 : 1024;
+}
 constexpr int kWideParts = 256;
 
 }  // namespace
@@ -410,7 +418,8 @@ int64_t layer_norm_grad_parts(int64_t n, int d, bool bf16) {
   if (!sh.w) return n < kWideParts ? n : kWideParts;
   // two rows in turn before there are as many workgroups as the device holds
   const int64_t groups = ceil_div(n, 2 * (kThreads / sh.w));
-  return groups < kMaxParts ? groups : kMaxParts;
+  const int most = most_at_once(sh, bf16 ? kPiece<uint16_t> : kPiece<float>, true);
+  return groups < most ? groups : most;
 }
 
 template <typename T, int W, int P, bool DW>
@@ -593,7 +602,8 @@ static hipError_t layer_norm_grad_rows(const LayerNormGradArgs &a, hipStream_t s
       layer_norm_grad_wide_kernel<T>
           <<<dim3((unsigned)(a.n < kMaxGroups ? a.n : kMaxGroups)), kThreads, 0, s>>>(a);
   }
-  const dim3 grid((unsigned)parts);
+  const int64_t most = most_at_once(sh, kPiece<T>, params);
+  const dim3 grid((unsigned)(params || parts < most ? parts : most));
 #define RVQ_NORM(W, P)                                                                    \
   if (a.n > 0 && sh.w == W && sh.p == P) {                                                \
     if (params)                                                                           \

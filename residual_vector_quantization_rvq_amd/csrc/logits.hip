@@ -69,55 +69,106 @@ __device__ __forceinline__ void add_values(const float (&v)[N], float c, Sums &s
   if (ENT) s.q += (q[0] + q[1]) + (q[2] + q[3]);
 }
 
+// P pieces of a row, W pieces apart, the first at column `at`.  With BITS, columns whose
+// bit is set in `bits` are left out.  At a row's end (TAIL) the last N columns are read
+// in place of a piece that goes past them, and what an earlier piece holds is left
+// out: no load waits for a branch.  (Rows of N columns or more; `bits` has a byte more.)
+template <typename T, int W, int P, bool ENT, bool BITS, bool TAIL>
+__device__ __forceinline__ void stream_pieces(const T *row, int cols, int at, float c, const uint8_t *bits, Sums &s) {
+  constexpr int N = kPiece<T>;
+  u32x4 raw[P];
+  int from[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    from[p] = at + p * W * N;
+    if (TAIL) from[p] = min(from[p], cols - N);
+    raw[p] = load16(row + from[p]);
+  }
+  float v[P * N];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    float u[N];
+    unpack(raw[p], u);
+    uint32_t out = 0;  // a bit for each column that is left out
+    if constexpr (BITS) {
+      out = bits[from[p] >> 3];
+      if (TAIL) out |= (uint32_t)bits[(from[p] >> 3) + 1] << 8;
+      if (TAIL || N == 4) out >>= from[p] & 7;
+    }
+    if (TAIL) out |= (1u << min(at + p * W * N - from[p], N)) - 1;
+    if (TAIL || BITS) {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (out >> e & 1) u[e] = -INFINITY;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[p * N + e] = u[e];
+  }
+  add_values<P * N, ENT>(v, c, s);
+}
+
 // The values of columns [0, cols) of a row that are this thread's: pieces lane,
-// lane + W, ...  With BITS, columns whose bit is set in `bits` are left out.
-template <typename T, int W, bool ENT, bool BITS>
+// lane + W, ...  ONE_SUM: inner pieces and a row's end are summed by the same instructions;
+// beside the search for the top alternatives that is faster (16,384 x 65,536 bf16 400 us, 450
+// with a sum for each), without it slower (16,384 x 2,049 bf16 35 us, 17 with a sum for each).
+template <typename T, int W, bool ENT, bool BITS, bool ONE_SUM>
 __device__ __forceinline__ void stream_row(const T *row, int cols, int lane, float c, const uint8_t *bits, Sums &s) {
   constexpr int N = kPiece<T>, P = kPieces;
-  for (int base = 0; base < cols; base += W * P * N) {
-    float v[P * N];
-    const int at = base + lane * N;
-    if (base + W * P * N <= cols) {
-      u32x4 raw[P];
-#pragma unroll
-      for (int p = 0; p < P; ++p) raw[p] = load16(row + at + p * W * N);
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float u[N];
-        unpack(raw[p], u);
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[p * N + e] = u[e];
-      }
-    } else {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float u[N];
-        load_values(row, at + p * W * N, cols - (at + p * W * N), u);
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[p * N + e] = u[e];
-      }
-    }
+  if (cols < N) {
+    float v[N];
+    load_values(row, lane * N, cols - lane * N, v);
     if constexpr (BITS) {
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int i = at + p * W * N;
-        uint32_t b = i < cols ? bits[i >> 3] : 0;
-        if (N == 4) b >>= i & 4;
-        if (b & ((1u << N) - 1)) {
+      for (int e = 0; e < N; ++e)
+        if (bits[0] >> e & 1) v[e] = -INFINITY;
+    }
+    add_values<N, ENT>(v, c, s);
+    return;
+  }
+  if constexpr (ONE_SUM) {
+    for (int base = 0; base < cols; base += W * P * N) {
+      float v[P * N];
+      const int at = base + lane * N;
+      if (base + W * P * N <= cols) {
+        u32x4 raw[P];
 #pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (b >> e & 1) v[p * N + e] = -INFINITY;
+        for (int p = 0; p < P; ++p) raw[p] = load16(row + at + p * W * N);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          float u[N];
+          unpack(raw[p], u);
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[p * N + e] = u[e];
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          float u[N];
+          load_values(row, at + p * W * N, cols - (at + p * W * N), u);
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[p * N + e] = u[e];
         }
       }
+      add_values<P * N, ENT>(v, c, s);
     }
-    add_values<P * N, ENT>(v, c, s);
+    return;
+  }
+  int base = 0;
+  for (; base + W * P * N <= cols; base += W * P * N)
+    stream_pieces<T, W, P, ENT, BITS, false>(row, cols, base + lane * N, c, bits, s);
+  if (cols - base > 2 * W * N) {
+    stream_pieces<T, W, P, ENT, BITS, true>(row, cols, base + lane * N, c, bits, s);
+  } else if (cols - base > W * N) {
+    stream_pieces<T, W, 2, ENT, BITS, true>(row, cols, base + lane * N, c, bits, s);
+  } else if (base < cols) {
+    stream_pieces<T, W, 1, ENT, BITS, true>(row, cols, base + lane * N, c, bits, s);
   }
 }
 
-// ---- over the W threads of a row; W == 64: a wave, else the whole workgroup ----
+// ---- over the W threads of a row; W > 64: the whole workgroup ----
 template <int W>
 __device__ __forceinline__ float all_max(float v, float *red) {
-  v = lane_max<64>(v);
+  v = lane_max<W < 64 ? W : 64>(v);
   if constexpr (W > 64) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -131,10 +182,10 @@ __device__ __forceinline__ float all_max(float v, float *red) {
 template <int W, typename F>
 __device__ __forceinline__ F all_sum(F v, F *red) {
   if constexpr (sizeof(F) == 4) {
-    v = lane_sum<64>(v);
+    v = lane_sum<W < 64 ? W : 64>(v);
   } else {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+    for (int off = (W < 64 ? W : 64) / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
   }
   if constexpr (W > 64) {
     __syncthreads();
@@ -149,8 +200,8 @@ __device__ __forceinline__ F all_sum(F v, F *red) {
 // two at once; `red` holds 2 W / 64
 template <int W>
 __device__ __forceinline__ void all_sum2(float &a, float &b, float *red) {
-  a = lane_sum<64>(a);
-  b = lane_sum<64>(b);
+  a = lane_sum<W < 64 ? W : 64>(a);
+  b = lane_sum<W < 64 ? W : 64>(b);
   if constexpr (W > 64) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) {
@@ -171,7 +222,7 @@ __device__ __forceinline__ void all_sum2(float &a, float &b, float *red) {
 template <int W>
 __device__ __forceinline__ int all_min(int v, int *red) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = min(v, __shfl_xor(v, off, 64));
+  for (int off = (W < 64 ? W : 64) / 2; off >= 1; off >>= 1) v = min(v, __shfl_xor(v, off, 64));
   if constexpr (W > 64) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -357,21 +408,26 @@ __device__ __forceinline__ float log_prob(float x, float m, float log_s, float i
   return -((m - x) * inv_t) - log_s;
 }
 
+// The given token of a row and its value.
+struct Given {
+  int id;  // -1: none
+  float x;
+};
 template <typename T>
-__device__ void finish_row(const LogprobArgs &a, int64_t row, float m, float rest, float q) {
+__device__ __forceinline__ Given given_of(const LogprobArgs &a, int64_t row, int id, bool report) {
+  if (id < 0 || id >= a.V) {
+    if (report && id != -1 && a.bad) atomicAdd(a.bad, 1u);
+    return {-1, 0.f};
+  }
+  return {id, load_f32((const T *)a.x, row * a.V + id)};
+}
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, int64_t row, const Given &given, float m, float rest,
+                                           float q) {
   const float log_s = log_sum(m, rest);
   a.stats[2 * row] = m;
   a.stats[2 * row + 1] = log_s;
   if (a.entropy) a.entropy[row] = m == -INFINITY && !(log_s != log_s) ? 0.f : log_s + q * kLn2 / (1.f + rest);
-  if (a.ids) {
-    const int id = a.ids[row];
-    float lp = 0.f;
-    if (id >= 0 && id < a.V)
-      lp = log_prob(load_f32((const T *)a.x, row * a.V + id), m, log_s, a.inv_t);
-    else if (id != -1 && a.bad)
-      atomicAdd(a.bad, 1u);
-    a.logprob[row] = lp;
-  }
+  if (a.ids) a.logprob[row] = given.id >= 0 ? log_prob(given.x, m, log_s, a.inv_t) : 0.f;
 }
 __device__ __forceinline__ void finish_top(const LogprobArgs &a, int64_t row, int i, uint64_t key, float m,
                                            float log_s) {
@@ -403,13 +459,19 @@ __global__ __launch_bounds__(256, 6) void logprob_kernel(LogprobArgs a, LogprobP
     const int64_t c0 = (job - row * plan.slices) * plan.slice;
     const int cols = (int)(a.V - c0 < plan.slice ? a.V - c0 : plan.slice);
     const T *x = (const T *)a.x + row * a.V + c0;
+    const int id = !TOP && a.ids && plan.slices == 1 ? a.ids[row] : -1;
     Sums s = {-INFINITY, 0.f, 0.f};
-    stream_row<T, W, ENT, false>(x, cols, lane, c, nullptr, s);
+    stream_row<T, W, ENT, false, TOP>(x, cols, lane, c, nullptr, s);
+    Given given = {-1, 0.f};
+    if (!TOP) given = given_of<T>(a, row, id, lane == 0);  // comes while the sums are joined
     const Sums all = join_threads<W, ENT>(s, c, red);
     const float rest = rest_of<T, W>(x, cols, lane, c, s, all, red);
     if constexpr (TOP) top_of_row<T>(x, cols, s.m, a.top, tmax, cand, count, best);
     if (plan.slices == 1) {
-      if (lane == 0) finish_row<T>(a, row, all.m, rest, all.q);
+      if (lane == 0) {
+        if (TOP && a.ids) given = given_of<T>(a, row, a.ids[row], true);
+        finish_row(a, row, given, all.m, rest, all.q);
+      }
       if constexpr (TOP) {
         const float log_s = log_sum(all.m, rest);
         for (int i = lane; i < a.top; i += W) finish_top(a, row, i, best[i], all.m, log_s);
@@ -465,7 +527,7 @@ __global__ __launch_bounds__(kTopThreads) void logprob_join_kernel(LogprobArgs a
     all_sum2<64>(r, qq, nullptr);
     if (top == -INFINITY && !(r != r)) r = -1.f;
     if (i == 0) {
-      finish_row<T>(a, row, top, r, qq);
+      finish_row(a, row, given_of<T>(a, row, a.ids ? a.ids[row] : -1, true), top, r, qq);
       got[0] = top;
       got[1] = log_sum(top, r);
     }
@@ -518,9 +580,19 @@ static void start_logprobs(const LogprobArgs &a, const LogprobPlan &plan, hipStr
 template <typename T>
 static hipError_t logprobs(const LogprobArgs &a, hipStream_t s) {
   const LogprobPlan plan = logprob_plan(a.n, a.V, a.top);
+  // Threads of a row.  Of short rows what is done once a row weighs most, and a wave does it
+  // for four rows as for one: 1,024 bf16 columns of 293,000 rows 112 us with 16 threads, 139
+  // with 32, 189 with 64; 2,048 of 146,000 113, 117, 137, but of 6,144 10.0 and 9.1 with 64.  A
+  // workgroup for a row of 2,049 takes 311 where a wave takes 163; of 24,576 rows of 8,192
+  // 91 where a wave takes 80, but fp32 rows of 4,096 79 where that takes 83, and 512 rows of
+  // 4,096 4.6 where that takes 5.2.  The top alternatives are picked by a workgroup.
+  const int64_t bytes = (int64_t)a.V * sizeof(T);
+  constexpr bool narrow = sizeof(T) == 2;
   if (a.top > 0)
     start_logprobs<T, 256, true>(a, plan, s);
-  else if (a.V <= 2048)
+  else if (bytes <= 2048 || (narrow && bytes <= 4096 && a.n >= 16384))
+    start_logprobs<T, 16, false>(a, plan, s);
+  else if (bytes <= 4096 || (bytes <= (narrow ? 16384 : 12288) && a.n >= 2048))
     start_logprobs<T, 64, false>(a, plan, s);
   else
     start_logprobs<T, 256, false>(a, plan, s);
@@ -541,28 +613,53 @@ __device__ __forceinline__ void zero_row(T *dx, int cols, int lane) {
   const float v[N] = {};
   for (int i = lane * N; i < cols; i += W * N) store_n<N>(dx + i, cols - i, v);
 }
-// dx = f(x) for a lane's pieces of a row; dx may be x
+// dx = f(x) for a thread's pieces of a row; dx may be x.  At the row's end as above: what
+// is read twice is written by the piece that it belongs to, out of that piece's own load.
+template <typename T, int W, int P, bool TAIL, typename F>
+__device__ __forceinline__ void map_pieces(const T *x, T *dx, int cols, int at, F f) {
+  constexpr int N = kPiece<T>;
+  u32x4 raw[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int i = at + p * W * N;
+    raw[p] = load16(x + (TAIL ? min(i, cols - N) : i));
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int i = at + p * W * N;
+    if (TAIL && i >= cols) break;
+    float v[N];
+    unpack(raw[p], v);
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = f(v[e]);
+    if (!TAIL || i + N <= cols) {
+      store_n<N>(dx + i, N, v);
+    } else {
+#pragma unroll
+      for (int e = 1; e < N; ++e)
+        if (cols - N + e >= i) store_f32(dx, cols - N + e, v[e]);
+    }
+  }
+}
 template <typename T, int W, typename F>
 __device__ __forceinline__ void map_row(const T *x, T *dx, int cols, int lane, F f) {
   constexpr int N = kPiece<T>, P = kPieces;
-  for (int base = lane * N; base < cols; base += W * P * N) {
-    u32x4 raw[P];
+  if (cols < N) {
+    if (lane > 0) return;
+    float v[N];
+    unpack(load_piece(x, cols), v);
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int i = base + p * W * N;
-      raw[p] = load_piece(x + (i < cols ? i : 0), cols - i);
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int i = base + p * W * N;
-      if (i >= cols) break;
-      float v[N];
-      unpack(raw[p], v);
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = f(v[e]);
-      store_n<N>(dx + i, cols - i, v);
-    }
+    for (int e = 0; e < N; ++e) v[e] = f(v[e]);
+    store_n<N>(dx, cols, v);
+    return;
   }
+  int base = 0;
+  for (; base + W * P * N <= cols; base += W * P * N)
+    map_pieces<T, W, P, false>(x, dx, cols, base + lane * N, f);
+  if (cols - base > 2 * W * N)
+    map_pieces<T, W, P, true>(x, dx, cols, base + lane * N, f);
+  else if (base < cols)
+    map_pieces<T, W, 2, true>(x, dx, cols, base + lane * N, f);
 }
 
 }  // namespace
@@ -623,15 +720,22 @@ static hipError_t logprobs_grad(const LogprobGradArgs &a, hipStream_t s) {
   }
   const int64_t slice = round_up(ceil_div(a.V, slices), 8);
   slices = ceil_div(a.V, slice);
-  if (slices == 1 && a.V <= 2048) {
-    const int64_t groups = ceil_div(a.n, 4);
-    logprob_grad_kernel<T, 64>
-        <<<dim3((unsigned)(groups < kMaxGroups ? groups : kMaxGroups)), 256, 0, s>>>(a, 1, slice);
-  } else {
-    const int64_t groups = a.n * slices;
-    logprob_grad_kernel<T, 256>
-        <<<dim3((unsigned)(groups < kMaxGroups ? groups : kMaxGroups)), 256, 0, s>>>(a, (int)slices, slice);
-  }
+  const auto grid = [&](int rows) {
+    const int64_t groups = ceil_div(a.n * slices, rows);
+    return dim3((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
+  };
+  // Threads of a row, four pieces each: 512 bf16 columns of 586,000 rows 201 us with 16
+  // threads, 251 with 32; 1,024 of 293,000 199 with 32, 224 with 16, 246 with 64; 4,096 of 73,000 218 with
+  // 64, 234 with a workgroup, which takes 200 for 8,192 of 36,600 where a wave takes 225.
+  const int64_t bytes = (int64_t)a.V * sizeof(T);
+  if (slices == 1 && bytes <= 1024)
+    logprob_grad_kernel<T, 16><<<grid(16), 256, 0, s>>>(a, 1, slice);
+  else if (slices == 1 && bytes <= 2048)
+    logprob_grad_kernel<T, 32><<<grid(8), 256, 0, s>>>(a, 1, slice);
+  else if (slices == 1 && (bytes <= 4096 || (bytes <= 8192 && a.n >= 2048)))
+    logprob_grad_kernel<T, 64><<<grid(4), 256, 0, s>>>(a, 1, slice);
+  else
+    logprob_grad_kernel<T, 256><<<grid(1), 256, 0, s>>>(a, (int)slices, slice);
   return hipGetLastError();
 }
 
@@ -734,10 +838,10 @@ __global__ __launch_bounds__(256, 4) void distill_kernel(DistillArgs a, int word
         row_barrier<W>();
         if (en.id >= c0 && en.id < c0 + cols) atomicOr(map + ((en.id - (int)c0) >> 5), 1u << (en.id & 31));
         row_barrier<W>();
-        stream_row<T, W, false, true>(x + c0, cols, lane, c, (const uint8_t *)map, s);
+        stream_row<T, W, false, true, false>(x + c0, cols, lane, c, (const uint8_t *)map, s);
       }
     } else {
-      stream_row<T, W, false, false>(x, a.V, lane, c, nullptr, s);
+      stream_row<T, W, false, false, false>(x, a.V, lane, c, nullptr, s);
     }
     const Sums others = join_threads<W, false>(s, c, (float *)red);  // without tail: all tokens
     float m = others.m, S = others.t;
@@ -825,7 +929,7 @@ static void start_distill(const DistillArgs &a, bool grad, hipStream_t s) {
   if (grad) {
     distill_grad_kernel<T, W><<<grid, 256, 0, s>>>(a);
   } else if (a.tail) {
-    const int words = (int)ceil_div(a.V < kSegment ? a.V : kSegment, 32);
+    const int words = (int)ceil_div(a.V < kSegment ? a.V : kSegment, 32) + 1;
     distill_kernel<T, W, true><<<grid, 256, (size_t)R * words * 4, s>>>(a, words);
   } else {
     distill_kernel<T, W, false><<<grid, 256, 0, s>>>(a, 0);
@@ -836,7 +940,7 @@ template <typename T>
 static hipError_t distill(const DistillArgs &a, bool grad, hipStream_t s) {
   // at least as many threads as the teacher has entries
   static_assert(kMaxTeacher <= 256, "a thread each");
-  if (a.V <= 2048 && a.k <= 64)
+  if (a.k <= 64 && (a.V <= 2048 || (a.V * sizeof(T) <= (grad ? 12288 : 65536) && a.n >= 2048)))
     start_distill<T, 64>(a, grad, s);
   else
     start_distill<T, 256>(a, grad, s);
