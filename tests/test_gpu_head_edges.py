@@ -1,5 +1,7 @@
 """Edges of the calls for a model's head: memory past 32-bit offsets, buffers that begin
 at any element, rows left as they were, results that do not depend on what stands beside."""
+import math
+
 import pytest
 import torch
 
@@ -197,3 +199,82 @@ def test_rows_do_not_depend_on_their_neighbours(rvq, dev):
         c = rvq.rvq_matmul_f8(q, s, w, sw, out_dtype=odt)
         d = rvq.rvq_matmul_f8(q[perm], s[perm], w, sw, out_dtype=odt)
         assert torch.equal(c[perm], d)
+
+
+# Rows are shared by 16, 32 or 64 threads or a workgroup, by their length and, of some
+# lengths, by their number; a row's last values come with the ones before them.
+MANY = [(16500, 1025), (16400, 2047), (16384, 1024), (4100, 513), (2100, 2049), (2048, 4097), (2049, 8191), (2048, 2999)]
+
+
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_many_short_rows(rvq, dev, shape, dtype):
+    n, V = shape
+    g = torch.Generator(device=dev).manual_seed(n + V)
+    x = (3 * torch.randn((n, V), generator=g, device=dev)).to(dtype)
+    x[5] = -math.inf
+    x[6, 1:] = torch.finfo(dtype).min
+    ids = torch.randint(-1, V, (n,), generator=g, device=dev).int()
+    w, wh = torch.randn(n, generator=g, device=dev), torch.randn(n, generator=g, device=dev)
+    tid = torch.stack([torch.randperm(V, generator=g, device=dev)[:9] for _ in range(16)]).int()[torch.arange(n, device=dev) % 16]
+    tv = torch.log_softmax(torch.randn((n, 10), generator=g, device=dev), 1)[:, :9].contiguous()
+
+    def all_of(x, rows):
+        a, b, c, d = (None if t is None else t[rows].contiguous() for t in (ids, tid, tv, w))
+        p = rvq.rvq_token_logprobs(x, a, 0.9)
+        out = [p.logprob, p.entropy, p.stats, rvq.rvq_token_logprobs_backward(x, a, p.stats, d, p.entropy, wh[rows], 0.9)]
+        for tail in (False, True):
+            q = rvq.rvq_distill_loss(x, b, c, 1.3, tail)
+            out += [q.loss, q.stats, rvq.rvq_distill_loss_backward(x, b, c, q.stats, d, 1.3, tail)]
+        return out
+
+    got = all_of(x, slice(None))
+    # the same rows, few at a time: other threads add the same numbers in another order.  A
+    # sum of V terms of one sign is off by (V / 1024 + 144) 2^-24 at most on either side (144:
+    # the chains, trees and exponentials of a term), the results by a few times that.
+    tol = 8 * (V / 1024 + 144) * 2.0 ** -24 + (2.0 ** -7 if dtype == BF16 else 0.0)
+    for r0 in (0, 4, n - 40):
+        rows = slice(r0, r0 + 40)
+        want = all_of(x[rows].contiguous(), rows)
+        for i, (a, b) in enumerate(zip(got, want)):
+            a, b = a[rows].double(), b.double()
+            fine = torch.isfinite(b)
+            assert torch.equal(a[~fine], b[~fine]), i
+            # results are differences of numbers up to 40; a row's gradient, of its largest element
+            scale = b[fine].abs() + (40.0 if a.dim() == 1 or i in (2, 5, 8) else w.abs().max().double() + 40 * wh.abs().max().double())
+            assert torch.all((a[fine] - b[fine]).abs() <= tol * scale), i
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_every_row_end(rvq, dev, dtype):
+    """Lengths around a piece and around a wave's pieces: by the rows' own softmax in 64 bits."""
+    g = torch.Generator(device=dev).manual_seed(5)
+    for V in [*range(1, 36), 127, 129, 255, 257, 511, 513, 1023, 1033, 2055, 4095, 4103]:
+        n = 37
+        x = torch.randn((n, V), generator=g, device=dev).to(dtype)
+        ids = torch.randint(0, V, (n,), generator=g, device=dev).int()
+        p = rvq.rvq_token_logprobs(x, ids)
+        lp = torch.log_softmax(x.double(), 1)
+        rows = torch.arange(n, device=dev)
+        # log probabilities below 16: (64 + 80) roundings of the sum and of its terms' exponents
+        tol = 16 * 144 * 2.0 ** -24
+        assert torch.all((p.logprob.double() - lp[rows, ids.long()]).abs() <= tol)
+        assert torch.all((p.entropy.double() + (lp.exp() * lp).sum(1)).abs() <= tol)
+        one = torch.ones(n, device=dev)
+        want = -lp.exp()
+        want[rows, ids.long()] += 1
+        half = 2.0 ** -8 if dtype == BF16 else 0.0
+        for place in (None, x.clone()):
+            y = x if place is None else place
+            d = rvq.rvq_token_logprobs_backward(y, ids, p.stats, one, out=place)
+            assert torch.all((d.double() - want).abs() <= tol + half * want.abs())
+        k = min(V, 3)
+        tid = torch.argsort(torch.rand((n, V), generator=g, device=dev), 1)[:, :k].int().contiguous()
+        tv = torch.log_softmax(torch.randn((n, k + 1), generator=g, device=dev), 1)[:, :k].contiguous()
+        if V > k:
+            q = rvq.rvq_distill_loss(x, tid, tv, 1.0, True)
+            mine = lp.gather(1, tid.long())
+            rest = torch.log((lp.exp().sum(1) - mine.exp().sum(1)).clamp(min=1e-300))
+            qt = 1 - tv.double().exp().sum(1)
+            loss = (tv.double().exp() * (tv.double() - mine)).sum(1) + qt * (qt.log() - rest)
+            assert torch.all((q.loss.double() - loss).abs() <= tol)
