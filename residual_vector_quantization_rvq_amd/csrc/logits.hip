@@ -313,6 +313,7 @@ __device__ __forceinline__ void rank_keys(const uint64_t *cand, int found, int t
   for (int i = threadIdx.x; i < found; i += kTopThreads) {
     const uint64_t key = cand[i];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < found; ++j) rank += cand[j] > key;
     if (rank < top) out[rank] = key;
   }
@@ -500,16 +501,18 @@ __global__ __launch_bounds__(kTopThreads) void logprob_join_kernel(LogprobArgs a
   const float *part = a.part + row * plan.slices * part_floats(a.top);
   const float c = a.inv_t * kLog2e;
   const int total = plan.slices * a.top;
-  for (int i = threadIdx.x; i < kMaxCand; i += kTopThreads) {
-    const int slice = i < total ? i / a.top : 0;
-    cand[i] = i < total ? ((const uint64_t *)(part + slice * part_floats(a.top) + 4))[i - slice * a.top] : 0;
+  // the first wave's part is on its way before the keys are
+  const int i = threadIdx.x;
+  const bool in = i < plan.slices && i < 64;
+  const float *p = part + (in ? i : 0) * part_floats(a.top);
+  const float m = in ? p[0] : -INFINITY, rest = in ? p[1] : -1.f, q = in ? p[2] : 0.f;
+  const Given given = i == 0 ? given_of<T>(a, row, a.ids ? a.ids[row] : -1, true) : Given{-1, 0.f};
+  for (int i = threadIdx.x; i < total; i += kTopThreads) {
+    const int slice = i / a.top;
+    cand[i] = ((const uint64_t *)(part + slice * part_floats(a.top) + 4))[i - slice * a.top];
   }
   if (threadIdx.x == 0) count[0] = 0;
   if (threadIdx.x < 64) {
-    const int i = threadIdx.x;
-    const bool in = i < plan.slices;
-    const float *p = part + (in ? i : 0) * part_floats(a.top);
-    const float m = in ? p[0] : -INFINITY, rest = in ? p[1] : -1.f, q = in ? p[2] : 0.f;
     const float top = all_max<64>(m, nullptr);
     // a slice's whole sum, but for the first that holds the largest value
     const uint64_t holds = __ballot(m == top);
@@ -527,7 +530,7 @@ __global__ __launch_bounds__(kTopThreads) void logprob_join_kernel(LogprobArgs a
     all_sum2<64>(r, qq, nullptr);
     if (top == -INFINITY && !(r != r)) r = -1.f;
     if (i == 0) {
-      finish_row(a, row, given_of<T>(a, row, a.ids ? a.ids[row] : -1, true), top, r, qq);
+      finish_row(a, row, given, top, r, qq);
       got[0] = top;
       got[1] = log_sum(top, r);
     }
@@ -535,11 +538,13 @@ __global__ __launch_bounds__(kTopThreads) void logprob_join_kernel(LogprobArgs a
   if (a.top == 0) return;
   __syncthreads();
   if (threadIdx.x >= 64 && threadIdx.x < 128) {
-    uint32_t mine[kMaxCand / 64];
-#pragma unroll
-    for (int i = 0; i < kMaxCand / 64; ++i) mine[i] = (uint32_t)(cand[i * 64 + threadIdx.x - 64] >> 32);
-    const uint32_t bound = bound_of(mine, a.top);
-    if (threadIdx.x == 64) count[1] = (int)max(bound, kNoneBits + 1);
+    // A slice's keys are in order: where `of` slices have a key of the bound or more in place
+    // `deep`, at least `top` keys reach it.
+    const int deep = (a.top - 1) / plan.slices, of = (a.top + deep) / (deep + 1);
+    const int slice = threadIdx.x - 64;
+    const uint32_t mine[1] = {slice < plan.slices ? (uint32_t)(cand[slice * a.top + deep] >> 32) : 0};
+    const uint32_t bound = bound_of(mine, of);
+    if (slice == 0) count[1] = (int)max(bound, kNoneBits + 1);
   }
   __syncthreads();
   const uint32_t bound = (uint32_t)count[1];
