@@ -849,18 +849,30 @@ __global__ __launch_bounds__(256, 4) void distill_kernel(DistillArgs a, int word
       stream_row<T, W, false, false, false>(x, a.V, lane, c, nullptr, s);
     }
     const Sums others = join_threads<W, false>(s, c, (float *)red);  // without tail: all tokens
-    float m = others.m, S = others.t;
-    if (TAIL) {
+    // log S out of the sum without one of its largest terms, in 64 bits: where student and teacher
+    // are all but certain, the loss is the difference of such small numbers.
+    const double inv_t = (double)a.inv_t;
+    float m = others.m;
+    double rest_s, log_s;
+    bool empty;
+    if constexpr (TAIL) {
       m = fmaxf(m, all_max<W>(xe, (float *)red));
-      float t = xe > -INFINITY || xe != xe ? exp2_neg((m - xe) * c) : 0.f;
-      t = all_sum<W>(t, (float *)red);
-      S = t + (others.t == 0.f ? 0.f : others.t * exp2_neg(fminf((m - others.m) * c, kFar)));
-      if (m == INFINITY) S = NAN;
+      const int owner = all_min<W>(xe == m && m > -INFINITY ? lane : W, (int *)red);
+      double t = 0.0;
+      if (lane != owner && (xe > -INFINITY || xe != xe)) t = exp(((double)xe - (double)m) * inv_t);
+      rest_s = all_sum<W>(t, red);
+      if (!(others.t == 0.f)) rest_s += (double)others.t * exp(((double)others.m - (double)m) * inv_t);
+      empty = owner == W && rest_s == 0.0;
+      log_s = owner < W ? log1p(rest_s) : log(rest_s);
+      if (m == INFINITY) log_s = NAN;
+    } else {
+      const float rest = rest_of<T, W>(x, a.V, lane, c, s, others, (float *)red);
+      empty = others.t == 0.f;
+      log_s = log1p((double)rest);
     }
-    const double log_s = log((double)S);
     double term = 0.0;
     if (en.id >= 0 && en.q != 0.0) {  // NaN goes on
-      const double log_p = ((double)xe - (double)m) * (double)a.inv_t - log_s;
+      const double log_p = ((double)xe - (double)m) * inv_t - log_s;
       term = en.q * (en.logq - log_p);
     }
     const double any = all_sum<W>(en.id >= 0 ? 1.0 : 0.0, red);
@@ -878,13 +890,13 @@ __global__ __launch_bounds__(256, 4) void distill_kernel(DistillArgs a, int word
           factor = 0.0;
         } else {
           // by the others' own largest value: p_T may be too small for fp32
-          const double down = ((double)others.m - (double)m) * (double)a.inv_t - log_s;
+          const double down = ((double)others.m - (double)m) * inv_t - log_s;
           if (rest != 0.0) loss += rest * (log(rest) - (down + log((double)others.t)));
           from = others.m;
           factor = exp(down) - rest / (double)others.t;
         }
       }
-      const bool masked = m == -INFINITY && S == 0.f;  // no token to put weight on
+      const bool masked = m == -INFINITY && empty;  // no token to put weight on
       const bool none = any == 0.0;
       a.loss[row] = none ? 0.f : masked ? INFINITY : (float)loss;
       float *st = a.stats + 4 * row;

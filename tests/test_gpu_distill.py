@@ -187,3 +187,68 @@ def test_refusals(rvq, dev):
             rvq.rvq_distill_loss_backward(**{**ok, **bad})
     e = rvq.rvq_distill_loss(x[:0], ids[:0], t[:0])
     assert e.loss.shape == (0,) and rvq.rvq_distill_loss_backward(x[:0], ids[:0], t[:0], e.stats, one[:0]).shape == (0, 32)
+
+
+@pytest.mark.parametrize("V", [17, 300, 5000, 70000])
+@pytest.mark.parametrize("tail", [False, True], ids=["top", "tail"])
+def test_certain_rows_keep_their_small_numbers(rvq, dev, V, tail):
+    """Student and teacher put all but 10^-3 to 10^-9 of their weight on one token: loss and
+    gradient are differences of such numbers, and as exact as these."""
+    g = torch.Generator(device=dev).manual_seed(V)
+    n, k = 24, min(9, V - 3)
+    x = torch.randn((n, V), generator=g, device=dev)
+    x[:, 3] = torch.linspace(16.0, 30.0, n, device=dev)
+    t = x + torch.randn((n, V), generator=g, device=dev)
+    z = t.double() if not tail else torch.log_softmax(t.double(), 1)
+    if tail:
+        # log q of the token itself, as log1p of what the others have
+        e = torch.exp(t.double() - t.double()[:, 3:4])
+        e[:, 3] = 0
+        z[:, 3] = -torch.log1p(e.sum(1))
+    _, ids = torch.topk(t, k, dim=1)
+    v = z.gather(1, ids).float()
+    # 64 bits have numbers just below 1 in steps of 2^-53: p and q of token 3 and 1 - sum q
+    # (k + 2 roundings) are off by that on either side, whatever is left of them.
+    last = 2 * (k + 2) * 2.0 ** -53
+    if tail:
+        assert torch.all(1 - v.double().exp().sum(1) > 8 * last)
+    ids = ids.int()
+    w = torch.rand(n, generator=g, device=dev) + 0.5
+    got = rvq.rvq_distill_loss(x, ids, v, 1.0, tail)
+    d = rvq.rvq_distill_loss_backward(x, ids, v, got.stats, w, 1.0, tail)
+
+    at = ids.long()
+    y = x.double() - x.double()[:, 3:4]
+    e = torch.exp(y)
+    e[:, 3] = 0
+    others = e.sum(1)                                      # of weight 1 for token 3
+    logp = y - torch.log1p(others)[:, None]
+    p = logp.exp()
+    if tail:
+        logq = v.double()
+        rest = 1 - logq.exp().sum(1)
+        left = e.scatter(1, at, 0.0).sum(1)
+        p_rest = left / (1 + others)
+    else:
+        u = v.double() - v.double()[:, :1]
+        eu = torch.exp(u)
+        logq = u - torch.log1p(eu[:, 1:].sum(1))[:, None]
+    q = logq.exp()
+    mine = logp.gather(1, at)
+    loss = (q * (logq - mine)).sum(1)
+    grad = p.clone() if not tail else p * (1 - rest / p_rest)[:, None]
+    grad.scatter_(1, at, p.gather(1, at) - q)
+    if tail:
+        loss = loss + rest * (rest.log() - p_rest.log())
+    # What token 3 does not have: sums over it are off by 160 roundings (chains, trees) and a
+    # term's exponent below 40 by 3 each; a float32 log q or log p of it carries one more.
+    small = 1 - p[:, 3] + (1 - q[:, 0]) + 2.0 ** -52
+    tol = (160 + 3 * 40 + 8) * ref.U
+    off = 40 * (tol * small + last)                         # logarithms' factors: below 40
+    assert torch.all((got.loss.double() - loss).abs() <= off + ref.U * loss.abs())
+    want = grad * w.double()[:, None]
+    bound = w.double()[:, None] * (tol * (p + torch.zeros_like(p).scatter(1, at, q))) + 2 * ref.U * want.abs()
+    bound[:, 3] = w.double() * (tol * small + last) + 2 * ref.U * want[:, 3].abs()
+    if tail:
+        bound = bound + w.double()[:, None] * p * ((tol * rest + last) / p_rest)[:, None]
+    assert torch.all((d.double() - want).abs() <= bound)
