@@ -82,7 +82,7 @@ struct LogprobPlan {
   int slices;                   // workgroups per row
   int64_t slice;                // columns of each, a multiple of 8
 };
-LogprobPlan logprob_plan(int64_t n, int V, int top);
+LogprobPlan logprob_plan(int64_t n, int V, int top, bool bf16);
 size_t logprob_part_floats(int64_t n, const LogprobPlan &p, int top);
 hipError_t launch_logprobs(const LogprobArgs &a, bool x_bf16, hipStream_t s);
 

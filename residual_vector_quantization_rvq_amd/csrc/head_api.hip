@@ -218,7 +218,13 @@ rvq_status rvq_token_logprobs_workspace_size(int64_t n, int32_t V, int32_t top, 
   if (top < 0 || top > kMaxTop)
     return fail(RVQ_ERR_INVALID_ARGUMENT, "top must be within 0 .. %d (got %d)", kMaxTop, top);
   if (!bytes) return fail(RVQ_ERR_INVALID_ARGUMENT, "bytes must not be NULL");
-  *bytes = n == 0 ? 0 : al256(logprob_part_floats(n, logprob_plan(n, V, top), top) * sizeof(float));
+  size_t floats = 0;
+  if (n > 0)
+    for (const bool bf16 : {false, true}) {
+      const size_t f = logprob_part_floats(n, logprob_plan(n, V, top, bf16), top);
+      if (f > floats) floats = f;
+    }
+  *bytes = al256(floats * sizeof(float));
   return RVQ_OK;
 }
 

@@ -13,7 +13,9 @@
 //
 // Bound by memory, as the RMS norm: one read and one write of a row, shared by W
 // lanes of P 16-byte pieces; rows of more than 2048 pieces are read again for each
-// pass over them.
+// pass over them.  bf16 with weight and bias: 39,731 x 4096 129 us (5.0 TB/s; a copy takes 123),
+// 37,003 x 1152 38 us (4.5), with residual and sum 277,777 x 1152 505 us (5.1); one row
+// of 4096 with residual to 8 bits 4.0 us, which is a launch.
 #include "head.h"
 #include "lanes.h"
 #include "rows.h"
@@ -395,7 +397,8 @@ hipError_t launch_layer_norm(const LayerNormArgs &a, bool x_bf16, hipStream_t s)
 // One pass: a workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its
 // parts of dw and db in registers; the parts are added in order by a second
 // launch.  The number of parts depends on n, d and the type alone, so the result
-// does too.
+// does too.  Bound by memory: 39,731 x 4096 bf16 with dsum 232 us (5.6 TB/s) and 6 for
+// the parts; 1024 x 1152 fp32, four rows in turn at most, 7.1 and 4.0.
 
 namespace {
 

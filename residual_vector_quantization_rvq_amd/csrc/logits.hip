@@ -556,10 +556,15 @@ __global__ __launch_bounds__(kTopThreads) void logprob_join_kernel(LogprobArgs a
   for (int i = threadIdx.x; i < a.top; i += kTopThreads) finish_top(a, row, i, best[i], got[0], got[1]);
 }
 
-LogprobPlan logprob_plan(int64_t n, int V, int top) {
-  // fewer rows than would fill the device, and long ones: several workgroups each
+LogprobPlan logprob_plan(int64_t n, int V, int top, bool bf16) {
+  // Fewer rows than would fill the device, and so long that a second launch takes less than one
+  // workgroup's way along them: several workgroups each (65,536 fp32: one row 5.0 us, 10.7 in one, 255
+  // rows 15.5 and 18.7, 400 rows 21.5 and 20.1; 65,536 bf16: one row 5.1 and 8.3, 160 rows 8.7 and 9.1, 200
+  // rows 11.6 and 11.2; 16,384 fp32, one row: 5.0 and 4.5; with five alternatives 9.3 and 13.2, 10.2 and
+  // 11.9, 9.3 and 7.2).
   int64_t slices = 1;
-  if (n < 256 && V >= 8192) {
+  const int64_t bytes = (int64_t)V * (bf16 ? 2 : 4);
+  if (bytes >= 1 << 17 && n <= (bytes >= 1 << 18 ? 256 : 160)) {
     slices = ceil_div(512, n);
     if (slices > V / 2048) slices = V / 2048;
     if (slices > 64) slices = 64;  // a lane each in the join
@@ -584,7 +589,7 @@ static void start_logprobs(const LogprobArgs &a, const LogprobPlan &plan, hipStr
 
 template <typename T>
 static hipError_t logprobs(const LogprobArgs &a, hipStream_t s) {
-  const LogprobPlan plan = logprob_plan(a.n, a.V, a.top);
+  const LogprobPlan plan = logprob_plan(a.n, a.V, a.top, sizeof(T) == 2);
   // Threads of a row.  Of short rows what is done once a row weighs most, and a wave does it
   // for four rows as for one: 1,024 bf16 columns of 293,000 rows 112 us with 16 threads, 139
   // with 32, 189 with 64; 2,048 of 146,000 113, 117, 137, but of 6,144 10.0 and 9.1 with 64.  A

@@ -99,8 +99,8 @@ def test_logprob_arguments(rvq):
     assert call(n=(1 << 25) + 1) == 2 and call(V=(1 << 24) + 1) == 2
     assert call(n=0, x=None, ids=None, lp=None, stats=None) == 0
     size = rvq.rvq_token_logprobs_workspace_size
-    assert size(100000, 65536, 64) == 0 and size(0, 65536, 64) == 0
-    for n, V in ((1, 8192), (1, 65536), (3, 200000), (255, 1 << 24)):
+    assert size(100000, 65536, 64) == 0 and size(0, 65536, 64) == 0 and size(1, 8192, 64) == 0
+    for n, V in ((1, 32768), (1, 65536), (3, 200000), (255, 1 << 24)):
         for top in (0, 1, 20, 64):
             assert size(n, V, top) % 256 == 0 and size(n, V, top) > 0
     for kw in (dict(top=65), dict(top=-1)):
