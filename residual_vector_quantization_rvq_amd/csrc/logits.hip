@@ -15,7 +15,9 @@
 // instructions an element, four of them the exponential): each row is read once,
 // with a running maximum and sum.  What a row needs after that (top alternatives, the
 // sum of an all but certain row) is read again by the few threads whose largest
-// value says that they hold it.
+// value says that they hold it.  4577 x 65,536 bf16 110 us (5.5 TB/s), with five alternatives
+// 119, fp32 201 (6.0); 36,621 x 8192 bf16 108 (5.6) and its gradient 200 (6.0); 1,171,875 x
+// 256 174 (3.5), where what is done once a row takes longer than its bytes.
 #include "head.h"
 #include "lanes.h"
 
@@ -295,11 +297,11 @@ constexpr int kMaxCand = 1024, kTopThreads = 256;
 static_assert(kMaxTop <= kMaxCand, "the join ranks at least one slice's keys");
 
 // A bound that at least `top` of the `total` numbers in v reach (0 if there are fewer):
-// the upper 16 bits of the top-th largest.  By one wave, a bit at a time.
+// the upper 16 bits of the top-th largest (or the lower, with first = 15 and the upper as
+// bound).  By one wave, a bit at a time.
 template <int PER>
-__device__ __forceinline__ uint32_t bound_of(const uint32_t (&v)[PER], int top) {
-  uint32_t bound = 0;
-  for (int bit = 31; bit >= 16; --bit) {
+__device__ __forceinline__ uint32_t bound_of(const uint32_t (&v)[PER], int top, uint32_t bound = 0, int first = 31) {
+  for (int bit = first; bit > first - 16; --bit) {
     const uint32_t trial = bound | (1u << bit);
     int reached = 0;
 #pragma unroll
@@ -326,9 +328,13 @@ __device__ __forceinline__ void rank_keys(const uint64_t *cand, int found, int t
 // At least `top` threads have a largest value of the top-th largest of these or
 // more, so it bounds the answer from below: only the values of threads that reach it
 // are looked at again, all threads together, and the few that reach it are ranked by
-// counting.  (Of that bound the upper 16 bits are found: for bf16 all there is.)  Should
-// more than kMaxCand values reach it (a row of mostly equal values), the largest is
-// taken `top` times over the whole row.
+// counting.  (Of that bound the upper 16 bits are found.)  Should more than kMaxCand
+// values reach it, it is mostly because they are equal (tokens masked by the type's lowest
+// value): then all of the bound is found, the values above it are ranked, and those that
+// equal it come in the row's order until there are enough.  And should more than kMaxCand
+// be above it, the largest is taken `top` times over the whole row.
+// 4096 x 65,536 bf16 with ten tokens left and five alternatives 184 us (by rounds over the whole
+// row 1134), ordinary rows 110.
 template <typename T>
 __device__ void top_of_row(const T *row, int cols, float own_max, int top, uint32_t *tmax, uint64_t *cand, int *count,
                            uint64_t *out) {
@@ -351,7 +357,8 @@ __device__ void top_of_row(const T *row, int cols, float own_max, int top, uint3
   if (own >= bound) tmax[atomicAdd(count + 2, 1)] = lane;  // nobody's tmax is read from here on
   __syncthreads();
   const int holders = count[2], each = (cols + W * N - 1) / (W * N);
-  for (int i = lane; i < holders * each; i += W) {
+  bool room = true;  // all that overflow need to know is that there are too many
+  for (int i = lane; room && i < holders * each; i += W) {
     const int j = i / holders, at = (j * W + (int)tmax[i - j * holders]) * N;
     float v[N];
     load_values(row, at, cols - at, v);
@@ -359,13 +366,79 @@ __device__ void top_of_row(const T *row, int cols, float own_max, int top, uint3
     for (int e = 0; e < N; ++e)
       if (order_bits(v[e]) >= bound) {
         const int place = atomicAdd(count, 1);  // the order does not matter: ranked below
-        if (place < kMaxCand) cand[place] = order_key(v[e], at + e);
+        if (place < kMaxCand)
+          cand[place] = order_key(v[e], at + e);
+        else
+          room = false;
       }
   }
   __syncthreads();
   const int found = count[0];
   if (found <= kMaxCand) {
     rank_keys(cand, found, top, out);
+    __syncthreads();
+    return;
+  }
+  // the whole bound; -inf where fewer than `top` threads hold more
+  __syncthreads();
+  tmax[lane] = own;
+  if (lane == 0) count[0] = 0;
+  __syncthreads();
+  if (lane < 64) {
+    uint32_t mine[W / 64];
+#pragma unroll
+    for (int i = 0; i < W / 64; ++i) mine[i] = tmax[i * 64 + lane];
+    const uint32_t exact = bound_of(mine, top, bound_of(mine, top), 15);
+    if (lane == 0) count[1] = (int)max(exact, kNoneBits);
+  }
+  __syncthreads();
+  const uint32_t least = (uint32_t)count[1];
+  if (own > least)
+    for (int i = lane * N; i < cols; i += W * N) {
+      float v[N];
+      load_values(row, i, cols - i, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (order_bits(v[e]) > least) {
+          const int place = atomicAdd(count, 1);
+          if (place < kMaxCand) cand[place] = order_key(v[e], i + e);
+        }
+    }
+  __syncthreads();
+  int have = count[0];
+  if (have <= kMaxCand) {
+    for (int base = 0; base < cols && have < top && least > kNoneBits; base += W * N) {
+      const int i = base + lane * N;
+      float v[N];
+      load_values(row, i, cols - i, v);
+      int equal = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) equal += order_bits(v[e]) == least;
+      int before = equal;  // of this piece and the lower ones
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(before, off, 64);
+        if ((lane & 63) >= off) before += o;
+      }
+      __syncthreads();
+      if ((lane & 63) == 63) tmax[lane >> 6] = before;
+      __syncthreads();
+      int place = have + before - equal, all = 0;
+#pragma unroll
+      for (int w = 0; w < W / 64; ++w) {
+        if (w < lane >> 6) place += (int)tmax[w];
+        all += (int)tmax[w];
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (order_bits(v[e]) == least) {
+          if (place < top) cand[place] = order_key(v[e], i + e);
+          ++place;
+        }
+      have = min(have + all, top);
+    }
+    __syncthreads();
+    rank_keys(cand, have, top, out);
     __syncthreads();
     return;
   }
@@ -721,7 +794,8 @@ __global__ __launch_bounds__(256, 6) void logprob_grad_kernel(LogprobGradArgs a,
 template <typename T>
 static hipError_t logprobs_grad(const LogprobGradArgs &a, hipStream_t s) {
   constexpr int N = kPiece<T>;
-  // a workgroup a row; of few rows, several
+  // a workgroup a row; of few rows several, of four pieces a thread at least (65,536 fp32, one
+  // row 2.8 us, 8.5 in one; 128 rows 11.9 and 14.1, 400 rows 33.0 and 32.6)
   int64_t slices = 1;
   if (a.n < 1024) {
     slices = ceil_div(2048, a.n);
@@ -766,6 +840,10 @@ hipError_t launch_logprobs_grad(const LogprobGradArgs &a, bool x_bf16, hipStream
 // One thread an entry; q and the loss are computed in 64 bits (a few numbers a
 // row).  p_T is added up over the others themselves, whose places a map of bits in
 // LDS tells apart, not as 1 - sum p, which would lose a small p_T.
+//
+// Bound by memory where rows are long (4096 x 65,536 bf16 with tail 125 us, 4.3 TB/s,
+// without 108; its gradient 231, 4.7), and by what is done once a row, in 64 bits, where
+// they are short (1,171,875 x 256 with 64 entries 2.1 ms).
 
 namespace {
 
@@ -960,7 +1038,10 @@ static void start_distill(const DistillArgs &a, bool grad, hipStream_t s) {
 
 template <typename T>
 static hipError_t distill(const DistillArgs &a, bool grad, hipStream_t s) {
-  // at least as many threads as the teacher has entries
+  // At least as many threads as the teacher has entries.  What is done once a row a wave does
+  // for itself, the four of a workgroup together for one row: 16,384 x 2049 bf16 40 us with a wave
+  // a row and 136, 16,384 x 32,000 200 and 288; the gradient, with less of it, of 16,384 x 2049 37
+  // and 80, of 8192 columns 136 and 128.
   static_assert(kMaxTeacher <= 256, "a thread each");
   if (a.k <= 64 && (a.V <= 2048 || (a.V * sizeof(T) <= (grad ? 12288 : 65536) && a.n >= 2048)))
     start_distill<T, 64>(a, grad, s);

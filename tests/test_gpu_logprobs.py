@@ -291,3 +291,45 @@ def test_refusals(rvq, dev):
     e = rvq.rvq_token_logprobs(x[:0], ids[:0], top=3)
     assert e.logprob.shape == (0,) and e.top_ids.shape == (0, 3)
     assert rvq.rvq_token_logprobs_backward(x[:0], ids[:0], e.stats, one[:0]).shape == (0, 32)
+
+
+def _top_of(x, k):
+    order = torch.argsort(x.float() + 0.0, dim=1, descending=True, stable=True)[:, :k]
+    return order, x.float().gather(1, order)
+
+
+@pytest.mark.parametrize("shape", [(5, 2500), (3, 65536), (260, 33000), (170, 65536), (300, 9001)], ids=lambda s: "x".join(map(str, s)))
+def test_alternatives_among_equal_and_near_values(rvq, dev, shape):
+    """More than 1024 values reach the bound of the first search: masks of the type's lowest
+    value that leave fewer tokens than are asked for, rows of equal values, and fp32 values
+    whose upper halves are the same."""
+    n, V = shape
+    g = torch.Generator(device=dev).manual_seed(V)
+    for dtype in (F32, BF16):
+        low = torch.finfo(dtype).min
+        x = torch.full((n, V), low, device=dev, dtype=dtype)
+        x[0] = 0.5                                                  # all equal
+        x[1, :] = -INF
+        x[1, V // 2:V // 2 + 1500] = low                            # some of them, behind a middle
+        for r in range(2, n):                                       # 0 to 14 tokens are left
+            x[r, torch.randint(0, V, (r % 15,), generator=g, device=dev)] = torch.randn(r % 15, generator=g, device=dev).to(dtype)
+        x[2, ::3] = -0.0
+        x[2, 1::3] = 0.0
+        for k in (1, 5, 20, 64):
+            got = rvq.rvq_token_logprobs(x, torch.zeros(n, dtype=torch.int32, device=dev), top=k)
+            ids, values = _top_of(x, k)
+            assert torch.equal(got.top_ids, torch.where(values > -INF, ids, -1).int()), (dtype, k)
+    # 1 to 1 + 2^-9 in steps of 2^-23: no two values alike in the first 2^14 columns
+    x = 1 + torch.randperm(V, generator=g, device=dev).expand(n, V).contiguous() % 2 ** 14 * 2.0 ** -23
+    for k in (3, 64):
+        got = rvq.rvq_token_logprobs(x, top=k)
+        assert torch.equal(got.top_ids, _top_of(x, k)[0].int()), k
+
+
+def test_alternatives_where_one_thread_holds_the_largest(rvq, dev):
+    # 4 columns of each 1024 hold all of the largest values: more than 1024 above the bound
+    n, V = 260, 300000
+    x = torch.rand(V, device=dev).expand(n, V).contiguous()
+    x[:, (torch.arange(V, device=dev) // 4) % 256 == 77] += 5
+    got = rvq.rvq_token_logprobs(x, top=3)
+    assert torch.equal(got.top_ids, _top_of(x, 3)[0].int())
