@@ -848,6 +848,9 @@ hipError_t launch_logprobs_grad(const LogprobGradArgs &a, bool x_bf16, hipStream
 namespace {
 
 constexpr int kSegment = 1 << 18;  // columns that the map holds at once: 32 KB
+// What the teacher's entries may leave where no other token has any weight: fp32 logarithms
+// are off by 2^-24 of themselves, the teacher's own softmax by a few times that.
+constexpr double kNoRest = 0x1p-16;
 
 struct Entry {
   int id;       // -1: does not count
@@ -969,7 +972,7 @@ __global__ __launch_bounds__(256, 4) void distill_kernel(DistillArgs a, int word
         double rest = 1.0 - sum_q;
         if (rest < 0.0) rest = 0.0;
         if (others.t == 0.f) {
-          if (rest != 0.0) loss = INFINITY;
+          if (rest > kNoRest) loss = INFINITY;
           factor = 0.0;
         } else {
           // by the others' own largest value: p_T may be too small for fp32

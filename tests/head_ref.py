@@ -176,7 +176,7 @@ def distill(x, ids, teacher, T, tail, chain):
                     b_loss[i] += rest * (b_T + b_S)
                 d = d - rest * share
                 b = b + rest * share * (b_T + U * (4 * dt + 12))
-            elif float(rest) > 0:
+            elif float(rest) > 2.0 ** -16:     # below: the logarithms' rounding
                 loss[i] = torch.inf
         d[at] = p[at] - q
         b[at] = p[at] * rel[at] + 2 * U * (p[at] + q)

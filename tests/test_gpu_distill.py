@@ -252,3 +252,28 @@ def test_certain_rows_keep_their_small_numbers(rvq, dev, V, tail):
     if tail:
         bound = bound + w.double()[:, None] * p * ((tol * rest + last) / p_rest)[:, None]
     assert torch.all((d.double() - want).abs() <= bound)
+
+
+def test_entries_that_name_all_there_is(rvq, dev):
+    """The teacher's logarithms are rounded, so that its weights do not add up to 1 exactly:
+    with no other token to take the rest the loss stays finite."""
+    g = torch.Generator(device=dev).manual_seed(11)
+    for n, V, k in ((5000, 38, 38), (300, 256, 256), (40, 5000, 20)):
+        x = torch.randn((n, V), generator=g, device=dev) * 3
+        ids = torch.stack([torch.randperm(V, generator=g, device=dev)[:k] for _ in range(n)]).int()
+        if k < V:       # the others are masked
+            x = torch.full_like(x, -INF).scatter(1, ids.long(), x.gather(1, ids.long()))
+        t = torch.log_softmax(x.gather(1, ids.long()) + torch.randn((n, k), generator=g, device=dev), 1)
+        got = rvq.rvq_distill_loss(x, ids, t, 1.0, True)
+        logp = torch.log_softmax(x.double(), 1).gather(1, ids.long())
+        q = t.double().exp()
+        want = (q * (t.double() - logp)).sum(1)
+        # the teacher's logarithms as given; log p within 160 roundings and 3 of d < 40
+        assert torch.all((got.loss.double() - want).abs() <= (160 + 120) * ref.U + ref.U * want.abs())
+        one = torch.ones(n, device=dev)
+        d = rvq.rvq_distill_loss_backward(x, ids, t, got.stats, one, 1.0, True)
+        p = logp.exp()
+        grad = torch.zeros(n, V, device=dev, dtype=torch.float64).scatter(1, ids.long(), p - q)
+        assert torch.all((d.double() - grad).abs() <= (160 + 120) * ref.U * (p.amax(1, keepdim=True) + 1))
+        t = t - 0.01                                     # and with a rest that is one, it does not
+        assert torch.all(torch.isinf(rvq.rvq_distill_loss(x, ids, t, 1.0, True).loss))
