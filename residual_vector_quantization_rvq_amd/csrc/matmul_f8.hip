@@ -114,7 +114,7 @@ __device__ __forceinline__ void product(const Operand<EXACT> (&b)[NT], const Ope
 // its registers hold beside the rest).  1 x 65,536 x 4096 54 us, 5.0 TB/s.
 template <int MT, int KW, bool SWAP, bool W_BLOCKS>
 __global__ __launch_bounds__(KW * 64, KW == 4 && !W_BLOCKS ? 3 : 4) void matmul_f8_few_kernel(MatmulArgs a) {
-  constexpr int U = MT == 1 && W_BLOCKS ? 8 : 4, E = W_BLOCKS ? 1 : 4;
+  constexpr int U = W_BLOCKS ? (MT == 1 ? 8 : 4) : KW == 16 ? 2 : 4, E = W_BLOCKS ? 1 : 4;
   __shared__ f32x4 sums[KW][MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
@@ -234,10 +234,13 @@ static hipError_t few(const MatmulArgs &a, hipStream_t s) {
 }
 template <int MT, bool SWAP>
 static hipError_t few(const MatmulArgs &a, hipStream_t s) {
-  // fewer workgroups than four a CU: more waves each (one row, k = 4096: of 4096 rows 6.6 us with sixteen
-  // waves and 9.8 with four, of 8192 rows 11.2 and 13.2; in the Infinity Cache 16,384 rows 18.5 and 17.1)
-  const int64_t groups = ceil_div(SWAP ? a.m : a.n, 16) * ceil_div(SWAP ? a.n : a.m, 16 * MT);
-  return groups >= 1024 ? few<MT, 4, SWAP>(a, s) : few<MT, 16, SWAP>(a, s);
+  // One workgroup a CU or less, of one row of tiles: more waves each (one row, k = 4096, of 4096 rows 6.2 us with
+  // sixteen waves and 8.1 with four, k = 1152 3.6 and 3.6; of 5000 rows 9.9 and 9.4, k = 1152 5.5 and 4.2, of 8192
+  // rows 11.0 and 10.7.  32 rows by 4096 11.7 and 11.4, by 15,000 40 and 35).
+  const int64_t groups = ceil_div(SWAP ? a.m : a.n, 16);
+  if constexpr (MT == 1)
+    if (groups <= 256) return few<MT, 16, SWAP>(a, s);
+  return few<MT, 4, SWAP>(a, s);
 }
 
 // The order of a block's instructions: behind each matrix instruction the sums of
@@ -553,12 +556,16 @@ hipError_t launch_matmul_f8(const MatmulArgs &a, hipStream_t s) {
   };
   const bool direct = even(a.a, a.a_stride, a.k) && even(a.b, a.b_stride, a.k);
   const int64_t few_rows = a.m < a.n ? a.m : a.n, many = a.m < a.n ? a.n : a.m;
-  // Straight from memory where that is less than a tile's time, which is at least that of its stages, about 1.2 us
-  // for each of its blocks of k: it takes about (52 + 2.2 rows) us for 65,536 rows of 4096 on the other side (from HBM: 1 x
-  // 65,536 57 and 82 us, 8 rows 69 and 75, 16 rows 82 and 76; 16 x 32,768 45 and 47, 32 rows 63 and 47; 32 x 16,384 35
-  // and 39, 64 rows 62 and 40; 64 x 8192 34 and 38; 128 x 4096 33 and 38).  And few rows at any address (tiles of them
-  // go through registers, at half the rate).
-  if (many * (few_rows + 2) <= 655360 || (few_rows <= 32 && !direct)) {
+  // Straight from memory where that is less than the tiles' time.  For k = 4096 that is about 34 us for up to 256 tiles
+  // and 80 for 65,536 rows on the other side; up to 16 rows straight take (52 + 2.2 rows) us for 65,536 (one row 57
+  // and 82 us, 9 rows 68 and 81, 12 x 40,000 49 and 48, 16 x 65,536 82 and 76, 16 x 32,768 42 and 41, 16 x 24,576
+  // 33 and 37), more rows 33 us for each 16,384 times a pass of 32 (32 x 16,384 33 and 35, 32 x 20,000 40 and 36; 64 x
+  // 8192 32 and 34, 72 x 8192 40 and 34; 128 x 4096 32 and 33, 150 x 4096 37 and 33).  Both grow with k.  And few
+  // rows at any address (tiles of them go through registers, at half the rate).
+  const bool straight = few_rows <= 12 ? true
+                        : few_rows <= 16 ? many <= 27500
+                                         : many * ceil_div(few_rows, 32) <= 16384;
+  if (straight || (few_rows <= 32 && !direct)) {
     if (a.m <= a.n) return a.m <= 16 ? few<1, false>(a, s) : few<2, false>(a, s);
     return a.n <= 16 ? few<1, true>(a, s) : few<2, true>(a, s);
   }
