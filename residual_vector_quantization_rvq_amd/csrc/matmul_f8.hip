@@ -272,15 +272,20 @@ __device__ __forceinline__ void order_block() {
 //
 // Rows at any address or distance (not DIRECT) go through registers into LDS.
 //
+// KG groups of WM x WN waves share a tile's blocks of k by turns, each with two stages and sums of
+// its own, which are added at the end: where there are fewer tiles than CUs, so that each SIMD
+// has two waves all the same.
+//
 // The first operand of a matrix instruction is b: then a lane's results are four
 // columns of one row of out, it needs one scale of a, and stores them side by side.
-template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS, bool DIRECT>
-__global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulArgs a, int tiles_m, int tiles_n) {
+template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS, bool DIRECT, int KG>
+__global__ __launch_bounds__(WM *WN *KG * 64, 2) void matmul_f8_tile_kernel(MatmulArgs a, int tiles_m, int tiles_n) {
   constexpr int kWaves = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16, kRows = BM + BN;
   constexpr int kStage = kRows * kScaleBlock;
-  __shared__ uint4 ring[2 * kStage / 16];
-  __shared__ float scales[2][kRows];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  __shared__ uint4 ring[2 * KG * kStage / 16];
+  __shared__ float scales[2 * KG][kRows];
+  const int lane = threadIdx.x & 63, wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = wave_of_all / kWaves, wave = wave_of_all % kWaves, tid = wave * 64 + lane;
   const int wm = wave % WM, wn = wave / WM;
 
   // each XCD a run of tiles, in groups of eight rows of tiles: those at work at one time share their operands in its L2
@@ -295,8 +300,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
   const uint8_t *pa = a.a + m0 * a.a_stride, *pb = a.b + n0 * a.b_stride;
   // The second half of the waves bring the data in (on each SIMD one of its two waves):
   // while they send for the next stage, the others multiply, and then wait for them.
-  // (Through registers all waves do: half of them would not have enough.)
-  constexpr int kLoaders = DIRECT ? kWaves / 2 : kWaves;
+  // (Through registers all waves do: half of them would not have enough; and of two groups all.)
+  constexpr int kLoaders = DIRECT && KG == 1 ? kWaves / 2 : kWaves;
   constexpr int GA = BM / 8 / kLoaders, GB = BN / 8 / kLoaders;  // a wave's loads: 8 rows each
   static_assert(GA * 8 * kLoaders == BM && GB * 8 * kLoaders == BN, "whole loads");
   const bool loader = wave >= kWaves - kLoaders;
@@ -437,33 +442,59 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
     if constexpr (!EXACT) order_block<B_BLOCKS, MT, NT>();
   };
 
-  if (loader) {
-    load_scales(0);
-    load_stage(0, 0);
-    store_stage(0);
-    store_scales(0);
-    if (blocks > 1) load_scales(1);
-  } else if (!EXACT) {
+  // this group's blocks are kg, kg + KG, ..., block kb in stage kb % (2 KG)
+  if (loader && kg < blocks) {
+    load_scales(kg);
+    load_stage(kg, kg);
+    store_stage(kg);
+    store_scales(kg);
+    if (kg + KG < blocks) load_scales(kg + KG);
+  } else if (!EXACT && KG == 1) {
     __builtin_amdgcn_s_setprio(1);
   }
   const auto advance = [&](int kb) {
     // this stage and the next scales are here, for all waves; the other stage has been read
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (loader && kb + 1 < blocks) {
-      store_scales((kb + 1) & 1);
-      if (kb + 2 < blocks) load_scales(kb + 2);
-      load_stage(kb + 1, (kb + 1) & 1);
+    if (loader && kb + KG < blocks) {
+      store_scales((kb + KG) % (2 * KG));
+      if (kb + 2 * KG < blocks) load_scales(kb + 2 * KG);
+      load_stage(kb + KG, (kb + KG) % (2 * KG));
     }
   };
   const int whole = k / kScaleBlock;
-  for (int kb = 0; kb < whole; ++kb) {
+  int first = 0;  // of the groups' next blocks
+  for (; first + KG <= whole; first += KG) {
+    const int kb = first + kg;
     advance(kb);
-    block(std::false_type{}, kb, kb & 1);
-    if (loader && kb + 1 < blocks) store_stage((kb + 1) & 1);
+    block(std::false_type{}, kb, kb % (2 * KG));
+    if (loader && kb + KG < blocks) store_stage((kb + KG) % (2 * KG));
   }
-  if (whole < blocks) {
-    advance(whole);
-    block(std::true_type{}, whole, whole & 1);
+  if (first < blocks) {
+    const int kb = first + kg;
+    advance(kb);
+    if (KG > 1 && kb < whole)
+      block(std::false_type{}, kb, kb % (2 * KG));
+    else if (kb < blocks)
+      block(std::true_type{}, kb, kb % (2 * KG));
+  }
+
+  if constexpr (KG > 1) {
+    // the second group's sums to the first, behind the place of the results below
+    static_assert(KG == 2 && kWaves * MT * NT * 1024 + kWaves * MT * 16 * 128 <= 2 * KG * kStage, "the ring holds them");
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // all have read their last fragments
+    f32x4 *sums = (f32x4 *)(ring + kWaves * MT * 16 * 128 / 16) + wave * MT * NT * 64 + lane;
+    if (kg == 1) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sums[(i * NT + j) * 64] = acc[i][j];
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kg == 1) return;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] += sums[(i * NT + j) * 64];
   }
 
   if constexpr (EXACT) {  // fp32
@@ -483,7 +514,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void matmul_f8_tile_kernel(MatmulAr
     // bf16, turned through the wave's part of LDS so that whole lines leave: a row of 64
     // columns is eight pieces of 16 bytes, at their place ^ (row % 8)
     static_assert(NT == 4 && kWaves * MT * 16 * 128 <= 2 * kStage, "the ring holds the tile");
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // all have read their last fragments
+    if (KG == 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // all have read their last fragments
     const uint32_t own = lds + wave * MT * 16 * 128;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -521,17 +552,22 @@ __global__ __launch_bounds__(kThreads) void matmul_f8_empty_kernel(MatmulArgs a)
     a.out_bf16 ? store_f32((uint16_t *)a.out, i, 0.f) : store_f32((float *)a.out, i, 0.f);
 }
 
-template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS, bool DIRECT>
+template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS, bool DIRECT, int KG = 1>
 static hipError_t tiles(const MatmulArgs &a, hipStream_t s) {
   const int tm = (int)ceil_div(a.m, WM * MT * 16), tn = (int)ceil_div(a.n, WN * NT * 16);
   const dim3 grid((unsigned)(ceil_div((int64_t)tm * tn, 8) * 8));
-  matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, B_BLOCKS, DIRECT><<<grid, WM * WN * 64, 0, s>>>(a, tm, tn);
+  matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, B_BLOCKS, DIRECT, KG><<<grid, WM * WN * KG * 64, 0, s>>>(a, tm, tn);
   return hipGetLastError();
 }
 template <bool EXACT, bool B_BLOCKS>
 static hipError_t tiles(const MatmulArgs &a, bool direct, hipStream_t s) {
+  // Up to a tile a CU: two groups of waves share k (512 x 4096 x 4096 27 us, 33 with one, to fp32 34 and 40; 1152 x 1152 x
+  // 39,731 222 and 286).  For both ways, whose results are the same.
+  const bool shared = ceil_div(a.m, 128) * ceil_div(a.n, 128) <= 256;
   // 8192 x 8192 x 8192: 498 us direct and 1223 us through registers, fp32 results 962 and 2470
-  if (!direct) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false>(a, s);
+  if (!direct)
+    return shared ? tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false, 2>(a, s) : tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false>(a, s);
+  if (shared) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, true, 2>(a, s);
   // 256 x 256 where the registers hold a wave's 128 x 64, that is 8-bit operands and one scale of b a
   // wave; else 256 x 128.  Large tiles move half the bytes, but only as many workgroups as there are of them
   // (k = 4096: 192 of 256 x 256 66 us, their 768 parts 83; 128 of them 60 us, their 512 parts 45; fp32 results, 192 of
@@ -556,15 +592,15 @@ hipError_t launch_matmul_f8(const MatmulArgs &a, hipStream_t s) {
   };
   const bool direct = even(a.a, a.a_stride, a.k) && even(a.b, a.b_stride, a.k);
   const int64_t few_rows = a.m < a.n ? a.m : a.n, many = a.m < a.n ? a.n : a.m;
-  // Straight from memory where that is less than the tiles' time.  For k = 4096 that is about 34 us for up to 256 tiles
-  // and 80 for 65,536 rows on the other side; up to 16 rows straight take (52 + 2.2 rows) us for 65,536 (one row 57
-  // and 82 us, 9 rows 68 and 81, 12 x 40,000 49 and 48, 16 x 65,536 82 and 76, 16 x 32,768 42 and 41, 16 x 24,576
-  // 33 and 37), more rows 33 us for each 16,384 times a pass of 32 (32 x 16,384 33 and 35, 32 x 20,000 40 and 36; 64 x
-  // 8192 32 and 34, 72 x 8192 40 and 34; 128 x 4096 32 and 33, 150 x 4096 37 and 33).  Both grow with k.  And few
-  // rows at any address (tiles of them go through registers, at half the rate).
+  // Straight from memory where that is less than the tiles' time.  For k = 4096 that is 25 to 29 us for up to 256
+  // tiles (33 for fp32 results) and 80 for 65,536 rows on the other side; up to 16 rows straight take (52 + 2.2
+  // rows) us for 65,536 (one row 57 and 82 us, 9 rows 68 and 81, 12 x 40,000 48 and 46, or 105 to fp32, 16 x 65,536
+  // 82 and 76, 16 x 20,000 28 and 28, 16 x 27,500 37 and 33, 35 to fp32), more rows 33 us for each 16,384 times a pass
+  // of 32 (32 x 13,000 33 and 26, 32 to fp32, 64 x 6144 25 and 26, 96 x 4096 25 and 27, 128 x 4096 32 and 29, 34 to
+  // fp32).  All grow with k.  And few rows at any address (tiles of them go through registers, at half the rate).
   const bool straight = few_rows <= 12 ? true
-                        : few_rows <= 16 ? many <= 27500
-                                         : many * ceil_div(few_rows, 32) <= 16384;
+                        : few_rows <= 16 ? many <= (a.out_bf16 ? 20000 : 27500)
+                                         : many * ceil_div(few_rows, 32) <= (a.out_bf16 ? 12288 : 16384);
   if (straight || (few_rows <= 32 && !direct)) {
     if (a.m <= a.n) return a.m <= 16 ? few<1, false>(a, s) : few<2, false>(a, s);
     return a.n <= 16 ? few<1, true>(a, s) : few<2, true>(a, s);
