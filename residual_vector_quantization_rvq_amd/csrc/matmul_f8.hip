@@ -10,14 +10,16 @@
 // added in fp32: for fp32 results, and where few rows leave the matrix cores idle anyway,
 // operands are widened to bf16 on the way, at half the rate.
 //
-// A tile is bound by its matrix instructions and what goes on around them: a block's sums
-// are multiplied by their scales and added (one multiply-add a result for 128 products,
-// and a multiplication with a scale for each row of b), and a stage ends at a barrier.
-// 8192 x 8192 x 8192 to bf16 498 us (2.2 PFLOP/s; 755 with a scale for each row of b), to
-// fp32 962 (1.14); the vendor's library takes 403 for 8 bits with one scale for all (2.73)
-// and 902 for bf16 (1.22).  8192 x 65,536 x 4096 to bf16 2140 (2.05), 8192 x 4096 x 39,731
-// to fp32 2520 to 2700 (1.02).  The matrix cores are busy for half of these two's cycles
-// (0.51 and 0.47), and no two lanes meet in a bank of LDS when a fragment is read.
+// A tile of 8-bit products is bound by its operands' way into LDS: a CU receives 34 to 39
+// KB/us, whether one stage is on its way or three, all CUs work or a quarter of them, and
+// however rows are spaced; hence the largest tile that the registers hold.  A tile of exact
+// products is bound by widening and scaling beside its matrix instructions (eight
+// conversions for four of them, two operations a result and block).  8192 x 8192 x 8192 to bf16
+// 450 to 460 us (2.4 PFLOP/s; 667 with a scale for each row of b), to fp32 913 (1.20; 1024);
+// the vendor's library takes 403 for 8 bits with one scale for all (2.73) and 775 for bf16
+// (1.42).  8192 x 65,536 x 4096 to bf16 1940 (2.27), 8192 x 4096 x 39,731 to fp32 2450 to 2560
+// (1.05).  The matrix cores are busy for half of these two's cycles (0.56 and 0.47), and no two
+// lanes meet in a bank of LDS when a fragment is read.
 #include <type_traits>
 
 #include "head.h"
@@ -564,7 +566,7 @@ static hipError_t tiles(const MatmulArgs &a, bool direct, hipStream_t s) {
   // Up to a tile a CU: two groups of waves share k (512 x 4096 x 4096 27 us, 33 with one, to fp32 34 and 40; 1152 x 1152 x
   // 39,731 222 and 286).  For both ways, whose results are the same.
   const bool shared = ceil_div(a.m, 128) * ceil_div(a.n, 128) <= 256;
-  // 8192 x 8192 x 8192: 498 us direct and 1223 us through registers, fp32 results 962 and 2470
+  // 8192 x 8192 x 8192: 460 us direct and 730 us through registers, fp32 results 913 and 1160
   if (!direct)
     return shared ? tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false, 2>(a, s) : tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false>(a, s);
   if (shared) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, true, 2>(a, s);
