@@ -570,12 +570,13 @@ static hipError_t tiles(const MatmulArgs &a, bool direct, hipStream_t s) {
   if (!direct)
     return shared ? tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false, 2>(a, s) : tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false>(a, s);
   if (shared) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, true, 2>(a, s);
-  // 256 x 256 where the registers hold a wave's 128 x 64, that is 8-bit operands and one scale of b a
-  // wave; else 256 x 128.  Large tiles move half the bytes, but only as many workgroups as there are of them
-  // (k = 4096: 192 of 256 x 256 66 us, their 768 parts 83; 128 of them 60 us, their 512 parts 45; fp32 results, 192 of
-  // 256 x 128 73 us and 78, 128 of them 67 us and 49).
+  // 256 x 256 where the registers hold a wave's 128 x 64, that is 8-bit operands and one scale of b a wave; else
+  // 256 x 128.  Large tiles move half or three quarters of the bytes, but go in rounds of 256, which have to be filled
+  // (k = 4096: 128 of 256 x 256 52 us, their 512 parts 44; 144 of them 52 and 66; 272 of them 106 and 104; to fp32, 256
+  // of 256 x 128 70 us and 76, 288 of them 126 and 104, 416 of them 129 and 135, 544 of them 195 and 169).
   constexpr bool kSquare = !EXACT && B_BLOCKS;
-  if (ceil_div(a.m, 256) * ceil_div(a.n, kSquare ? 256 : 128) < 160) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, true>(a, s);
+  const int64_t large = ceil_div(a.m, 256) * ceil_div(a.n, kSquare ? 256 : 128);
+  if (large * 100 < ceil_div(large, 256) * 256 * (kSquare ? 55 : 75)) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, true>(a, s);
   if constexpr (kSquare)
     return tiles<2, 4, 8, 4, EXACT, B_BLOCKS, true>(a, s);
   else

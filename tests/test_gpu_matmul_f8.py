@@ -254,3 +254,24 @@ def test_product_refusals(rvq, dev):
             rvq.rvq_quantize_f8(bad)
     with pytest.raises(ValueError):
         rvq.rvq_quantize_f8(x, 64)
+
+
+@pytest.mark.parametrize("shape", [(1100, 4100, 400), (1700, 2600, 1155), (2050, 4097, 128), (130, 140, 100), (300, 500, 129), (900, 1000, 257)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_tiles_that_share_k_and_tiles_that_do_not(rvq, dev, shape):
+    """More tiles of 128 than a device has CUs, and fewer (then two groups of waves share k, one of
+    them without a block where k is a block or less): every layout, result and alignment."""
+    m, n, k = shape
+    a, sa = _operand(rvq, m, k, "line", 1, dev)
+    for kind in ("block", "line", "row"):
+        b, sb = _operand(rvq, n, k, kind, 2, dev)
+        for odt in (F32, BF16):
+            want = _check_product(rvq, a, sa, b, sb, odt)
+            apart = []
+            for t in (a, b):        # rows at any byte, 0x7f (NaN) between them
+                buf = torch.full((t.shape[0], k + 3), 0x7f, dtype=torch.uint8, device=dev).view(F8)
+                buf[:, :k] = t
+                apart.append(buf[:, :k])
+            assert torch.equal(rvq.rvq_matmul_f8(apart[0], sa, apart[1], sb, out_dtype=odt), want)
+            again = rvq.rvq_matmul_f8(a, sa, b, sb, out_dtype=odt)
+            assert torch.equal(again, want)
