@@ -56,9 +56,6 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
   const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
   return {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-__device__ __forceinline__ float scale_at(const ScaleView &s, int64_t row, int64_t kb) {
-  return s.p[(row >> s.shift) * s.row_stride + kb * s.block_stride];
-}
 
 // 16 bytes a lane from base + off to lds + 16 * lane.  Written out because the compiler
 // would wait for every load of this kind before the next read of LDS; the waits are
