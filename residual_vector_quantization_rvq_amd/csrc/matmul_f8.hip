@@ -108,9 +108,10 @@ __device__ __forceinline__ void product(const Operand<EXACT> (&b)[NT], const Ope
 // ---- few rows on one side ----
 // `w` is the operand with many rows, `s` the one with few: a workgroup takes 16 rows
 // of w and 16 MT of s, its KW waves the blocks of k in turn, straight from memory to
-// registers (each byte of w is read once).  The waves' sums are added in order.
-// Bound by the bytes of w: four or eight blocks of a wave are on their way at once (as many as
-// its registers hold beside the rest).  1 x 65,536 x 4096 54 us, 5.0 TB/s.
+// registers (each byte of w is read once for 16 MT rows of s).  The waves' sums are added
+// in order.  Bound by the bytes of w: two to eight blocks of a wave are on their way at
+// once, as many as its registers hold (sixteen waves with a scale for each row of w: two, 4096
+// rows of 4096 6.2 us; with four, which spill, 8.1).  1 x 65,536 x 4096 54 us, 5.0 TB/s.
 template <int MT, int KW, bool SWAP, bool W_BLOCKS>
 __global__ __launch_bounds__(KW * 64, KW == 4 && !W_BLOCKS ? 3 : 4) void matmul_f8_few_kernel(MatmulArgs a) {
   constexpr int U = W_BLOCKS ? (MT == 1 ? 8 : 4) : KW == 16 ? 2 : 4, E = W_BLOCKS ? 1 : 4;
