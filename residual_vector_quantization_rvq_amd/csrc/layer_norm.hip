@@ -458,8 +458,14 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(LayerNormGrad
       float w[N];
       load_weight<N>(a.weight, a.w_bf16, c, a.d - c, w);
 #pragma unroll
+      for (int e = 0; e < N; ++e) u[p][e] = (u[p][e] - m) * r;
+      if (a.d - c < N) {  // what is not of the row: 0, where m r may be beyond fp32 (and dy, 0, is no help)
+#pragma unroll
+        for (int e = 1; e < N; ++e)
+          if (c + e >= a.d) u[p][e] = 0.f;
+      }
+#pragma unroll
       for (int e = 0; e < N; ++e) {
-        u[p][e] = (u[p][e] - m) * r;  // beyond the row's end beside a dy of 0
         if (DW) {
           acc[p][e] += g[p][e] * u[p][e];
           accb[p][e] += g[p][e];
