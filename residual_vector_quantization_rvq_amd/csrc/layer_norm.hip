@@ -397,10 +397,24 @@ hipError_t launch_layer_norm(const LayerNormArgs &a, bool x_bf16, hipStream_t s)
 // One pass: a workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its
 // parts of dw and db in registers; the parts are added in order by a second
 // launch.  The number of parts depends on n, d and the type alone, so the result
-// does too.  Bound by memory: 39,731 x 4096 bf16 with dsum 232 us (5.6 TB/s) and 6 for
+// does too.
+// h - m can be beyond fp32 where h and m are not (values of both signs near its largest):
+// where m is large, both are halved and r is doubled, for the cost of an fma in place of a
+// difference and with the same bits.
+// Bound by memory: 39,731 x 4096 bf16 with dsum 232 us (5.6 TB/s) and 6 for
 // the parts; 1024 x 1152 fp32, four rows in turn at most, 7.1 and 4.0.
 
 namespace {
+
+// u = (h - m) r = (h f - m f) (r / f); h f is exact inside the fma
+struct Centre {
+  float f, mf, rf;
+  __device__ __forceinline__ Centre(float m, float r) : f(fabsf(m) > 0x1p100f ? 0.5f : 1.f) {
+    mf = m * f;
+    rf = f < 1.f ? r * 2.f : r;
+  }
+  __device__ __forceinline__ float u(float h) const { return __builtin_fmaf(h, f, -mf) * rf; }
+};
 
 // Workgroups of a launch, and with them the parts: three a CU, which are at work at once
 // with most shapes' registers (277,777 x 1152 bf16 476 us, 621 with four; 78,125 x 4096 459 and
@@ -438,7 +452,8 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(LayerNormGrad
     for (int e = 0; e < N; ++e) acc[p][e] = accb[p][e] = 0.f;
   for (int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / W; row < a.n; row += (int64_t)gridDim.x * R) {
     const int64_t at = row * a.d;
-    const float r = a.rstd[row], m = a.mean[row];
+    const float r = a.rstd[row];
+    const Centre centre(a.mean[row], r);
     u32x4 q[P][3];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -458,8 +473,8 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(LayerNormGrad
       float w[N];
       load_weight<N>(a.weight, a.w_bf16, c, a.d - c, w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) u[p][e] = (u[p][e] - m) * r;
-      if (a.d - c < N) {  // what is not of the row: 0, where m r may be beyond fp32 (and dy, 0, is no help)
+      for (int e = 0; e < N; ++e) u[p][e] = centre.u(u[p][e]);
+      if (a.d - c < N) {  // what is not of the row: 0, where m times r may be beyond fp32 (and dy, 0, is no help)
 #pragma unroll
         for (int e = 1; e < N; ++e)
           if (c + e >= a.d) u[p][e] = 0.f;
@@ -534,11 +549,12 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_wide_kernel(LayerNor
   const T *dy = (const T *)a.dy, *h = (const T *)a.h, *ds = (const T *)a.dsum;
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
     const int64_t at = row * a.d;
-    const float r = a.rstd[row], m = a.mean[row];
+    const float r = a.rstd[row];
+    const Centre centre(a.mean[row], r);
     const auto g_of = [&](int i) {
       return load_f32(dy, at + i) * (a.weight ? load_either(a.weight, a.w_bf16, i) : 1.f);
     };
-    const auto u_of = [&](int i) { return (load_f32(h, at + i) - m) * r; };
+    const auto u_of = [&](int i) { return centre.u(load_f32(h, at + i)); };
     float sum = 0.f, dot = 0.f;
     for (int i = threadIdx.x; i < a.d; i += kThreads) {
       const float g = g_of(i);
@@ -564,7 +580,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_params_wide_kernel(LayerN
   float s = 0.f, b = 0.f;
   for (int64_t r = r0; r < r1; ++r) {
     const float dy = load_f32((const T *)a.dy, r * a.d + c);
-    s += dy * ((load_f32((const T *)a.h, r * a.d + c) - a.mean[r]) * a.rstd[r]);
+    s += dy * Centre(a.mean[r], a.rstd[r]).u(load_f32((const T *)a.h, r * a.d + c));
     b += dy;
   }
   a.part[part * 2 * a.d + c] = s;

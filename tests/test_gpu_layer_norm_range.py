@@ -65,3 +65,18 @@ def test_rows_of_one_large_value(rvq, dev, d, dtype):
         h[2], h[5] = values[0], values[1]
         for dsum in (None, _randn((9, d), d + 1, dev, dtype)):
             _check(rvq, h.to(dtype), _randn((9, d), d + 2, dev, dtype), eps, dsum)
+
+
+@pytest.mark.parametrize("d", [3, 9, 41, 255, 1001, 1152, 5001, 9001, 20001])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_differences_beyond_the_range(rvq, dev, d, dtype):
+    """A third of a row at 3.3e38 and the rest at -3e38: the values are within fp32, their
+    distances from the mean (4.2e38) are not."""
+    g = torch.Generator(device=dev).manual_seed(d)
+    h = _randn((7, d), d, dev)
+    at = torch.arange(d, device=dev)
+    sign = torch.where(at % 3 == 0, 3.3e38, -3e38)
+    h[1] = sign * (1 - 0.01 * torch.rand(d, generator=g, device=dev))
+    h[4] = -sign * (1 - 0.01 * torch.rand(d, generator=g, device=dev))
+    for dsum in (None, _randn((7, d), d + 1, dev, dtype)):
+        _check(rvq, h.to(dtype), _randn((7, d), d + 2, dev, dtype), 1e-6, dsum)
