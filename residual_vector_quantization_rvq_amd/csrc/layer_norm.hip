@@ -588,28 +588,30 @@ __global__ __launch_bounds__(kThreads) void layer_norm_params_wide_kernel(LayerN
 }
 
 // Columns' sums over the parts: 64 columns a workgroup, a wave for every 1/16
-// of the parts; columns d .. 2d - 1 are dbias'.
+// of the parts; columns d .. 2d - 1 are dbias'.  In 64 bits: the parts of few rows are many
+// beside what each of them sums (1024 x 1152 fp32: 512 of two rows, the result's error 4e-8 and
+// 2.3e-7 in 32 bits), and the kernel waits for its loads (4.0 us there in 32 bits, 4.3 in 64).
 __global__ __launch_bounds__(1024) void layer_norm_params_join_kernel(const float *part, int64_t parts, int d,
                                                                       float *dweight, float *dbias) {
-  __shared__ float sums[16][64];
+  __shared__ double sums[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
-  float s = 0.f;
+  double s = 0.0;
   if (c < 2 * d) {
     const int p1 = (int)(parts * (wave + 1) / 16);
 #pragma unroll 8
-    for (int p = (int)(parts * wave / 16); p < p1; ++p) s += part[(int64_t)p * 2 * d + c];
+    for (int p = (int)(parts * wave / 16); p < p1; ++p) s += (double)part[(int64_t)p * 2 * d + c];
   }
   sums[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < 2 * d) {
-    s = 0.f;
+    s = 0.0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) s += sums[w][lane];
     if (c < d) {
-      if (dweight) dweight[c] = s;
+      if (dweight) dweight[c] = (float)s;
     } else if (dbias) {
-      dbias[c - d] = s;
+      dbias[c - d] = (float)s;
     }
   }
 }
