@@ -963,9 +963,8 @@ def rvq_matmul_f8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sca
     """a b^T [m, n] of 8-bit operands a [m, k] and b [n, k] (float8_e4m3fn) with
     their scales: one for a row ([rows], as the norms' 8-bit outputs have), for
     every 128 elements of a row ([rows, ceil(k / 128)]) or for 128 x 128 elements
-    ([ceil(rows / 128), ceil(k / 128)]).  Rows may be spaced apart.  Sums in fp32.
-    With out_dtype float32 products are exact; with bfloat16 the matrix cores may cut
-    off parts of them, about 2.5e-4 of a result from random values."""
+    ([ceil(rows / 128), ceil(k / 128)]).  Rows may be spaced apart.  Products are
+    exact and sums in fp32, rounded once to out_dtype."""
     if not (isinstance(a, torch.Tensor) and a.is_cuda):
         raise ValueError("a must be a device tensor")
     dev = a.device

@@ -2,24 +2,23 @@
 //
 //   out[m][n] = sum over blocks kb of sa(m, kb) sb(n, kb) sum_{k in kb} a[m][k] b[n][k]
 //
-// The matrix cores' own 8-bit products are not added in fp32: of each eight that are
-// added at once, what is below 2^-13 of the largest is cut off (measured with single
-// products; a group's error is up to 7 2^-13 of its largest product, and of random
-// values 2.5e-4 of the result's size).  bf16 results, whose own rounding is up to 3.9e-3,
-// are made of them.  e4m3 values are bf16 values, though, whose products are exact and
-// added in fp32: for fp32 results, and where few rows leave the matrix cores idle anyway,
-// operands are widened to bf16 on the way, at half the rate.
+// Sums are fp32.  The matrix cores' own 8-bit products are not added in fp32: of each eight
+// that are added at once, what is below 2^-13 of the largest is cut off (measured with single
+// products), up to 7 2^-13 of the products' magnitudes and far more of a result that
+// cancels.  e4m3 values are bf16 values, though, whose products are exact and added in
+// fp32: operands are widened to bf16 on the way, at half the rate (8192 x 65,536 x 4096 to bf16
+// 1940 us with 8-bit products).  The same kernels make fp32 and bf16 results, so a bf16 result is the
+// fp32 result rounded once.
 //
-// A tile of 8-bit products is bound by its operands' way into LDS: a CU receives 34 to 39
-// KB/us, whether one stage is on its way or three, all CUs work or a quarter of them, and
-// however rows are spaced; hence the largest tile that the registers hold.  A tile of exact
-// products is bound by widening and scaling beside its matrix instructions (eight
-// conversions for four of them, two operations a result and block).  8192 x 8192 x 8192 to bf16
-// 450 to 460 us (2.4 PFLOP/s; 667 with a scale for each row of b), to fp32 913 (1.20; 1024);
-// the vendor's library takes 403 for 8 bits with one scale for all (2.73) and 775 for bf16
-// (1.42).  8192 x 65,536 x 4096 to bf16 1940 (2.27), 8192 x 4096 x 39,731 to fp32 2450 to 2560
-// (1.05).  The matrix cores are busy for half of these two's cycles (0.56 and 0.47), and no two
-// lanes meet in a bank of LDS when a fragment is read.
+// A tile is bound by widening and scaling beside its matrix instructions (eight conversions
+// for four of them, two operations a result and block; one where b has a scale for 128 rows).
+// Its operands' way into LDS comes next: a CU receives 34 to 39 KB/us, whether one stage is on
+// its way or three, and however rows are spaced; hence the largest tile that the registers
+// hold.  8192 x 8192 x 8192 to bf16 953 us (1.15 PFLOP/s; 1056 with a scale for each row of b), to
+// fp32 932; the vendor's library takes 775 for bf16 (1.42), and 403 for 8-bit products with one
+// scale for all.  8192 x 65,536 x 4096 to bf16 3800 (1.16), 8192 x 4096 x 39,731 to fp32
+// 2450 to 2580 (1.03).  The matrix cores are busy for half of the last one's cycles (0.47), and no
+// two lanes meet in a bank of LDS when a fragment is read.
 #include <type_traits>
 
 #include "head.h"
@@ -28,7 +27,6 @@ namespace rvq {
 
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 
@@ -69,38 +67,22 @@ __device__ __forceinline__ u32x4 read_lds(uint32_t at) {
 struct Frag {  // 32 e4m3 values of a row
   u32x4 lo, hi;
 };
-// A fragment as the matrix instructions take it: as it is, or widened to bf16.
-template <bool EXACT>
-struct Operand;
-template <>
-struct Operand<false> {
-  i32x8 v;
-  Operand() = default;
-  __device__ __forceinline__ explicit Operand(const Frag &f)
-      : v{(int)f.lo[0], (int)f.lo[1], (int)f.lo[2], (int)f.lo[3], (int)f.hi[0], (int)f.hi[1], (int)f.hi[2], (int)f.hi[3]} {}
-};
-template <>
-struct Operand<true> {
+// A fragment as the matrix instructions take it
+struct Operand {
   bf16x8 v[4];
   Operand() = default;
   __device__ __forceinline__ explicit Operand(const Frag &f)
       : v{widen(f.lo[0], f.lo[1]), widen(f.lo[2], f.lo[3]), widen(f.hi[0], f.hi[1]), widen(f.hi[2], f.hi[3])} {}
 };
 // NT products of one block: 16 rows of b each with 16 rows of a
-template <bool EXACT, int NT>
-__device__ __forceinline__ void product(const Operand<EXACT> (&b)[NT], const Operand<EXACT> &a, f32x4 (&p)[NT]) {
+template <int NT>
+__device__ __forceinline__ void product(const Operand (&b)[NT], const Operand &a, f32x4 (&p)[NT]) {
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  if constexpr (EXACT) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].v[q], a.v[q], q ? p[j] : zero, 0, 0, 0);
-  } else {
+  for (int q = 0; q < 4; ++q)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      p[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j].v, a.v, zero, 0, 0, 0, 0, 0, 0);
-  }
+      p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].v[q], a.v[q], q ? p[j] : zero, 0, 0, 0);
 }
 
 }  // namespace
@@ -164,12 +146,12 @@ __global__ __launch_bounds__(KW * 64, KW == 4 && !W_BLOCKS ? 3 : 4) void matmul_
   };
   // adds a block; what comes next is sent for as soon as a fragment is free
   const auto add = [&](const Frag &f, int next) {
-    const Operand<true> ow[1] = {Operand<true>(f)};
+    const Operand ow[1] = {Operand(f)};
     f32x4 p[MT][1];
     float factor[MT][E];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      product<true, 1>(ow, Operand<true>(fs[i]), p[i]);
+      product<1>(ow, Operand(fs[i]), p[i]);
 #pragma unroll
       for (int e = 0; e < E; ++e) factor[i][e] = ss[i] * sw[e];
     }
@@ -243,24 +225,6 @@ static hipError_t few(const MatmulArgs &a, hipStream_t s) {
   return few<MT, 4, SWAP>(a, s);
 }
 
-// The order of a block's instructions: behind each matrix instruction the sums of
-// the row of tiles before, which run while it does.  Left to itself the compiler puts all
-// of a row's products first and its sums behind them, and two waves that begin together
-// then wait for the matrix core together and leave it idle together.
-template <bool B_BLOCKS, int MT, int NT>
-__device__ __forceinline__ void order_block() {
-  constexpr int kMfma = 0x8, kValu = 0x2, kRead = 0x100;
-  __builtin_amdgcn_sched_group_barrier(kRead, 2 * NT + (B_BLOCKS ? 1 : NT) + MT / 2 + 2, 0);
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-      if (j == 0 && i + 1 < MT) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
-      if (i > 0) __builtin_amdgcn_sched_group_barrier(kValu, B_BLOCKS ? 4 : 8, 0);
-    }
-}
-
 // ---- tiles ----
 // A workgroup of WM x WN waves makes a tile of BM x BN results, a wave MT x NT
 // products of 16 x 16.  Both operands' rows of one block (128 bytes each) are in LDS,
@@ -278,7 +242,7 @@ __device__ __forceinline__ void order_block() {
 //
 // The first operand of a matrix instruction is b: then a lane's results are four
 // columns of one row of out, it needs one scale of a, and stores them side by side.
-template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS, bool DIRECT, int KG>
+template <int WM, int WN, int MT, int NT, bool BF16, bool B_BLOCKS, bool DIRECT, int KG>
 __global__ __launch_bounds__(WM *WN *KG * 64, 2) void matmul_f8_tile_kernel(MatmulArgs a, int tiles_m, int tiles_n) {
   constexpr int kWaves = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16, kRows = BM + BN;
   constexpr int kStage = kRows * kScaleBlock;
@@ -412,9 +376,9 @@ __global__ __launch_bounds__(WM *WN *KG * 64, 2) void matmul_f8_tile_kernel(Matm
 #pragma unroll
         for (int e = 0; e < 4; ++e) sb[j][e] = sc[BM + (wn * NT + j) * 16 + g * 4 + e];
     }
-    Operand<EXACT> fb[NT];
+    Operand fb[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) fb[j] = Operand<EXACT>(read(b_lo, b_hi, j));
+    for (int j = 0; j < NT; ++j) fb[j] = Operand(read(b_lo, b_hi, j));
     // Products of one row of tiles run while those of the row before are scaled and
     // added, and the next row's fragment is on its way; no further ahead, for registers.
     float sa[MT];
@@ -428,7 +392,7 @@ __global__ __launch_bounds__(WM *WN *KG * 64, 2) void matmul_f8_tile_kernel(Matm
       if (i + 1 < MT) f[(i + 1) & 1] = read(a_lo, a_hi, i + 1);
       if (i < MT) {
         if (B_BLOCKS) sa[i] *= sb[0][0];
-        product<EXACT, NT>(fb, Operand<EXACT>(f[i & 1]), p[i & 1]);
+        product<NT>(fb, Operand(f[i & 1]), p[i & 1]);
       }
       if (i > 0) {
 #pragma unroll
@@ -439,7 +403,6 @@ __global__ __launch_bounds__(WM *WN *KG * 64, 2) void matmul_f8_tile_kernel(Matm
                                               acc[i - 1][j][e]);
       }
     }
-    if constexpr (!EXACT) order_block<B_BLOCKS, MT, NT>();
   };
 
   // this group's blocks are kg, kg + KG, ..., block kb in stage kb % (2 KG)
@@ -449,8 +412,6 @@ __global__ __launch_bounds__(WM *WN *KG * 64, 2) void matmul_f8_tile_kernel(Matm
     store_stage(kg);
     store_scales(kg);
     if (kg + KG < blocks) load_scales(kg + KG);
-  } else if (!EXACT && KG == 1) {
-    __builtin_amdgcn_s_setprio(1);
   }
   const auto advance = [&](int kb) {
     // this stage and the next scales are here, for all waves; the other stage has been read
@@ -497,7 +458,7 @@ __global__ __launch_bounds__(WM *WN *KG * 64, 2) void matmul_f8_tile_kernel(Matm
       for (int j = 0; j < NT; ++j) acc[i][j] += sums[(i * NT + j) * 64];
   }
 
-  if constexpr (EXACT) {  // fp32
+  if constexpr (!BF16) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       const int64_t m = m0 + (wm * MT + i) * 16 + r16;
@@ -552,33 +513,28 @@ __global__ __launch_bounds__(kThreads) void matmul_f8_empty_kernel(MatmulArgs a)
     a.out_bf16 ? store_f32((uint16_t *)a.out, i, 0.f) : store_f32((float *)a.out, i, 0.f);
 }
 
-template <int WM, int WN, int MT, int NT, bool EXACT, bool B_BLOCKS, bool DIRECT, int KG = 1>
+template <int WM, int WN, int MT, int NT, bool BF16, bool B_BLOCKS, bool DIRECT, int KG = 1>
 static hipError_t tiles(const MatmulArgs &a, hipStream_t s) {
   const int tm = (int)ceil_div(a.m, WM * MT * 16), tn = (int)ceil_div(a.n, WN * NT * 16);
   const dim3 grid((unsigned)(ceil_div((int64_t)tm * tn, 8) * 8));
-  matmul_f8_tile_kernel<WM, WN, MT, NT, EXACT, B_BLOCKS, DIRECT, KG><<<grid, WM * WN * KG * 64, 0, s>>>(a, tm, tn);
+  matmul_f8_tile_kernel<WM, WN, MT, NT, BF16, B_BLOCKS, DIRECT, KG><<<grid, WM * WN * KG * 64, 0, s>>>(a, tm, tn);
   return hipGetLastError();
 }
-template <bool EXACT, bool B_BLOCKS>
+template <bool BF16, bool B_BLOCKS>
 static hipError_t tiles(const MatmulArgs &a, bool direct, hipStream_t s) {
-  // Up to a tile a CU: two groups of waves share k (512 x 4096 x 4096 27 us, 33 with one, to fp32 34 and 40; 1152 x 1152 x
-  // 39,731 222 and 286).  For both ways, whose results are the same.
+  // Up to a tile a CU: two groups of waves share k (512 x 4096 x 4096 34 us, 39 with one; 1152 x 1152 x 39,731 396 and
+  // 436; 256 x 8192 x 1152 13.8 and 14.4).  For both ways, whose results are the same.
   const bool shared = ceil_div(a.m, 128) * ceil_div(a.n, 128) <= 256;
-  // 8192 x 8192 x 8192: 460 us direct and 730 us through registers, fp32 results 913 and 1160
+  // 8192 x 8192 x 8192 to bf16: 953 us direct and 1240 through registers
   if (!direct)
-    return shared ? tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false, 2>(a, s) : tiles<2, 2, 4, 4, EXACT, B_BLOCKS, false>(a, s);
-  if (shared) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, true, 2>(a, s);
-  // 256 x 256 where the registers hold a wave's 128 x 64, that is 8-bit operands and one scale of b a wave; else
-  // 256 x 128.  Large tiles move half or three quarters of the bytes, but go in rounds of 256, which have to be filled
-  // (k = 4096: 128 of 256 x 256 52 us, their 512 parts 44; 144 of them 52 and 66; 272 of them 106 and 104; to fp32, 256
-  // of 256 x 128 70 us and 76, 288 of them 126 and 104, 416 of them 129 and 135, 544 of them 195 and 169).
-  constexpr bool kSquare = !EXACT && B_BLOCKS;
-  const int64_t large = ceil_div(a.m, 256) * ceil_div(a.n, kSquare ? 256 : 128);
-  if (large * 100 < ceil_div(large, 256) * 256 * (kSquare ? 55 : 75)) return tiles<2, 2, 4, 4, EXACT, B_BLOCKS, true>(a, s);
-  if constexpr (kSquare)
-    return tiles<2, 4, 8, 4, EXACT, B_BLOCKS, true>(a, s);
-  else
-    return tiles<4, 2, 4, 4, EXACT, B_BLOCKS, true>(a, s);
+    return shared ? tiles<2, 2, 4, 4, BF16, B_BLOCKS, false, 2>(a, s) : tiles<2, 2, 4, 4, BF16, B_BLOCKS, false>(a, s);
+  if (shared) return tiles<2, 2, 4, 4, BF16, B_BLOCKS, true, 2>(a, s);
+  // 256 x 128 moves three quarters of the bytes of 128 x 128, but goes in rounds of 256, which have to be filled (k =
+  // 4096: 256 of 256 x 128 66 us, their 512 halves 73; 288 of them 109 and 92; 416 112 and 120; 544 169 and 148; 2048
+  // 476 and 505).
+  const int64_t large = ceil_div(a.m, 256) * ceil_div(a.n, 128);
+  if (large * 100 < ceil_div(large, 256) * 256 * 75) return tiles<2, 2, 4, 4, BF16, B_BLOCKS, true>(a, s);
+  return tiles<4, 2, 4, 4, BF16, B_BLOCKS, true>(a, s);
 }
 
 hipError_t launch_matmul_f8(const MatmulArgs &a, hipStream_t s) {
@@ -593,22 +549,22 @@ hipError_t launch_matmul_f8(const MatmulArgs &a, hipStream_t s) {
   };
   const bool direct = even(a.a, a.a_stride, a.k) && even(a.b, a.b_stride, a.k);
   const int64_t few_rows = a.m < a.n ? a.m : a.n, many = a.m < a.n ? a.n : a.m;
-  // Straight from memory where that is less than the tiles' time.  For k = 4096 that is 25 to 29 us for up to 256
-  // tiles (33 for fp32 results) and 80 for 65,536 rows on the other side; up to 16 rows straight take (52 + 2.2
-  // rows) us for 65,536 (one row 57 and 82 us, 9 rows 68 and 81, 12 x 40,000 48 and 46, or 105 to fp32, 16 x 65,536
-  // 82 and 76, 16 x 20,000 28 and 28, 16 x 27,500 37 and 33, 35 to fp32), more rows 33 us for each 16,384 times a pass
-  // of 32 (32 x 13,000 33 and 26, 32 to fp32, 64 x 6144 25 and 26, 96 x 4096 25 and 27, 128 x 4096 32 and 29, 34 to
-  // fp32).  All grow with k.  And few rows at any address (tiles of them go through registers, at half the rate).
+  // Straight from memory where that is less than the tiles' time, which is one for up to 256 tiles: k = 1152 12 to 13 us,
+  // 4096 32, 8192 59 to 62.  More than 16 rows straight take that for about 16,384 rows on the other side times a pass
+  // of 32 (k = 1152 10 us, 4096 31 to 34, 8192 59 to 61, whether 32, 64, 128 or 256 rows; for 24,576 15, 46 to 49, 90),
+  // up to 16 rows for 27,500 (12.3, 39 and 69 us, tiles 13.6, 38 and 68), up to 12 always (k = 4096, 12 x 40,000
+  // 48, tiles 59; one row of 65,536 54).  k = 512 is a launch either way.  And few rows at any address (tiles of
+  // them go through registers).
   const bool straight = few_rows <= 12 ? true
-                        : few_rows <= 16 ? many <= (a.out_bf16 ? 20000 : 27500)
-                                         : many * ceil_div(few_rows, 32) <= (a.out_bf16 ? 12288 : 16384);
+                        : few_rows <= 16 ? many <= 27500
+                                         : many * ceil_div(few_rows, 32) <= 16384;
   if (straight || (few_rows <= 32 && !direct)) {
     if (a.m <= a.n) return a.m <= 16 ? few<1, false>(a, s) : few<2, false>(a, s);
     return a.n <= 16 ? few<1, true>(a, s) : few<2, true>(a, s);
   }
   const bool blocks = a.sb.shift != 0;
-  if (a.out_bf16) return blocks ? tiles<false, true>(a, direct, s) : tiles<false, false>(a, direct, s);
-  return blocks ? tiles<true, true>(a, direct, s) : tiles<true, false>(a, direct, s);
+  if (a.out_bf16) return blocks ? tiles<true, true>(a, direct, s) : tiles<true, false>(a, direct, s);
+  return blocks ? tiles<false, true>(a, direct, s) : tiles<false, false>(a, direct, s);
 }
 
 }  // namespace rvq
