@@ -544,8 +544,8 @@ def rvq_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
         out = torch.empty_like(dy)
     else:
         _need_like("out", out, dy)
-    if (dy.requires_grad or h.requires_grad or weight is not None and weight.requires_grad or
-            dsum is not None and dsum.requires_grad):
+    if (dy.requires_grad or h.requires_grad or rstd.requires_grad or
+            weight is not None and weight.requires_grad or dsum is not None and dsum.requires_grad):
         _refuse_grad()
     dweight, ws, nbytes = None, None, 0
     if need_dweight:
@@ -881,8 +881,8 @@ def rvq_layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, mean: torch.Tenso
         out = torch.empty_like(dy)
     else:
         _need_like("out", out, dy)
-    if (dy.requires_grad or h.requires_grad or weight is not None and weight.requires_grad or
-            dsum is not None and dsum.requires_grad):
+    if (dy.requires_grad or h.requires_grad or mean.requires_grad or rstd.requires_grad or
+            weight is not None and weight.requires_grad or dsum is not None and dsum.requires_grad):
         _refuse_grad()
     dweight = torch.empty(d, dtype=torch.float32, device=dev) if need_dweight else None
     dbias = torch.empty(d, dtype=torch.float32, device=dev) if need_dbias else None
@@ -973,7 +973,7 @@ def rvq_matmul_f8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sca
     (m, k), n = a.shape, b.shape[0]
     if b.shape[1] != k:
         raise ValueError(f"a [{m}, {k}] and b {list(b.shape)} must have rows of the same length")
-    if a_scale.requires_grad or b_scale.requires_grad:
+    if a.requires_grad or a_scale.requires_grad or b.requires_grad or b_scale.requires_grad:
         _refuse_grad()
     ocode = _dtype_code(out_dtype)
     if out is None:
@@ -1070,7 +1070,8 @@ def rvq_token_logprobs_backward(logits: torch.Tensor, ids: Optional[torch.Tensor
         if entropy is None:
             raise ValueError("dentropy needs entropy")
         _need_shape("entropy", entropy, (n,), torch.float32, dev)
-    if dlogprob is not None and dlogprob.requires_grad or dentropy is not None and dentropy.requires_grad:
+    if (stats.requires_grad or dlogprob is not None and dlogprob.requires_grad or
+            dentropy is not None and (dentropy.requires_grad or entropy.requires_grad)):
         _refuse_grad()
     if out is None:
         out = torch.empty_like(logits)
@@ -1137,7 +1138,7 @@ def rvq_distill_loss_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, t
     k = _need_teacher(teacher_ids, teacher, n, dev)
     _need_shape("stats", stats, (n, 4), torch.float32, dev)
     _need_shape("dloss", dloss, (n,), torch.float32, dev)
-    if dloss.requires_grad:
+    if stats.requires_grad or dloss.requires_grad:
         _refuse_grad()
     if out is None:
         out = torch.empty_like(logits)
