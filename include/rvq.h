@@ -607,8 +607,9 @@ rvq_status rvq_token_logprobs_backward(const void *logits, rvq_dtype dtype, int6
  *   tail != 0: q = exp(teacher) (teacher: log probabilities at this temperature, as
  *              rvq_token_logprobs gives them), and all other tokens are one more
  *              outcome: rest = max(0, 1 - sum q), against the sum of their p.
- *              Where no other token has any (the entries name all that are not
- *              masked), a rest of up to 2^-16 is taken as the logarithms' rounding.
+ *              Where the other tokens have no weight (a sum below 2^-149: the entries
+ *              name all that are not masked, by -inf or a large negative value), a
+ *              rest of up to 2^-16 is taken as the logarithms' rounding.
  *
  * logits      : as for rvq_token_logprobs.
  * teacher_ids : device, [n][k] int32.  -1: no entry; any other ID outside [0, V) is

@@ -1113,8 +1113,9 @@ def rvq_distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher: t
     temperature) over its entries (logits, or log probabilities at temperature
     1).  tail true: teacher holds log probabilities at this temperature, as
     rvq_token_logprobs gives them, and all other tokens are one outcome more (where
-    all others are masked, or there are none, up to 2^-16 of weight left for them is
-    taken as rounding; more makes the loss infinite).
+    there are none, or all others are masked, by -inf or a large negative value, up to
+    2^-16 of weight left for them is taken as rounding; more makes the loss infinite, or
+    in proportion to a finite mask).
     No factor temperature^2 is applied."""
     dev, code, n, V = _need_logits(logits)
     k = _need_teacher(teacher_ids, teacher, n, dev)

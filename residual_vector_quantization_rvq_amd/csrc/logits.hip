@@ -851,6 +851,10 @@ constexpr int kSegment = 1 << 18;  // columns that the map holds at once: 32 KB
 // What the teacher's entries may leave where no other token has any weight: fp32 logarithms
 // are off by 2^-24 of themselves, the teacher's own softmax by a few times that.
 constexpr double kNoRest = 0x1p-16;
+// The others have no weight where log p_T is below that of fp32's smallest number, 2^-149: they are
+// masked, by -inf or by a large negative value alike (whose logarithm times a rounding's rest would
+// be the whole loss: 2^-26 times the type's lowest value is 5e30).
+constexpr double kNoWeight = -149 * 0.69314718055994530942;
 
 struct Entry {
   int id;       // -1: does not count
@@ -971,13 +975,16 @@ __global__ __launch_bounds__(256, 4) void distill_kernel(DistillArgs a, int word
       if (TAIL) {
         double rest = 1.0 - sum_q;
         if (rest < 0.0) rest = 0.0;
-        if (others.t == 0.f) {
+        // by the others' own largest value: p_T may be too small for fp32
+        const double down = ((double)others.m - (double)m) * inv_t - log_s;
+        const double log_left = others.t == 0.f ? -INFINITY : down + log((double)others.t);
+        if (rest <= kNoRest && log_left < kNoWeight) {
+          factor = 0.0;
+        } else if (others.t == 0.f) {
           if (rest > kNoRest) loss = INFINITY;
           factor = 0.0;
         } else {
-          // by the others' own largest value: p_T may be too small for fp32
-          const double down = ((double)others.m - (double)m) * inv_t - log_s;
-          if (rest != 0.0) loss += rest * (log(rest) - (down + log((double)others.t)));
+          if (rest != 0.0) loss += rest * (log(rest) - log_left);
           from = others.m;
           factor = exp(down) - rest / (double)others.t;
         }
