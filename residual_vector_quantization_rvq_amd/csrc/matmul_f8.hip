@@ -255,7 +255,7 @@ __global__ __launch_bounds__(WM *WN *KG * 64, 2) void matmul_f8_tile_kernel(Matm
   // each XCD a run of tiles, in groups of eight rows of tiles: those at work at one time share their operands in its L2
   const int tiles = tiles_m * tiles_n, per = (tiles + 7) / 8;
   const int t = (blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (t >= tiles || (int)(blockIdx.x / 8) >= per) return;
+  if (t >= tiles) return;  // the grid is 8 per
   const int group = t / (8 * tiles_n), in_group = t - group * 8 * tiles_n;
   const int rows_here = min(8, tiles_m - group * 8);
   const int64_t m0 = (int64_t)(group * 8 + in_group % rows_here) * BM, n0 = (int64_t)(in_group / rows_here) * BN;
