@@ -12,25 +12,19 @@
 // transposed 98 (5.0); 39,731 x 8192 transposed 191.
 #include "head.h"
 #include "lanes.h"
+#include "rows.h"
 
 namespace rvq {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kB = kScaleBlock;
 
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(fabsf(v)); }
-// NaN where a value of the block is not finite, which its e4m3 bytes cannot say
-__device__ __forceinline__ float scale_of(uint32_t top) {
-  const float t = __uint_as_float(top);
-  return t < INFINITY ? fmaxf(t / 448.f, kScaleMin) : NAN;
-}
 template <int N>
 __device__ __forceinline__ uint32_t top_of(const float (&v)[N]) {
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < N; ++e) top = max(top, magnitude(v[e]));
+  for (int e = 0; e < N; ++e) top = max(top, magnitude_bits(v[e]));
   return top;
 }
 
@@ -53,7 +47,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantArgs a) {
     uint32_t top = top_of<N>(v);
 #pragma unroll
     for (int off = L / 2; off >= 1; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
-    const float scale = scale_of(top), inv = 1.f / scale;
+    const float scale = row_scale_of(top), inv = 1.f / scale;
     if (lane == 0) a.scale[i] = scale;
     if (left <= 0) continue;
 #pragma unroll
@@ -92,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs a) {
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int e = 0; e < N; ++e) top[e] = max(top[e], magnitude(v[i][e]));
+      for (int e = 0; e < N; ++e) top[e] = max(top[e], magnitude_bits(v[i][e]));
     float scale[N], inv[N];
     if constexpr (BLOCK) {
       uint32_t all = top[0];
@@ -106,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs a) {
 #pragma unroll
       for (int w = 0; w < kThreads / 64; ++w) all = max(all, tops[w]);
 #pragma unroll
-      for (int e = 0; e < N; ++e) scale[e] = scale_of(all);
+      for (int e = 0; e < N; ++e) scale[e] = row_scale_of(all);
       if (threadIdx.x == 0) a.scale[TRANS ? tc * tiles_r + tr : t] = scale[0];
     } else {
       // over the groups of this wave, then over the waves
@@ -132,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs a) {
         }
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        scale[e] = scale_of(top[e]);
+        scale[e] = row_scale_of(top[e]);
         if (g == 0 && e < left) a.scale[(c + e) * tiles_r + tr] = scale[e];
       }
     }
@@ -182,14 +176,13 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs a) {
 
 template <typename T>
 static hipError_t quantize(const QuantArgs &a, hipStream_t s) {
-  const int64_t most = 1 << 20;  // workgroups of a launch; what is beyond is looped over
   if (!a.block_rows && !a.transpose) {
     const int64_t groups = ceil_div(a.rows * ceil_div(a.cols, kB), kThreads / (kB / kPiece<T>));
-    quantize_rows_kernel<T><<<dim3((unsigned)(groups < most ? groups : most)), kThreads, 0, s>>>(a);
+    quantize_rows_kernel<T><<<dim3((unsigned)(groups < kMaxGroups ? groups : kMaxGroups)), kThreads, 0, s>>>(a);
     return hipGetLastError();
   }
   const int64_t tiles = ceil_div(a.rows, kB) * ceil_div(a.cols, kB);
-  const dim3 grid((unsigned)(tiles < most ? tiles : most));
+  const dim3 grid((unsigned)(tiles < kMaxGroups ? tiles : kMaxGroups));
   if (a.block_rows && a.transpose)
     quantize_tile_kernel<T, true, true><<<grid, kThreads, 0, s>>>(a);
   else if (a.block_rows)

@@ -1,4 +1,4 @@
-// rows.h -- what the kernels that norm rows share: how a row is spread over
+// rows.h -- what the kernels that norm or quantise rows share: how a row is spread over
 // lanes, sums and largest values over them, the scale of an 8-bit row, and rows
 // whose squares leave fp32.
 #pragma once
@@ -50,7 +50,7 @@ __device__ __forceinline__ float row_scale(uint32_t top) {
   const float t = __uint_as_float(top);
   return t < INFINITY ? fmaxf(t * kF8Unit, kScaleMin) : NAN;
 }
-// the same with the quotient by 448 itself, nearest
+// the same with the quotient by 448 itself, nearest (of a block of 128 or 128 x 128 values, too)
 __device__ __forceinline__ float row_scale_of(uint32_t top) {
   const float t = __uint_as_float(top);
   return t < INFINITY ? fmaxf(t / 448.f, kScaleMin) : NAN;
