@@ -290,7 +290,8 @@ __global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a) {
 }
 
 // Rows too wide for registers: one workgroup per row, which is read again for
-// each pass over it, by elements.
+// each pass over it, by elements.  Bound by these loads: 4000 x 20,000 bf16 300 us (1.1 TB/s of
+// its bytes once), 1000 x 65,536 298, 2000 x 20,000 fp32 174; the gradient 304, 446 and 232.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void layer_norm_wide_kernel(LayerNormArgs a) {
   __shared__ float red[2][2 * kThreads / 64];
@@ -401,8 +402,8 @@ hipError_t launch_layer_norm(const LayerNormArgs &a, bool x_bf16, hipStream_t s)
 // h - m can be beyond fp32 where h and m are not (values of both signs near its largest):
 // where m is large, both are halved and r is doubled, for the cost of an fma in place of a
 // difference and with the same bits.
-// Bound by memory: 39,731 x 4096 bf16 with dsum 232 us (5.6 TB/s) and 6 for
-// the parts; 1024 x 1152 fp32, four rows in turn at most, 7.1 and 4.0.
+// Bound by memory: 39,731 x 4096 bf16 with dsum 236 us (5.6 TB/s) and 6 for the parts; 1024 x
+// 1152 fp32, two rows in turn, 7.2 and 4.4.
 
 namespace {
 
@@ -590,7 +591,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_params_wide_kernel(LayerN
 // Columns' sums over the parts: 64 columns a workgroup, a wave for every 1/16
 // of the parts; columns d .. 2d - 1 are dbias'.  In 64 bits: the parts of few rows are many
 // beside what each of them sums (1024 x 1152 fp32: 512 of two rows, the result's error 4e-8 and
-// 2.3e-7 in 32 bits), and the kernel waits for its loads (4.0 us there in 32 bits, 4.3 in 64).
+// 2.3e-7 in 32 bits), and the kernel waits for its loads (4.0 us there in 32 bits, 4.4 in 64).
 __global__ __launch_bounds__(1024) void layer_norm_params_join_kernel(const float *part, int64_t parts, int d,
                                                                       float *dweight, float *dbias) {
   __shared__ double sums[16][64];

@@ -841,9 +841,9 @@ hipError_t launch_logprobs_grad(const LogprobGradArgs &a, bool x_bf16, hipStream
 // row).  p_T is added up over the others themselves, whose places a map of bits in
 // LDS tells apart, not as 1 - sum p, which would lose a small p_T.
 //
-// Bound by memory where rows are long (4096 x 65,536 bf16 with tail 125 us, 4.3 TB/s,
-// without 108; its gradient 231, 4.7), and by what is done once a row, in 64 bits, where
-// they are short (1,171,875 x 256 with 64 entries 2.1 ms).
+// Bound by memory where rows are long (4096 x 65,536 bf16 with tail 125 to 129 us, 4.2 TB/s,
+// without 108; its gradient 204 behind the loss, 5.4, and 231 where gradients follow one another and
+// wait for each other's writes), and by what is done once a row, in 64 bits, where they are short (1,171,875 x 256 with 64 entries 2.1 ms).
 
 namespace {
 

@@ -17,8 +17,8 @@
 // hold.  8192 x 8192 x 8192 to bf16 953 us (1.15 PFLOP/s; 1056 with a scale for each row of b), to
 // fp32 932; the vendor's library takes 775 for bf16 (1.42), and 403 for 8-bit products with one
 // scale for all.  8192 x 65,536 x 4096 to bf16 3800 (1.16), 8192 x 4096 x 39,731 to fp32
-// 2450 to 2580 (1.03).  The matrix cores are busy for half of the last one's cycles (0.47), and no
-// two lanes meet in a bank of LDS when a fragment is read.
+// 2450 to 2620 (1.02).  The matrix cores are busy for half of these two's cycles (0.54 and 0.48), and
+// no two lanes meet in a bank of LDS when a fragment is read.
 #include <type_traits>
 
 #include "head.h"
